@@ -296,7 +296,7 @@ def _hash(st, nb):
     """32 random-looking bits for each element, from (seed, tensor, place in the tensor)."""
     mask = 0xFFFFFFFF
     e = st["block_in_tensor"] * BLOCK + torch.arange(BLOCK, device="cuda")
-    x = ((e + STEP + st["tensor_of_block"] * 0x3504F333) * 0x9E3779B9) & mask
+    x = ((e + STEP * 0xB7E15163 + st["tensor_of_block"] * 0x3504F333) * 0x9E3779B9) & mask
     x = ((x ^ (x >> 16)) * 0x6A09E667) & mask
     x = ((x ^ (x >> 15)) * 0xBB67AE85) & mask
     return x ^ (x >> 16)
