@@ -52,6 +52,22 @@ class AdamWC(ctypes.Structure):
                 ("weight_decay", ctypes.c_float)]
 
 
+class PoolC(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("r", ctypes.c_int32), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class TensorC(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("grad", ctypes.c_void_p), ("param", ctypes.c_void_p),
+                ("param_bf16", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p), ("lr_scale", ctypes.c_float)]
+
+
+class TensorListC(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_tensors", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("n_chunks", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -65,6 +81,7 @@ def lib():
     L = ctypes.CDLL(LIB_PATH)
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
     pT, pL = ctypes.POINTER(NF4TensorC), ctypes.POINTER(LoraC)
+    pP, pTL = ctypes.POINTER(PoolC), ctypes.POINTER(TensorListC)
     sigs = {
         "qlora_abi_version": (ctypes.c_int, []),
         "qlora_nf4_codebook": (None, [ctypes.POINTER(ctypes.c_float)]),
@@ -85,6 +102,19 @@ def lib():
                                                   sz, vp]),
         "qlora_lora_merge": (ctypes.c_int, [pT, pL, vp, vp]),
         "qlora_adamw_step": (ctypes.c_int, [vp, vp, vp, vp, vp, i64, ctypes.POINTER(AdamWC), i64, vp]),
+        "qlora_adapter_groups": (ctypes.c_int, [vp, i64, i32, vp, vp, vp, vp]),
+        "qlora_workspace_bytes_adapters": (sz, [i64, i64, i64, i32, ctypes.c_int]),
+        "qlora_adapters_fwd": (ctypes.c_int, [pP, vp, vp, vp, i64, i64, i64, i64, vp, i64, ctypes.c_int, vp, vp, sz, vp]),
+        "qlora_adapters_bwd": (ctypes.c_int, [pP, vp, vp, vp, i64, vp, i64, i64, i64, i64, vp, vp, i64, ctypes.c_int, vp,
+                                              vp, ctypes.c_int, vp, sz, vp]),
+        "qlora_linear_fwd_pool": (ctypes.c_int, [pT, pP, vp, vp, vp, i64, vp, ctypes.c_int, vp, vp, sz, vp]),
+        "qlora_linear_bwd_pool": (ctypes.c_int, [pT, pP, vp, vp, vp, vp, i64, vp, vp, ctypes.c_int, vp, vp, ctypes.c_int,
+                                                 vp, sz, vp]),
+        "qlora_tensor_list_bytes": (sz, [ctypes.POINTER(TensorC), i32]),
+        "qlora_tensor_list_init": (ctypes.c_int, [ctypes.POINTER(TensorC), i32, ctypes.c_int, i32, vp, sz, pTL, vp]),
+        "qlora_workspace_bytes_grad_norm": (sz, []),
+        "qlora_grad_norm": (ctypes.c_int, [pTL, ctypes.c_float, vp, vp, sz, vp]),
+        "qlora_adamw_multi": (ctypes.c_int, [pTL, ctypes.POINTER(AdamWC), i64, vp, ctypes.c_uint32, vp]),
         "qlora_selftest_bounded_wait": (ctypes.c_int, [vp, ctypes.c_uint32, vp]),
         "qlora_clear_status": (ctypes.c_int, [vp, vp]),
         "qlora_read_status": (ctypes.c_int, [vp, vp]),
@@ -366,3 +396,268 @@ def linear_bwd_dropout(q: NF4Weight, A, B, alpha: float, X, dY, keep: torch.Tens
                                           _dtype_code(grad_dtype), _ptr(ws), ws.numel(), _stream(stream)),
            "qlora_linear_bwd_dropout")
     return dX, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# Many adapters on one base
+# ---------------------------------------------------------------------------
+def _here(*tensors):
+    """The operands of a call lie on the current device, where its kernels run."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+class AdapterPool:
+    """n adapters side by side: A [n, r, K] and B [n, N, r] bf16, scales [n] float32,
+    and, where ranks differ, ranks [n] int32 (adapter i is the first ranks[i] rows of
+    A[i] and columns of B[i])."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor, ranks: torch.Tensor | None = None):
+        assert A.dtype == torch.bfloat16 and B.dtype == torch.bfloat16 and A.is_contiguous() and B.is_contiguous()
+        assert A.dim() == 3 and B.dim() == 3 and A.shape[0] == B.shape[0] and A.shape[1] == B.shape[2]
+        assert scales.dtype == torch.float32 and scales.is_contiguous() and scales.numel() == A.shape[0]
+        assert scales.device == A.device == B.device
+        if ranks is not None:
+            assert ranks.dtype == torch.int32 and ranks.is_contiguous() and ranks.numel() == A.shape[0]
+            assert ranks.device == A.device
+        self.A, self.B, self.scales, self.ranks = A, B, scales, ranks
+        self.n, self.r = A.shape[0], A.shape[1]
+        self.cols, self.rows = A.shape[2], B.shape[1]  # K, N
+        self._c = PoolC(self.n, self.r, A.data_ptr(), B.data_ptr(), None if ranks is None else ranks.data_ptr(),
+                        scales.data_ptr())
+
+    def c_struct(self) -> PoolC:
+        return self._c
+
+
+def workspace_bytes_adapters(m: int, n: int, k: int, r: int, backward: bool) -> int:
+    return int(lib().qlora_workspace_bytes_adapters(m, n, k, r, 1 if backward else 0))
+
+
+def adapter_groups(adapter_of_token: torch.Tensor, n: int, out=None, ws: torch.Tensor | None = None, stream=None):
+    """(order [M], offsets [n + 1]) int32: the tokens grouped by adapter (-1: none, last)."""
+    idx = adapter_of_token
+    assert idx.dtype == torch.int32 and idx.is_contiguous() and idx.dim() == 1
+    if out is None:
+        buf = torch.empty(idx.numel() + n + 1, dtype=torch.int32, device=idx.device)
+        out = buf[:idx.numel()], buf[idx.numel():]
+    order, offsets = out
+    assert order.dtype == offsets.dtype == torch.int32 and order.is_contiguous() and offsets.is_contiguous()
+    assert order.numel() == idx.numel() and offsets.numel() == n + 1
+    _here(idx, order, offsets, ws)
+    if ws is None:
+        ws = new_workspace(STATUS_BYTES, idx.device)
+    _check(lib().qlora_adapter_groups(_ptr(idx), idx.numel(), n, _ptr(order), _ptr(offsets), _ptr(ws), _stream(stream)),
+           "qlora_adapter_groups")
+    return order, offsets
+
+
+def _group_ptrs(groups, pool: AdapterPool, m: int):
+    order, offsets = groups
+    assert order.dtype == offsets.dtype == torch.int32 and order.is_contiguous() and offsets.is_contiguous()
+    assert order.numel() == m and offsets.numel() == pool.n + 1
+    return _ptr(order), _ptr(offsets)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of a [rows, cols] tensor whose rows are contiguous."""
+    assert t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def adapters_fwd(pool: AdapterPool, groups, X: torch.Tensor, Y: torch.Tensor, save_t: bool = False, t_out=None,
+                 ws: torch.Tensor | None = None, stream=None):
+    """Adds every token's adapter term to Y in place: Y[t] += s_a (X[t] A_a^T) B_a^T.
+    groups: (order, offsets) of adapter_groups.  X and Y may be column slices of wider
+    tensors.  Returns T, the bf16 [3, M, r] planes whose sum is X A^T, or None."""
+    M = X.shape[0]
+    assert X.dtype == torch.bfloat16 and X.shape[1] == pool.cols and tuple(Y.shape) == (M, pool.rows)
+    order, offsets = _group_ptrs(groups, pool, M)
+    T = t_out if t_out is not None else (torch.empty(3, M, pool.r, dtype=torch.bfloat16, device=X.device) if save_t else None)
+    assert T is None or (T.dtype == torch.bfloat16 and T.is_contiguous() and T.numel() == 3 * M * pool.r)
+    _here(X, Y, T, ws, pool.A, *groups)
+    if ws is None:
+        ws = new_workspace(workspace_bytes_adapters(M, pool.rows, pool.cols, pool.r, False), X.device)
+    _check(lib().qlora_adapters_fwd(ctypes.byref(pool.c_struct()), order, offsets, _ptr(X), _row_stride(X), M, pool.rows,
+                                    pool.cols, _ptr(Y), _row_stride(Y), _dtype_code(Y.dtype), _ptr(T), _ptr(ws),
+                                    ws.numel(), _stream(stream)), "qlora_adapters_fwd")
+    return T
+
+
+def _pool_grads(pool: AdapterPool, grad_dtype, outs, device):
+    if outs is None:
+        return (torch.empty(pool.n, pool.r, pool.cols, dtype=grad_dtype, device=device),
+                torch.empty(pool.n, pool.rows, pool.r, dtype=grad_dtype, device=device))
+    dA, dB = outs
+    assert dA.dtype == dB.dtype and dA.is_contiguous() and dB.is_contiguous()
+    assert dA.shape == pool.A.shape and dB.shape == pool.B.shape
+    return dA, dB
+
+
+def adapters_bwd(pool: AdapterPool, groups, X: torch.Tensor, dY: torch.Tensor, T=None, dX: torch.Tensor | None = None,
+                 need_grads: bool = True, grad_dtype=torch.float32, outs=None, ws: torch.Tensor | None = None, stream=None):
+    """Gradients of adapters_fwd.  Adds the adapters' part to dX in place (if given) and
+    returns (dA [n, r, K], dB [n, N, r]), or (None, None) without need_grads."""
+    M = X.shape[0]
+    assert X.dtype == torch.bfloat16 and X.shape[1] == pool.cols
+    assert dY.dtype == torch.bfloat16 and tuple(dY.shape) == (M, pool.rows)
+    assert dX is None or tuple(dX.shape) == (M, pool.cols)
+    assert T is None or (T.dtype == torch.bfloat16 and T.is_contiguous() and T.numel() == 3 * M * pool.r)
+    order, offsets = _group_ptrs(groups, pool, M)
+    dA, dB = _pool_grads(pool, grad_dtype, outs, X.device) if need_grads else (None, None)
+    _here(X, dY, T, dX, dA, dB, ws, pool.A, *groups)
+    if ws is None:
+        ws = new_workspace(workspace_bytes_adapters(M, pool.rows, pool.cols, pool.r, True), X.device)
+    _check(lib().qlora_adapters_bwd(ctypes.byref(pool.c_struct()), order, offsets, _ptr(X), _row_stride(X), _ptr(dY),
+                                    _row_stride(dY), M, pool.rows, pool.cols, _ptr(T), _ptr(dX),
+                                    0 if dX is None else _row_stride(dX), QLORA_F32 if dX is None else _dtype_code(dX.dtype),
+                                    _ptr(dA), _ptr(dB), QLORA_F32 if dA is None else _dtype_code(dA.dtype), _ptr(ws),
+                                    ws.numel(), _stream(stream)), "qlora_adapters_bwd")
+    return dA, dB
+
+
+def linear_fwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, y_dtype=torch.bfloat16, save_t: bool = True,
+                    ws: torch.Tensor | None = None, out: torch.Tensor | None = None, t_out=None, stream=None):
+    """Forward of the NF4 layer with every token's own adapter.  Returns (Y, T or None)."""
+    M = X.shape[0]
+    assert X.dtype == torch.bfloat16 and X.is_contiguous() and X.shape[1] == q.cols == pool.cols and pool.rows == q.rows
+    Y = out if out is not None else torch.empty(M, q.rows, dtype=y_dtype, device=X.device)
+    assert Y.is_contiguous() and tuple(Y.shape) == (M, q.rows)
+    T = t_out if t_out is not None else (torch.empty(3, M, pool.r, dtype=torch.bfloat16, device=X.device) if save_t else None)
+    order, offsets = _group_ptrs(groups, pool, M)
+    _here(X, Y, T, ws, pool.A, q.codes, *groups)
+    if ws is None:
+        ws = new_workspace(workspace_bytes_adapters(M, q.rows, q.cols, pool.r, False), X.device)
+    t = q.c_struct()
+    _check(lib().qlora_linear_fwd_pool(ctypes.byref(t), ctypes.byref(pool.c_struct()), order, offsets, _ptr(X), M, _ptr(Y),
+                                       _dtype_code(Y.dtype), _ptr(T), _ptr(ws), ws.numel(), _stream(stream)),
+           "qlora_linear_fwd_pool")
+    return Y, T
+
+
+def linear_bwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, dY, T=None, dx_dtype=torch.bfloat16,
+                    grad_dtype=torch.bfloat16, ws: torch.Tensor | None = None, outs=None, stream=None):
+    """Returns (dX, dA [n, r, K], dB [n, N, r]) for upstream gradient dY."""
+    M = X.shape[0]
+    assert X.dtype == torch.bfloat16 and X.is_contiguous() and X.shape[1] == q.cols == pool.cols and pool.rows == q.rows
+    assert dY.dtype == torch.bfloat16 and dY.is_contiguous() and tuple(dY.shape) == (M, q.rows)
+    dX = outs[0] if outs is not None else torch.empty(M, q.cols, dtype=dx_dtype, device=X.device)
+    assert dX.is_contiguous() and tuple(dX.shape) == (M, q.cols)
+    dA, dB = _pool_grads(pool, grad_dtype, None if outs is None else outs[1:], X.device)
+    order, offsets = _group_ptrs(groups, pool, M)
+    _here(X, dY, T, dX, dA, dB, ws, pool.A, q.codes, *groups)
+    if ws is None:
+        ws = new_workspace(workspace_bytes_adapters(M, q.rows, q.cols, pool.r, True), X.device)
+    t = q.c_struct()
+    _check(lib().qlora_linear_bwd_pool(ctypes.byref(t), ctypes.byref(pool.c_struct()), order, offsets, _ptr(X), _ptr(dY), M,
+                                       _ptr(T), _ptr(dX), _dtype_code(dX.dtype), _ptr(dA), _ptr(dB), _dtype_code(dA.dtype),
+                                       _ptr(ws), ws.numel(), _stream(stream)), "qlora_linear_bwd_pool")
+    return dX, dA, dB
+
+
+class QLoRAPoolLinearFunction(torch.autograd.Function):
+    """Autograd wrapper of the NF4 layer with a pool: X, A [n, r, K] and B [n, N, r] get
+    gradients; groups, scales and ranks are the batch's and the pool's constants."""
+
+    @staticmethod
+    def forward(ctx, X, A, B, q: NF4Weight, groups, scales, ranks=None):
+        X = X.contiguous()
+        Y, T = linear_fwd_pool(q, AdapterPool(A, B, scales, ranks), groups, X)
+        ctx.save_for_backward(X, A, B, T, scales, *groups, *([] if ranks is None else [ranks]))
+        ctx.q = q
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, A, B, T, scales, order, offsets, *ranks = ctx.saved_tensors
+        pool = AdapterPool(A, B, scales, ranks[0] if ranks else None)
+        dX, dA, dB = linear_bwd_pool(ctx.q, pool, (order, offsets), X, dY.contiguous().to(torch.bfloat16), T)
+        return dX, dA, dB, None, None, None, None
+
+
+# ---------------------------------------------------------------------------
+# One optimiser step over a list of tensors
+# ---------------------------------------------------------------------------
+class TensorList:
+    """The tensors of one optimiser step and its device table.  grads alone serve
+    grad_norm; adamw_multi also needs params (float32) and the states: float32, or
+    8-bit codes (uint8, or float8_e4m3fn for exp_avg and float8_e5m2 for exp_avg_sq)
+    with a float32 scale per 256 elements.  The list keeps its tensors alive; they must
+    not move (a gradient that is allocated anew needs a new list)."""
+
+    def __init__(self, grads, params=None, exp_avg=None, exp_avg_sq=None, p_bf16=None, exp_avg_scale=None,
+                 exp_avg_sq_scale=None, lr_scale=None, stream=None):
+        grads = list(grads)
+        count = len(grads)
+        assert count > 0
+        gdt = grads[0].dtype
+        bits = 0 if params is None else (32 if exp_avg[0].dtype == torch.float32 else 8)
+        columns = [grads, params, p_bf16, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale]
+        columns = [None if c is None else list(c) for c in columns]
+        for c in columns:
+            assert c is None or len(c) == count
+        grads, params, p_bf16, exp_avg, exp_avg_sq, ms, vs = columns
+        code_m, code_v = (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e5m2)
+        for i, g in enumerate(grads):
+            assert g.dtype == gdt and g.is_contiguous()
+            if bits:
+                n, nb = g.numel(), -(-g.numel() // 256)
+                kinds = [(params, (torch.float32,), n), (p_bf16, (torch.bfloat16,), n),
+                         (exp_avg, (torch.float32,) if bits == 32 else code_m, n),
+                         (exp_avg_sq, (torch.float32,) if bits == 32 else code_v, n)]
+                if bits == 8:
+                    kinds += [(ms, (torch.float32,), nb), (vs, (torch.float32,), nb)]
+                for col, types, size in kinds:
+                    if col is None and col is p_bf16:
+                        continue
+                    t = col[i]
+                    assert t.dtype in types and t.is_contiguous() and t.numel() == size and t.device == g.device
+        _here(*(t for c in columns if c is not None for t in c))
+        arr = (TensorC * count)()
+        for i in range(count):
+            p = [0 if c is None else c[i].data_ptr() for c in (grads, params, p_bf16, exp_avg, exp_avg_sq, ms, vs)]
+            arr[i] = TensorC(grads[i].numel(), *p, 1.0 if lr_scale is None else float(lr_scale[i]))
+        nbytes = int(lib().qlora_tensor_list_bytes(arr, count))
+        if nbytes == 0:
+            raise QLoRAError(2, "qlora_tensor_list_bytes")
+        self.table = torch.empty(nbytes, dtype=torch.uint8, device=grads[0].device)
+        self._c = TensorListC()
+        _check(lib().qlora_tensor_list_init(arr, count, _dtype_code(gdt), bits, _ptr(self.table), nbytes,
+                                            ctypes.byref(self._c), _stream(stream)), "qlora_tensor_list_init")
+        self._keep = columns
+        self.state_bits = bits
+
+    def c_struct(self) -> TensorListC:
+        return self._c
+
+
+def workspace_bytes_grad_norm() -> int:
+    return int(lib().qlora_workspace_bytes_grad_norm())
+
+
+def grad_norm(tensors: TensorList, max_norm: float, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """float32 [2] on the device: the norm of all gradients and min(1, max_norm / (norm + 1e-6))."""
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=tensors.table.device)
+    assert out.dtype == torch.float32 and out.is_contiguous() and out.numel() == 2
+    _here(tensors.table, out, ws)
+    if ws is None:
+        ws = new_workspace(workspace_bytes_grad_norm(), tensors.table.device)
+    _check(lib().qlora_grad_norm(ctypes.byref(tensors.c_struct()), float(max_norm), _ptr(out), _ptr(ws), ws.numel(),
+                                 _stream(stream)), "qlora_grad_norm")
+    return out
+
+
+def adamw_multi(tensors: TensorList, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                weight_decay: float = 0.0, clip: torch.Tensor | None = None, seed: int = 0, stream=None) -> None:
+    """One AdamW step in place on every tensor of the list.  clip: what grad_norm returned
+    (gradients are multiplied by clip[1]; NaN there leaves everything as it is).  seed:
+    random bits of the 8-bit states' rounding, another one for each step."""
+    assert clip is None or (clip.dtype == torch.float32 and clip.is_contiguous() and clip.numel() == 2)
+    _here(tensors.table, clip)
+    hp = AdamWC(lr, beta1, beta2, eps, weight_decay)
+    _check(lib().qlora_adamw_multi(ctypes.byref(tensors.c_struct()), ctypes.byref(hp), step, _ptr(clip), seed & 0xffffffff,
+                                   _stream(stream)), "qlora_adamw_multi")

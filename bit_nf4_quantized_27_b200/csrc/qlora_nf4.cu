@@ -14,6 +14,8 @@
 #include "decode_kernel.cuh"
 #include "gemv_kernel.cuh"
 #include "host_common.h"
+#include "optimizer_kernels.cuh"
+#include "pool_kernels.cuh"
 #include "qlora_nf4.h"
 #include "quant_kernels.cuh"
 #include "selftest_kernel.cuh"
@@ -901,6 +903,452 @@ qlora_status qlora_adamw_step(float *param, void *param_bf16, const float *grad,
   const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)sms * 8)));
   adamw_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       param, static_cast<__nv_bfloat16 *>(param_bf16), grad, exp_avg, exp_avg_sq, n, c);
+  return launch_status();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Many adapters on one base
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int64_t kPoolMaxTokens = int64_t(1) << 30;
+
+qlora_status check_pool(const qlora_adapter_pool *p) {
+  if (!p || !p->A || !p->B || !p->scales) return QLORA_ERR_INVALID_ARGUMENT;
+  if (p->n < 1 || p->n > QLORA_MAX_ADAPTERS || p->r < 8 || p->r > QLORA_MAX_RANK || p->r % 8)
+    return QLORA_ERR_INVALID_ARGUMENT;
+  if (!aligned(p->A, 16) || !aligned(p->B, 16) || !aligned(p->scales, 4) || (p->ranks && !aligned(p->ranks, 4)))
+    return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
+
+// Checks that both directions share; M = 0 needs no token pointers.
+qlora_status check_pool_call(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets,
+                             const void *X, int64_t ldx, int64_t M, int64_t N, int64_t K, const void *ws) {
+  const qlora_status s = check_pool(pool);
+  if (s != QLORA_OK) return s;
+  if (M < 0 || M > kPoolMaxTokens || !offsets || !ws || (M > 0 && (!order || !X))) return QLORA_ERR_INVALID_ARGUMENT;
+  if (N <= 0 || K <= 0 || N % 8 || K % 8 || N > (int64_t(1) << 30) || K > (int64_t(1) << 30) || ldx < K || ldx % 8)
+    return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(order, 4) || !aligned(offsets, 4) || !aligned(X, 16) || !aligned(ws, 256)) return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
+
+size_t pool_ws_bytes(int64_t M, int32_t r, int for_backward) {
+  return QLORA_STATUS_BYTES + (for_backward ? 2 : 1) * align256(static_cast<size_t>(kPoolPlanes) * M * r * 2);
+}
+
+PoolArgs pool_args(const qlora_adapter_pool *p, const int32_t *order, const int32_t *offsets, int64_t M, int64_t N,
+                   int64_t K, void *ws) {
+  PoolArgs a{};
+  a.A = static_cast<const __nv_bfloat16 *>(p->A);
+  a.B = static_cast<const __nv_bfloat16 *>(p->B);
+  a.ranks = p->ranks;
+  a.scales = p->scales;
+  a.n = p->n;
+  a.r = p->r;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.order = order;
+  a.offsets = offsets;
+  a.status = status_ptr(ws);
+  return a;
+}
+
+unsigned pool_grid(int64_t threads, int sms) {
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((threads + 255) / 256, static_cast<int64_t>(sms) * 16)));
+}
+
+// P = V W_a for every grouped token, as three planes.
+qlora_status launch_pool_down(const PoolArgs &a, const void *V, int64_t ldv, int64_t len, bool transposed,
+                              __nv_bfloat16 *P, int sms, cudaStream_t st) {
+  pool_down_kernel<<<pool_grid(a.M * a.r * 32, sms), 256, 0, st>>>(a, static_cast<const __nv_bfloat16 *>(V), ldv, len,
+                                                                  transposed, P);
+  return launch_status();
+}
+
+// Out[t] += s_a P[t] W_a for every grouped token.
+qlora_status launch_pool_up(const PoolArgs &a, const __nv_bfloat16 *P, bool transposed, int64_t cols, void *Out,
+                            int64_t ldo, qlora_dtype dt, int sms, cudaStream_t st) {
+  const unsigned grid = pool_grid(a.M * cols, sms);
+  if (dt == QLORA_F32)
+    pool_up_kernel<float><<<grid, 256, 0, st>>>(a, P, transposed, cols, static_cast<float *>(Out), ldo);
+  else
+    pool_up_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a, P, transposed, cols, static_cast<__nv_bfloat16 *>(Out), ldo);
+  return launch_status();
+}
+
+template <typename O>
+qlora_status launch_pool_grads(const PoolArgs &a, const __nv_bfloat16 *U, const void *X, int64_t ldx,
+                               const __nv_bfloat16 *T, const void *dY, int64_t lddy, void *dA, void *dB, int sms, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.n) * a.r;
+  pool_grad_kernel<O><<<pool_grid(rows * a.K, sms), 256, 0, st>>>(a, U, static_cast<const __nv_bfloat16 *>(X), ldx,
+                                                                  a.K, false, static_cast<O *>(dA));
+  pool_grad_kernel<O><<<pool_grid(rows * a.N, sms), 256, 0, st>>>(a, T, static_cast<const __nv_bfloat16 *>(dY), lddy,
+                                                                  a.N, true, static_cast<O *>(dB));
+  return launch_status();
+}
+
+qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
+                      int64_t ldx, int64_t M, int64_t N, int64_t K, void *Y, int64_t ldy, qlora_dtype y_dtype,
+                      void *T_save, void *ws, int sms, cudaStream_t st) {
+  if (M == 0) return QLORA_OK;
+  const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
+  __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
+  const qlora_status s = launch_pool_down(a, X, ldx, K, false, T, sms, st);
+  return s != QLORA_OK ? s : launch_pool_up(a, T, true, N, Y, ldy, y_dtype, sms, st);
+}
+
+qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
+                      int64_t ldx, const void *dY, int64_t lddy, int64_t M, int64_t N, int64_t K, const void *T_saved,
+                      void *dX, int64_t lddx, qlora_dtype dx_dtype, void *dA, void *dB, qlora_dtype grad_dtype, void *ws,
+                      int sms, cudaStream_t st) {
+  const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
+  __nv_bfloat16 *U = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
+  const __nv_bfloat16 *T = static_cast<const __nv_bfloat16 *>(T_saved);
+  qlora_status s;
+  if (M > 0) {
+    if ((s = launch_pool_down(a, dY, lddy, N, true, U, sms, st)) != QLORA_OK) return s;
+    if (dX && (s = launch_pool_up(a, U, false, K, dX, lddx, dx_dtype, sms, st)) != QLORA_OK) return s;
+    if (dA && !T) {
+      __nv_bfloat16 *Tw = U + align256(static_cast<size_t>(kPoolPlanes) * M * a.r * 2) / 2;
+      if ((s = launch_pool_down(a, X, ldx, K, false, Tw, sms, st)) != QLORA_OK) return s;
+      T = Tw;
+    }
+  }
+  if (!dA) return QLORA_OK;
+  return grad_dtype == QLORA_F32 ? launch_pool_grads<float>(a, U, X, ldx, T, dY, lddy, dA, dB, sms, st)
+                                 : launch_pool_grads<__nv_bfloat16>(a, U, X, ldx, T, dY, lddy, dA, dB, sms, st);
+}
+
+// The base products alone: Y = X W'^T, and dX = dY W'.
+qlora_status base_fwd(const qlora_nf4_tensor *W, const void *X, int64_t M, void *Y, qlora_dtype y_dtype, void *ws,
+                      int dev, int sms, cudaStream_t st) {
+  const int64_t N = W->rows, K = W->cols;
+  CUtensorMap tmc;
+  if (M <= kGemvMaxM && gemv_bulk_ok(N, K) && aligned(W->scale_codes, 16) &&
+      tmap_codes_gemv(&tmc, W->codes, N, K, static_cast<uint32_t>((K < 4096 ? K : 4096) / 256))) {
+    GemvArgs g{};
+    g.codes = W->codes; g.scale_codes = W->scale_codes; g.c2 = W->c2; g.scale_format = W->scale_format;
+    g.N = N; g.K = K; g.M = static_cast<int>(M);
+    g.X = static_cast<const __nv_bfloat16 *>(X);
+    g.Y = Y;
+    g.y_f32 = y_dtype == QLORA_F32;
+    g.status = status_ptr(ws);
+    g.multi = 2;  // no adapter term
+    const qlora_status s = launch_gemv(g, &tmc, dev, sms, st);
+    if (s != QLORA_ERR_UNSUPPORTED_SHAPE) return s;
+  }
+  CUtensorMap tmX, tmCodes, tmCodesPair;
+  if (!tmap_bf16(&tmX, X, K, M, 64, 128) ||
+      !make_tmap(&tmCodes, W->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K / 2, N, K / 2, 32, 256, false) ||
+      !make_tmap(&tmCodesPair, W->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K / 2, N, K / 2, 32, 128, false))
+    return QLORA_ERR_CUDA;
+  GemmArgs g{};
+  g.M_rows = static_cast<int>(M);
+  g.N_cols = static_cast<int>(N);
+  g.k_steps = static_cast<int>(K / 64);
+  g.out = Y;
+  g.ldo = N;
+  g.out_f32 = y_dtype == QLORA_F32;
+  g.out_scale = 1.0f;
+  g.scale_codes = W->scale_codes;
+  g.c2 = W->c2;
+  g.scale_format = W->scale_format;
+  g.w_rows = N;
+  g.w_cols = K;
+  g.status = status_ptr(ws);
+  if (M >= kPairMinRows) {
+    const qlora_status s = launch_gemm_pair<false, kFusedMT>(tmX, tmX, tmCodesPair, g, dev, st);
+    if (s != QLORA_ERR_UNSUPPORTED_SHAPE) return s;
+  }
+  return launch_gemm<false, false, true, 256, kFusedMT>(tmX, tmX, tmX, tmX, tmCodes, g, dev, sms, st);
+}
+
+qlora_status base_bwd(const qlora_nf4_tensor *W, const void *dY, int64_t M, void *dX, qlora_dtype dx_dtype, void *ws,
+                      int dev, int sms, cudaStream_t st) {
+  const int64_t N = W->rows, K = W->cols;
+  CUtensorMap tmDY, tmCodes, tmCodesPair;
+  if (!tmap_bf16(&tmDY, dY, N, M, 64, 128) ||
+      !make_tmap(&tmCodes, W->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K / 2, N, K / 2, 128, 64, false) ||
+      !make_tmap(&tmCodesPair, W->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K / 2, N, K / 2, 64, 64, false))
+    return QLORA_ERR_CUDA;
+  GemmArgs g{};
+  g.M_rows = static_cast<int>(M);
+  g.N_cols = static_cast<int>(K);
+  g.k_steps = static_cast<int>((N + 63) / 64);
+  g.out = dX;
+  g.ldo = K;
+  g.out_f32 = dx_dtype == QLORA_F32;
+  g.out_scale = 1.0f;
+  g.scale_codes = W->scale_codes;
+  g.c2 = W->c2;
+  g.scale_format = W->scale_format;
+  g.w_rows = N;
+  g.w_cols = K;
+  g.status = status_ptr(ws);
+  if (M >= kPairMinRows) {
+    const qlora_status s = launch_gemm_pair<true, kFusedMT>(tmDY, tmDY, tmCodesPair, g, dev, st);
+    if (s != QLORA_ERR_UNSUPPORTED_SHAPE) return s;
+  }
+  return launch_gemm<false, true, true, 256, kFusedMT>(tmDY, tmDY, tmDY, tmDY, tmCodes, g, dev, sms, st);
+}
+
+qlora_status check_out(const void *p, int64_t ld, int64_t cols, qlora_dtype dt) {
+  if (!valid_dtype(dt)) return QLORA_ERR_INVALID_ARGUMENT;
+  if (ld < cols) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  return aligned(p, dt == QLORA_F32 ? 4 : 2) ? QLORA_OK : QLORA_ERR_MISALIGNED;
+}
+}  // namespace
+
+extern "C" {
+
+size_t qlora_workspace_bytes_adapters(int64_t M, int64_t N, int64_t K, int32_t r, int for_backward) {
+  if (M < 0 || M > kPoolMaxTokens || N <= 0 || K <= 0 || r < 8 || r > QLORA_MAX_RANK || r % 8) return 0;
+  return pool_ws_bytes(M, r, for_backward);
+}
+
+qlora_status qlora_adapter_groups(const int32_t *adapter_of_token, int64_t M, int32_t n, int32_t *order,
+                                  int32_t *offsets, void *ws, qlora_stream_t stream) {
+  if (M < 0 || M > kPoolMaxTokens || n < 1 || n > QLORA_MAX_ADAPTERS || !offsets || !ws ||
+      (M > 0 && (!adapter_of_token || !order)))
+    return QLORA_ERR_INVALID_ARGUMENT;
+  if (!aligned(adapter_of_token, 4) || !aligned(order, 4) || !aligned(offsets, 4) || !aligned(ws, 256))
+    return QLORA_ERR_MISALIGNED;
+  int dev, sms;
+  qlora_status s;
+  if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
+  static std::once_flag flags[64];
+  static qlora_status results[64];
+  const int smem = (kGroupThreads / 32) * (QLORA_MAX_ADAPTERS + 1) * 4;
+  if ((s = set_smem(adapter_groups_kernel, smem, dev, flags, results)) != QLORA_OK) return s;
+  adapter_groups_kernel<<<1, kGroupThreads, (kGroupThreads / 32) * (n + 1) * 4, reinterpret_cast<cudaStream_t>(stream)>>>(
+      adapter_of_token, M, n, order, offsets, status_ptr(ws));
+  return launch_status();
+}
+
+qlora_status qlora_adapters_fwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets,
+                                const void *X, int64_t ldx, int64_t M, int64_t N, int64_t K, void *Y, int64_t ldy,
+                                qlora_dtype y_dtype, void *T_save, void *ws, size_t ws_bytes, qlora_stream_t stream) {
+  qlora_status s;
+  if ((s = check_pool_call(pool, order, offsets, X, ldx, M, N, K, ws)) != QLORA_OK) return s;
+  if (M > 0 && !Y) return QLORA_ERR_INVALID_ARGUMENT;
+  if ((s = check_out(Y, ldy, N, y_dtype)) != QLORA_OK) return s;
+  if (!aligned(T_save, 16)) return QLORA_ERR_MISALIGNED;
+  if (ws_bytes < pool_ws_bytes(M, pool->r, 0)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  int dev, sms;
+  if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
+  return pool_fwd(pool, order, offsets, X, ldx, M, N, K, Y, ldy, y_dtype, T_save, ws, sms,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_adapters_bwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets,
+                                const void *X, int64_t ldx, const void *dY, int64_t lddy, int64_t M, int64_t N,
+                                int64_t K, const void *T_saved, void *dX, int64_t lddx, qlora_dtype dx_dtype, void *dA,
+                                void *dB, qlora_dtype grad_dtype, void *ws, size_t ws_bytes, qlora_stream_t stream) {
+  qlora_status s;
+  if ((s = check_pool_call(pool, order, offsets, X, ldx, M, N, K, ws)) != QLORA_OK) return s;
+  if ((M > 0 && !dY) || (!dA) != (!dB) || !valid_dtype(grad_dtype)) return QLORA_ERR_INVALID_ARGUMENT;
+  if (lddy < N || lddy % 8) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (dX && (s = check_out(dX, lddx, K, dx_dtype)) != QLORA_OK) return s;
+  if (!aligned(dY, 16) || !aligned(T_saved, 16) || !aligned(dA, 16) || !aligned(dB, 16)) return QLORA_ERR_MISALIGNED;
+  if (ws_bytes < pool_ws_bytes(M, pool->r, 1)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  int dev, sms;
+  if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
+  return pool_bwd(pool, order, offsets, X, ldx, dY, lddy, M, N, K, T_saved, dX, lddx, dx_dtype, dA, dB, grad_dtype, ws,
+                  sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_linear_fwd_pool(const qlora_nf4_tensor *W, const qlora_adapter_pool *pool, const int32_t *order,
+                                   const int32_t *offsets, const void *X, int64_t M, void *Y, qlora_dtype y_dtype,
+                                   void *T_save, void *ws, size_t ws_bytes, qlora_stream_t stream) {
+  qlora_status s = check_nf4(W);
+  if (s != QLORA_OK) return s;
+  const int64_t N = W->rows, K = W->cols;
+  if (M < 1 || !Y || !valid_dtype(y_dtype)) return QLORA_ERR_INVALID_ARGUMENT;
+  if ((s = check_pool_call(pool, order, offsets, X, K, M, N, K, ws)) != QLORA_OK) return s;
+  if (!aligned(Y, 16) || !aligned(T_save, 16)) return QLORA_ERR_MISALIGNED;
+  if (ws_bytes < pool_ws_bytes(M, pool->r, 0)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  int dev, sms;
+  if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((s = base_fwd(W, X, M, Y, y_dtype, ws, dev, sms, st)) != QLORA_OK) return s;
+  return pool_fwd(pool, order, offsets, X, K, M, N, K, Y, N, y_dtype, T_save, ws, sms, st);
+}
+
+qlora_status qlora_linear_bwd_pool(const qlora_nf4_tensor *W, const qlora_adapter_pool *pool, const int32_t *order,
+                                   const int32_t *offsets, const void *X, const void *dY, int64_t M,
+                                   const void *T_saved, void *dX, qlora_dtype dx_dtype, void *dA, void *dB,
+                                   qlora_dtype grad_dtype, void *ws, size_t ws_bytes, qlora_stream_t stream) {
+  qlora_status s = check_nf4(W);
+  if (s != QLORA_OK) return s;
+  const int64_t N = W->rows, K = W->cols;
+  if (M < 1 || !dY || !dX || !dA || !dB || !valid_dtype(dx_dtype) || !valid_dtype(grad_dtype))
+    return QLORA_ERR_INVALID_ARGUMENT;
+  if ((s = check_pool_call(pool, order, offsets, X, K, M, N, K, ws)) != QLORA_OK) return s;
+  if (!aligned(dY, 16) || !aligned(dX, 16) || !aligned(T_saved, 16) || !aligned(dA, 16) || !aligned(dB, 16))
+    return QLORA_ERR_MISALIGNED;
+  if (ws_bytes < pool_ws_bytes(M, pool->r, 1)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  int dev, sms;
+  if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((s = base_bwd(W, dY, M, dX, dx_dtype, ws, dev, sms, st)) != QLORA_OK) return s;
+  return pool_bwd(pool, order, offsets, X, K, dY, N, M, N, K, T_saved, dX, K, dx_dtype, dA, dB, grad_dtype, ws, sms, st);
+}
+
+// ---------------------------------------------------------------------------
+// One optimiser step over a list of tensors
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+int64_t chunks_of(int64_t n) { return (n + kOptChunk - 1) / kOptChunk; }
+
+// Chunks of a list; -1 if a size is negative or the list is too long.
+int64_t list_chunks(const qlora_tensor *t, int32_t n) {
+  int64_t c = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (t[i].n < 0 || t[i].n > (int64_t(1) << 42)) return -1;
+    c += chunks_of(t[i].n);
+    if (c >= (int64_t(1) << 31)) return -1;
+  }
+  return c;
+}
+
+size_t list_chunks_offset(int32_t n) { return align256(static_cast<size_t>(n) * sizeof(qlora_tensor)); }
+
+qlora_status check_list(const qlora_tensor_list *l) {
+  if (!l || !l->table || l->n_tensors < 1 || l->n_chunks < 0) return QLORA_ERR_INVALID_ARGUMENT;
+  if (l->grad_dtype != QLORA_F32 && l->grad_dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARGUMENT;
+  return aligned(l->table, 16) ? QLORA_OK : QLORA_ERR_MISALIGNED;
+}
+
+TensorTable table_of(const qlora_tensor_list *l) {
+  TensorTable t;
+  t.tensors = static_cast<const qlora_tensor *>(l->table);
+  t.chunks = reinterpret_cast<const int2 *>(static_cast<const uint8_t *>(l->table) + list_chunks_offset(l->n_tensors));
+  t.n_chunks = l->n_chunks;
+  return t;
+}
+}  // namespace
+
+extern "C" {
+
+size_t qlora_tensor_list_bytes(const qlora_tensor *tensors, int32_t n_tensors) {
+  if (!tensors || n_tensors < 1) return 0;
+  const int64_t c = list_chunks(tensors, n_tensors);
+  return c < 0 ? 0 : list_chunks_offset(n_tensors) + static_cast<size_t>(std::max<int64_t>(c, 1)) * sizeof(int2);
+}
+
+qlora_status qlora_tensor_list_init(const qlora_tensor *tensors, int32_t n_tensors, qlora_dtype grad_dtype,
+                                    int32_t state_bits, void *table, size_t table_bytes, qlora_tensor_list *out,
+                                    qlora_stream_t stream) {
+  if (!tensors || n_tensors < 1 || !table || !out || !valid_dtype(grad_dtype)) return QLORA_ERR_INVALID_ARGUMENT;
+  if (state_bits != 0 && state_bits != 8 && state_bits != 32) return QLORA_ERR_INVALID_ARGUMENT;
+  const size_t need = qlora_tensor_list_bytes(tensors, n_tensors);
+  if (need == 0) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(table, 16)) return QLORA_ERR_MISALIGNED;
+  if (table_bytes < need) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const qlora_tensor &t = tensors[i];
+    if (t.n == 0) continue;
+    if (!t.grad) return QLORA_ERR_INVALID_ARGUMENT;
+    if (!aligned(t.grad, grad_dtype == QLORA_F32 ? 4 : 2)) return QLORA_ERR_MISALIGNED;
+    if (state_bits == 0) continue;
+    if (!t.param || !t.exp_avg || !t.exp_avg_sq || !std::isfinite(t.lr_scale) || t.lr_scale < 0.0f)
+      return QLORA_ERR_INVALID_ARGUMENT;
+    if (state_bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return QLORA_ERR_INVALID_ARGUMENT;
+    const uintptr_t sa = state_bits == 8 ? 1 : 4;
+    if (!aligned(t.param, 4) || !aligned(t.param_bf16, 2) || !aligned(t.exp_avg, sa) || !aligned(t.exp_avg_sq, sa) ||
+        (state_bits == 8 && (!aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4))))
+      return QLORA_ERR_MISALIGNED;
+  }
+  qlora_status s;
+  if ((s = check_device(nullptr, nullptr)) != QLORA_OK) return s;
+  TableWrite w;
+  w.tensors = static_cast<qlora_tensor *>(table);
+  w.chunks = reinterpret_cast<int2 *>(static_cast<uint8_t *>(table) + list_chunks_offset(n_tensors));
+  int64_t c = 0;
+  for (int32_t i0 = 0; i0 < n_tensors; i0 += kTablePerLaunch) {
+    const int m = std::min(kTablePerLaunch, n_tensors - i0);
+    w.base = i0;
+    for (int i = 0; i < m; ++i) {
+      w.t[i] = tensors[i0 + i];
+      w.first_chunk[i] = c;
+      c += chunks_of(w.t[i].n);
+    }
+    w.first_chunk[m] = c;
+    tensor_table_kernel<<<m, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(w);
+    if ((s = launch_status()) != QLORA_OK) return s;
+  }
+  out->table = table;
+  out->n_tensors = n_tensors;
+  out->state_bits = state_bits;
+  out->grad_dtype = grad_dtype;
+  out->n_chunks = c;
+  return QLORA_OK;
+}
+
+size_t qlora_workspace_bytes_grad_norm(void) { return QLORA_STATUS_BYTES + kNormMaxCtas * sizeof(double); }
+
+qlora_status qlora_grad_norm(const qlora_tensor_list *list, float max_norm, float *norm_and_clip, void *ws,
+                             size_t ws_bytes, qlora_stream_t stream) {
+  qlora_status s = check_list(list);
+  if (s != QLORA_OK) return s;
+  if (!norm_and_clip || !ws || !(max_norm >= 0.0f)) return QLORA_ERR_INVALID_ARGUMENT;
+  if (!aligned(norm_and_clip, 4) || !aligned(ws, 256)) return QLORA_ERR_MISALIGNED;
+  if (ws_bytes < qlora_workspace_bytes_grad_norm()) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  int sms;
+  if ((s = check_device(nullptr, &sms)) != QLORA_OK) return s;
+  const int64_t most = std::min<int64_t>(kNormMaxCtas, static_cast<int64_t>(sms) * 8);
+  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(list->n_chunks, most)));
+  uint32_t *counter = status_ptr(ws) + 4;
+  double *partial = reinterpret_cast<double *>(static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (list->grad_dtype == QLORA_F32)
+    grad_norm_kernel<float><<<grid, kOptThreads, 0, st>>>(table_of(list), max_norm, norm_and_clip, counter, partial);
+  else
+    grad_norm_kernel<__nv_bfloat16><<<grid, kOptThreads, 0, st>>>(table_of(list), max_norm, norm_and_clip, counter, partial);
+  return launch_status();
+}
+
+qlora_status qlora_adamw_multi(const qlora_tensor_list *list, const qlora_adamw_hparams *hp, int64_t step,
+                               const float *norm_and_clip, uint32_t seed, qlora_stream_t stream) {
+  qlora_status s = check_list(list);
+  if (s != QLORA_OK) return s;
+  if (!hp || step < 1 || (list->state_bits != 8 && list->state_bits != 32)) return QLORA_ERR_INVALID_ARGUMENT;
+  if (!(hp->lr >= 0.0f) || !(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f) ||
+      !(hp->eps > 0.0f) || !(hp->weight_decay >= 0.0f) || !std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
+    return QLORA_ERR_INVALID_ARGUMENT;
+  if (!aligned(norm_and_clip, 4)) return QLORA_ERR_MISALIGNED;
+  int sms;
+  if ((s = check_device(nullptr, &sms)) != QLORA_OK) return s;
+  if (list->n_chunks == 0) return QLORA_OK;
+  AdamWMulti a;
+  const double bc1 = 1.0 - std::pow(static_cast<double>(hp->beta1), static_cast<double>(step));
+  const double bc2 = 1.0 - std::pow(static_cast<double>(hp->beta2), static_cast<double>(step));
+  a.beta1 = hp->beta1;
+  a.beta2 = hp->beta2;
+  a.eps = hp->eps;
+  a.sqrt_bc2 = static_cast<float>(std::sqrt(bc2));
+  a.lr = hp->lr;
+  a.weight_decay = hp->weight_decay;
+  a.step_size = hp->lr / bc1;
+  a.clip = norm_and_clip;
+  a.seed = seed;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(list->n_chunks, static_cast<int64_t>(sms) * 8));
+  const TensorTable t = table_of(list);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool f32 = list->grad_dtype == QLORA_F32;
+  if (list->state_bits == 32) {
+    if (f32) adamw_multi_kernel<float, false><<<grid, kOptThreads, 0, st>>>(t, a);
+    else adamw_multi_kernel<__nv_bfloat16, false><<<grid, kOptThreads, 0, st>>>(t, a);
+  } else {
+    if (f32) adamw_multi_kernel<float, true><<<grid, kOptThreads, 0, st>>>(t, a);
+    else adamw_multi_kernel<__nv_bfloat16, true><<<grid, kOptThreads, 0, st>>>(t, a);
+  }
   return launch_status();
 }
 

@@ -296,6 +296,162 @@ QLORA_API qlora_status qlora_adamw_step(float *param, void *param_bf16, const fl
                                         float *exp_avg_sq, int64_t n, const qlora_adamw_hparams *hp, int64_t step,
                                         qlora_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Many adapters on one base, any number of tokens ("What is LoRA?" (IBM): one
+ * shared frozen base, many small LoRA modules swapped per task; "QLoRA" glossary
+ * page, "Trade-offs": adapters are small enough to store and swap per task).
+ *
+ * A pool holds n adapters of at most rank r side by side.  Token t uses adapter
+ * a = adapter_of_token[t], or none (-1):
+ *   Y[t]  += s_a (X[t] A_a^T) B_a^T                 (qlora_adapters_fwd)
+ *   dX[t] += s_a (dY[t] B_a) A_a                    (qlora_adapters_bwd)
+ *   dA_a   = s_a sum_t (dY[t] B_a)^T X[t],   dB_a = s_a sum_t dY[t]^T (X[t] A_a^T)
+ * beside the output Y, or the input gradient dX, of a projection that the tokens
+ * share.  The tokens come grouped by adapter (qlora_adapter_groups), once per
+ * batch for all layers.
+ * ------------------------------------------------------------------------- */
+#define QLORA_MAX_ADAPTERS 1024
+
+/* Adapter pool; device buffers owned by the caller, A and B 16-byte aligned.
+ * r in [8, 256], a multiple of 8; n in [1, QLORA_MAX_ADAPTERS]. */
+typedef struct {
+  int32_t n;
+  int32_t r;
+  const void *A;        /* bf16 [n, r, K] */
+  const void *B;        /* bf16 [n, N, r] */
+  const int32_t *ranks; /* nullable int32 [n]: adapter i is made of the first ranks[i] rows of A[i] and columns of
+                           B[i] (a multiple of 8 in [0, r]; 0: an empty slot, adds nothing); what the buffers
+                           hold past them, NaN included, is not used.  NULL: every adapter has rank r */
+  const float *scales;  /* float32 [n]: s_i, for example alpha_i / rank_i */
+} qlora_adapter_pool;
+
+/* Groups M tokens by adapter: order [M] lists the tokens of adapter 0 in token
+ * order, then those of adapter 1, ..., and last the tokens without an adapter;
+ * adapter i's tokens are order[offsets[i] .. offsets[i + 1]) (offsets [n + 1]).
+ * All three are int32 device arrays.  M >= 0, below 2^30.  A value outside
+ * [-1, n) counts as -1 and sets QLORA_ERR_INVALID_ARGUMENT in the status word of
+ * ws (at least QLORA_STATUS_BYTES). */
+QLORA_API qlora_status qlora_adapter_groups(const int32_t *adapter_of_token, int64_t M, int32_t n, int32_t *order,
+                                            int32_t *offsets, void *ws, qlora_stream_t stream);
+
+/* Least workspace of qlora_adapters_fwd (for_backward = 0) and qlora_adapters_bwd
+ * (1), and of qlora_linear_fwd_pool and qlora_linear_bwd_pool: QLORA_STATUS_BYTES
+ * plus one, or two, bf16 [3, M, r] buffers, each rounded to 256 bytes; 0 for
+ * invalid sizes.  Only the status word has to start zeroed. */
+QLORA_API size_t qlora_workspace_bytes_adapters(int64_t M, int64_t N, int64_t K, int32_t r, int for_backward);
+
+/* Y[t] += s_a (X[t] A_a^T) B_a^T for every token of order[0 .. offsets[n]); the
+ * other rows of Y are not touched.  The sum is formed in float32 and rounded once.
+ *   order, offsets  as qlora_adapter_groups writes them
+ *   X   bf16 [M, K], row stride ldx (elements, a multiple of 8, >= K), 16-byte aligned
+ *   Y   [M, N] of y_dtype, row stride ldy >= N, element aligned; read and written
+ *   T_save  nullable bf16 [3, M, r], 16-byte aligned: receives T[t] = X[t] A_a^T for
+ *       the backward pass as three planes, each the bf16 rounding of what the ones
+ *       before leave, so that their sum carries 24 bits (columns past the adapter's
+ *       rank as zeros; rows of tokens without an adapter are not written)
+ * K and N multiples of 8, M >= 0.  An entry of order outside [0, M) is skipped,
+ * and, like a rank that is not a multiple of 8 in [0, r] (rounded down and
+ * clamped), sets QLORA_ERR_INVALID_ARGUMENT in the status word. */
+QLORA_API qlora_status qlora_adapters_fwd(const qlora_adapter_pool *pool, const int32_t *order,
+                                          const int32_t *offsets, const void *X, int64_t ldx, int64_t M, int64_t N,
+                                          int64_t K, void *Y, int64_t ldy, qlora_dtype y_dtype, void *T_save, void *ws,
+                                          size_t ws_bytes, qlora_stream_t stream);
+
+/* Gradients of qlora_adapters_fwd for the upstream gradient dY:
+ *   dX       nullable [M, K] of dx_dtype, row stride lddx >= K: added to as above
+ *   dA, dB   nullable, both or neither: [n, r, K] and [n, N, r] of grad_dtype,
+ *            16-byte aligned, overwritten; zeros for an adapter without tokens and
+ *            past an adapter's rank
+ *   T_saved  nullable: T_save of the forward; NULL recomputes it
+ * dY bf16 [M, N], row stride lddy (a multiple of 8, >= N), 16-byte aligned.  Sums
+ * run in a fixed order: the same inputs give the same bits. */
+QLORA_API qlora_status qlora_adapters_bwd(const qlora_adapter_pool *pool, const int32_t *order,
+                                          const int32_t *offsets, const void *X, int64_t ldx, const void *dY,
+                                          int64_t lddy, int64_t M, int64_t N, int64_t K, const void *T_saved, void *dX,
+                                          int64_t lddx, qlora_dtype dx_dtype, void *dA, void *dB,
+                                          qlora_dtype grad_dtype, void *ws, size_t ws_bytes, qlora_stream_t stream);
+
+/* The frozen NF4 layer with a pool beside it: Y = X W'^T, then qlora_adapters_fwd
+ * into Y (a bf16 Y is thus rounded twice: after the base product and after the
+ * adapters' term); and dX = dY W', then qlora_adapters_bwd into dX.  Arguments as
+ * qlora_linear_fwd / qlora_linear_bwd with the pool and the groups for the adapter
+ * (dX, dA and dB all required); M >= 1, W->rows a multiple of 8, contiguous rows.
+ * ws as for qlora_adapters_fwd / qlora_adapters_bwd. */
+QLORA_API qlora_status qlora_linear_fwd_pool(const qlora_nf4_tensor *W, const qlora_adapter_pool *pool,
+                                             const int32_t *order, const int32_t *offsets, const void *X, int64_t M,
+                                             void *Y, qlora_dtype y_dtype, void *T_save, void *ws, size_t ws_bytes,
+                                             qlora_stream_t stream);
+QLORA_API qlora_status qlora_linear_bwd_pool(const qlora_nf4_tensor *W, const qlora_adapter_pool *pool,
+                                             const int32_t *order, const int32_t *offsets, const void *X,
+                                             const void *dY, int64_t M, const void *T_saved, void *dX,
+                                             qlora_dtype dx_dtype, void *dA, void *dB, qlora_dtype grad_dtype, void *ws,
+                                             size_t ws_bytes, qlora_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * One optimiser step over the list of every adapter's tensors ("Grokking QLoRA"
+ * (vnread), "Paged Optimizers": Adam keeps a momentum and a variance for every
+ * trained parameter, and the memory they take), with states in 32 bits or in 8.
+ * ------------------------------------------------------------------------- */
+#define QLORA_STATE_BLOCK 256 /* elements that share one float32 scale of an 8-bit state */
+
+/* One tensor of a list: device pointers, aligned to their element type.  A list
+ * for qlora_grad_norm alone needs only n and grad.
+ * 8-bit states: element i of a block of 256 consecutive elements of the tensor is
+ * code value * scale of its block; exp_avg codes are OCP FP8 E4M3, exp_avg_sq
+ * codes OCP FP8 E5M2 (sign 0); zero codes and scales before step 1. */
+typedef struct {
+  int64_t n;               /* elements, >= 0 */
+  const void *grad;        /* [n] of the list's grad_dtype */
+  float *param;            /* float32 [n] */
+  void *param_bf16;        /* nullable bf16 [n]: receives bf16(param), the copy the layer reads */
+  void *exp_avg;           /* float32 [n], or uint8 codes [n] */
+  void *exp_avg_sq;
+  float *exp_avg_scale;    /* 8-bit states: float32 [ceil(n / 256)]; else not read */
+  float *exp_avg_sq_scale;
+  float lr_scale;          /* factor of the learning rate for this tensor (1: none), finite, >= 0 */
+} qlora_tensor;
+
+/* A list that qlora_tensor_list_init has written; a host struct of plain values. */
+typedef struct {
+  const void *table;   /* device memory owned by the caller */
+  int32_t n_tensors;
+  int32_t state_bits;  /* 0: gradients only, 8 or 32 */
+  int32_t grad_dtype;  /* qlora_dtype */
+  int64_t n_chunks;
+} qlora_tensor_list;
+
+/* Bytes of the device table of a list of n_tensors >= 1 tensors; 0 if one of
+ * them has a negative size or the list is too long (2^31 chunks of 2048). */
+QLORA_API size_t qlora_tensor_list_bytes(const qlora_tensor *tensors, int32_t n_tensors);
+
+/* Writes the table (16-byte aligned device memory of table_bytes) on `stream` and
+ * fills *out.  The pointers are read by the later calls, so the tensors must stay
+ * where they are; no tensor may be listed twice. */
+QLORA_API qlora_status qlora_tensor_list_init(const qlora_tensor *tensors, int32_t n_tensors, qlora_dtype grad_dtype,
+                                              int32_t state_bits, void *table, size_t table_bytes,
+                                              qlora_tensor_list *out, qlora_stream_t stream);
+
+/* norm_and_clip[0] = sqrt(sum of the squares of all gradients), [1] = min(1,
+ * max_norm / (norm + 1e-6)), float32 on the device (4-byte aligned).  Squares are
+ * summed in float64, in a fixed order.  A NaN or infinity among the gradients
+ * gives a norm that is not finite and a factor of NaN.  max_norm >= 0 (infinity: no
+ * clipping).  ws: qlora_workspace_bytes_grad_norm() bytes, zeroed when new. */
+QLORA_API size_t qlora_workspace_bytes_grad_norm(void);
+QLORA_API qlora_status qlora_grad_norm(const qlora_tensor_list *list, float max_norm, float *norm_and_clip, void *ws,
+                                       size_t ws_bytes, qlora_stream_t stream);
+
+/* One AdamW step, as qlora_adamw_step, on every tensor of the list, with the
+ * learning rate lr * lr_scale.
+ *   norm_and_clip  nullable, as qlora_grad_norm writes it: gradients are multiplied
+ *       by norm_and_clip[1]; where that is NaN the step changes nothing
+ *   seed  8-bit states are rounded stochastically: the random bits are a hash of
+ *       (seed, place in the list, element), so a step is reproducible; give each
+ *       step another seed
+ * The parameters see the new states before they are rounded to 8 bits.  A variance
+ * that is not zero is never rounded to zero. */
+QLORA_API qlora_status qlora_adamw_multi(const qlora_tensor_list *list, const qlora_adamw_hparams *hp, int64_t step,
+                                         const float *norm_and_clip, uint32_t seed, qlora_stream_t stream);
+
 /* Zero the status word and the decode forward's arrival count at the start of
  * ws (enqueued on stream).  The call generation is kept: the decode forward's
  * s*T entries in ws are tagged with it, and a generation that went backwards
