@@ -991,38 +991,6 @@ qlora_status launch_pool_grads(const PoolArgs &a, const __nv_bfloat16 *U, const 
   return launch_status();
 }
 
-qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
-                      int64_t ldx, int64_t M, int64_t N, int64_t K, void *Y, int64_t ldy, qlora_dtype y_dtype,
-                      void *T_save, void *ws, int sms, cudaStream_t st) {
-  if (M == 0) return QLORA_OK;
-  const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
-  __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
-  const qlora_status s = launch_pool_down(a, X, ldx, K, false, T, sms, st);
-  return s != QLORA_OK ? s : launch_pool_up(a, T, true, N, Y, ldy, y_dtype, sms, st);
-}
-
-qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
-                      int64_t ldx, const void *dY, int64_t lddy, int64_t M, int64_t N, int64_t K, const void *T_saved,
-                      void *dX, int64_t lddx, qlora_dtype dx_dtype, void *dA, void *dB, qlora_dtype grad_dtype, void *ws,
-                      int sms, cudaStream_t st) {
-  const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
-  __nv_bfloat16 *U = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
-  const __nv_bfloat16 *T = static_cast<const __nv_bfloat16 *>(T_saved);
-  qlora_status s;
-  if (M > 0) {
-    if ((s = launch_pool_down(a, dY, lddy, N, true, U, sms, st)) != QLORA_OK) return s;
-    if (dX && (s = launch_pool_up(a, U, false, K, dX, lddx, dx_dtype, sms, st)) != QLORA_OK) return s;
-    if (dA && !T) {
-      __nv_bfloat16 *Tw = U + align256(static_cast<size_t>(kPoolPlanes) * M * a.r * 2) / 2;
-      if ((s = launch_pool_down(a, X, ldx, K, false, Tw, sms, st)) != QLORA_OK) return s;
-      T = Tw;
-    }
-  }
-  if (!dA) return QLORA_OK;
-  return grad_dtype == QLORA_F32 ? launch_pool_grads<float>(a, U, X, ldx, T, dY, lddy, dA, dB, sms, st)
-                                 : launch_pool_grads<__nv_bfloat16>(a, U, X, ldx, T, dY, lddy, dA, dB, sms, st);
-}
-
 // The base products alone: Y = X W'^T, and dX = dY W'.
 qlora_status base_fwd(const qlora_nf4_tensor *W, const void *X, int64_t M, void *Y, qlora_dtype y_dtype, void *ws,
                       int dev, int sms, cudaStream_t st) {
@@ -1096,6 +1064,41 @@ qlora_status base_bwd(const qlora_nf4_tensor *W, const void *dY, int64_t M, void
   return launch_gemm<false, true, true, 256, kFusedMT>(tmDY, tmDY, tmDY, tmDY, tmCodes, g, dev, sms, st);
 }
 
+qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
+                      int64_t ldx, int64_t M, int64_t N, int64_t K, void *Y, int64_t ldy, qlora_dtype y_dtype,
+                      void *T_save, void *ws, int dev, int sms, cudaStream_t st, const qlora_nf4_tensor *W = nullptr) {
+  if (M == 0) return QLORA_OK;
+  const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
+  __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
+  qlora_status s = launch_pool_down(a, X, ldx, K, false, T, sms, st);
+  // The base product comes between T and the adapters' term: its decode kernel reads X before it waits for the
+  // kernel ahead of it, which is right only behind one that has itself waited for X, as T has.
+  if (s == QLORA_OK && W) s = base_fwd(W, X, M, Y, y_dtype, ws, dev, sms, st);
+  return s != QLORA_OK ? s : launch_pool_up(a, T, true, N, Y, ldy, y_dtype, sms, st);
+}
+
+qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
+                      int64_t ldx, const void *dY, int64_t lddy, int64_t M, int64_t N, int64_t K, const void *T_saved,
+                      void *dX, int64_t lddx, qlora_dtype dx_dtype, void *dA, void *dB, qlora_dtype grad_dtype, void *ws,
+                      int sms, cudaStream_t st) {
+  const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
+  __nv_bfloat16 *U = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
+  const __nv_bfloat16 *T = static_cast<const __nv_bfloat16 *>(T_saved);
+  qlora_status s;
+  if (M > 0) {
+    if ((s = launch_pool_down(a, dY, lddy, N, true, U, sms, st)) != QLORA_OK) return s;
+    if (dX && (s = launch_pool_up(a, U, false, K, dX, lddx, dx_dtype, sms, st)) != QLORA_OK) return s;
+    if (dA && !T) {
+      __nv_bfloat16 *Tw = U + align256(static_cast<size_t>(kPoolPlanes) * M * a.r * 2) / 2;
+      if ((s = launch_pool_down(a, X, ldx, K, false, Tw, sms, st)) != QLORA_OK) return s;
+      T = Tw;
+    }
+  }
+  if (!dA) return QLORA_OK;
+  return grad_dtype == QLORA_F32 ? launch_pool_grads<float>(a, U, X, ldx, T, dY, lddy, dA, dB, sms, st)
+                                 : launch_pool_grads<__nv_bfloat16>(a, U, X, ldx, T, dY, lddy, dA, dB, sms, st);
+}
+
 qlora_status check_out(const void *p, int64_t ld, int64_t cols, qlora_dtype dt) {
   if (!valid_dtype(dt)) return QLORA_ERR_INVALID_ARGUMENT;
   if (ld < cols) return QLORA_ERR_UNSUPPORTED_SHAPE;
@@ -1140,7 +1143,7 @@ qlora_status qlora_adapters_fwd(const qlora_adapter_pool *pool, const int32_t *o
   if (ws_bytes < pool_ws_bytes(M, pool->r, 0)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
   int dev, sms;
   if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
-  return pool_fwd(pool, order, offsets, X, ldx, M, N, K, Y, ldy, y_dtype, T_save, ws, sms,
+  return pool_fwd(pool, order, offsets, X, ldx, M, N, K, Y, ldy, y_dtype, T_save, ws, dev, sms,
                   reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -1173,9 +1176,8 @@ qlora_status qlora_linear_fwd_pool(const qlora_nf4_tensor *W, const qlora_adapte
   if (ws_bytes < pool_ws_bytes(M, pool->r, 0)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
   int dev, sms;
   if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if ((s = base_fwd(W, X, M, Y, y_dtype, ws, dev, sms, st)) != QLORA_OK) return s;
-  return pool_fwd(pool, order, offsets, X, K, M, N, K, Y, N, y_dtype, T_save, ws, sms, st);
+  return pool_fwd(pool, order, offsets, X, K, M, N, K, Y, N, y_dtype, T_save, ws, dev, sms,
+                  reinterpret_cast<cudaStream_t>(stream), W);
 }
 
 qlora_status qlora_linear_bwd_pool(const qlora_nf4_tensor *W, const qlora_adapter_pool *pool, const int32_t *order,
