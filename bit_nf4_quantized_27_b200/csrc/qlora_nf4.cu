@@ -912,7 +912,7 @@ qlora_status qlora_adamw_step(float *param, void *param_bf16, const float *grad,
 // Many adapters on one base
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int64_t kPoolMaxTokens = int64_t(1) << 30;
+constexpr int64_t kPoolMaxTokens = (int64_t(1) << 29) - 1;  // the rows of three planes count below 2^31
 
 qlora_status check_pool(const qlora_adapter_pool *p) {
   if (!p || !p->A || !p->B || !p->scales) return QLORA_ERR_INVALID_ARGUMENT;
@@ -942,8 +942,6 @@ size_t pool_ws_bytes(int64_t M, int32_t r, int for_backward) {
 PoolArgs pool_args(const qlora_adapter_pool *p, const int32_t *order, const int32_t *offsets, int64_t M, int64_t N,
                    int64_t K, void *ws) {
   PoolArgs a{};
-  a.A = static_cast<const __nv_bfloat16 *>(p->A);
-  a.B = static_cast<const __nv_bfloat16 *>(p->B);
   a.ranks = p->ranks;
   a.scales = p->scales;
   a.n = p->n;
@@ -957,38 +955,129 @@ PoolArgs pool_args(const qlora_adapter_pool *p, const int32_t *order, const int3
   return a;
 }
 
-unsigned pool_grid(int64_t threads, int sms) {
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((threads + 255) / 256, static_cast<int64_t>(sms) * 16)));
+// A pool's matrices [n][rows][inner] bf16, box 64 x box_rows of one of them: what lies past its rows or columns reads
+// as zeros and not as the next one's.
+bool tmap_pool(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, int n, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner) * 2, static_cast<cuuint64_t>(inner) * rows * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// P = V W_a for every grouped token, as three planes.
-qlora_status launch_pool_down(const PoolArgs &a, const void *V, int64_t ldv, int64_t len, bool transposed,
-                              __nv_bfloat16 *P, int sms, cudaStream_t st) {
-  pool_down_kernel<<<pool_grid(a.M * a.r * 32, sms), 256, 0, st>>>(a, static_cast<const __nv_bfloat16 *>(V), ldv, len,
-                                                                  transposed, P);
-  return launch_status();
+// Token rows to gather: [rows, inner] bf16 with row stride ld, one row a box.
+bool tmap_tokens(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, int64_t ld) {
+  return make_tmap(m, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, rows, ld, 64, 1, true);
 }
 
-// Out[t] += s_a P[t] W_a for every grouped token.
-qlora_status launch_pool_up(const PoolArgs &a, const __nv_bfloat16 *P, bool transposed, int64_t cols, void *Out,
-                            int64_t ldo, qlora_dtype dt, int sms, cudaStream_t st) {
-  const unsigned grid = pool_grid(a.M * cols, sms);
-  if (dt == QLORA_F32)
-    pool_up_kernel<float><<<grid, 256, 0, st>>>(a, P, transposed, cols, static_cast<float *>(Out), ldo);
-  else
-    pool_up_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a, P, transposed, cols, static_cast<__nv_bfloat16 *>(Out), ldo);
-  return launch_status();
+// Launch of `clusters` clusters of `cs` CTAs, allowed to begin while the kernel ahead ends.
+template <typename... KArgs, typename... Args>
+qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int threads, int n, int dev, std::once_flag *flags,
+                         qlora_status *results, cudaStream_t st, Args &&...args) {
+  const qlora_status s = set_smem(kernel, static_cast<int>(pool_smem_bytes(QLORA_MAX_ADAPTERS)), dev, flags, results);
+  if (s != QLORA_OK) return s;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cs));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = pool_smem_bytes(n);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return QLORA_OK;
+}
+
+// Most tiles of tn tokens that M tokens of n adapters can make.
+int64_t pool_most_tiles(int64_t M, int n, int tn) { return M / tn + std::min<int64_t>(n, M); }
+
+// P = V W_a for every grouped token.  T: V = X, W = A; U: V = dY, W = B (MN-major).
+template <bool W_MN>
+qlora_status launch_pool_down(const PoolArgs &p, const void *V, int64_t ldv, const void *W, __nv_bfloat16 *P, int dev,
+                              int sms, cudaStream_t st) {
+  const int64_t len = W_MN ? p.N : p.K;
+  CUtensorMap tmW, tmV;
+  if (!(W_MN ? tmap_pool(&tmW, W, p.r, len, p.n, 64) : tmap_pool(&tmW, W, len, p.r, p.n, std::min(p.r, 128))) ||
+      !tmap_tokens(&tmV, V, len, p.M, ldv))
+    return QLORA_ERR_CUDA;
+  PoolDownArgs a;
+  a.p = p;
+  a.k_steps = static_cast<int>((len + 63) / 64);
+  a.P = P;
+  // split the long dimension while the tiles that full groups make would leave CTAs idle (two to an SM)
+  const int nrb = (p.r + 127) / 128, target = 2 * sms;
+  const int64_t tiles = (p.M + kPoolDownTile - 1) / kPoolDownTile * nrb;
+  int cs = 8;
+  while (cs > 1 && (tiles * cs > target || cs * 2 > a.k_steps)) cs /= 2;
+  const int64_t clusters = std::min<int64_t>(pool_most_tiles(p.M, p.n, kPoolDownTile) * nrb, target / cs);
+  static std::once_flag flags[64];
+  static qlora_status results[64];
+  return launch_pool(pool_down_kernel<W_MN>, clusters, cs, kPoolDownThreads, p.n, dev, flags, results, st, tmW, tmV, a);
+}
+
+// Out[t] += s_a P[t] W_a for every grouped token.  Y: W = B; dX: W = A (MN-major).
+template <bool W_MN, typename O>
+qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo, int dev,
+                              int sms, cudaStream_t st) {
+  const int64_t cols = W_MN ? p.K : p.N;
+  CUtensorMap tmW, tmP;
+  if (!(W_MN ? tmap_pool(&tmW, W, cols, p.r, p.n, 64) : tmap_pool(&tmW, W, p.r, cols, p.n, 128)) ||
+      !tmap_tokens(&tmP, P, p.r, kPoolPlanes * p.M, p.r))
+    return QLORA_ERR_CUDA;
+  PoolUpArgs a;
+  a.p = p;
+  a.cols = cols;
+  a.ldo = ldo;
+  a.out = Out;
+  a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
+  a.tn = pool_up_tile(p.r, a.planes);
+  const int64_t units = pool_most_tiles(p.M, p.n, a.tn) * ((cols + 127) / 128);
+  static std::once_flag flags[64];
+  static qlora_status results[64];
+  return launch_pool(pool_up_kernel<W_MN, O>, std::min<int64_t>(units, 2 * sms), 1, kPoolUpThreads, p.n, dev, flags, results,
+                     st, tmW, tmP, a);
+}
+template <bool W_MN>
+qlora_status launch_pool_up(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo,
+                            qlora_dtype dt, int dev, int sms, cudaStream_t st) {
+  return dt == QLORA_F32 ? launch_pool_up_t<W_MN, float>(p, P, W, Out, ldo, dev, sms, st)
+                         : launch_pool_up_t<W_MN, __nv_bfloat16>(p, P, W, Out, ldo, dev, sms, st);
 }
 
 template <typename O>
-qlora_status launch_pool_grads(const PoolArgs &a, const __nv_bfloat16 *U, const void *X, int64_t ldx,
-                               const __nv_bfloat16 *T, const void *dY, int64_t lddy, void *dA, void *dB, int sms, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.n) * a.r;
-  pool_grad_kernel<O><<<pool_grid(rows * a.K, sms), 256, 0, st>>>(a, U, static_cast<const __nv_bfloat16 *>(X), ldx,
-                                                                  a.K, false, static_cast<O *>(dA));
-  pool_grad_kernel<O><<<pool_grid(rows * a.N, sms), 256, 0, st>>>(a, T, static_cast<const __nv_bfloat16 *>(dY), lddy,
-                                                                  a.N, true, static_cast<O *>(dB));
-  return launch_status();
+qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const void *X, int64_t ldx,
+                               const __nv_bfloat16 *T, const void *dY, int64_t lddy, void *dA, void *dB, int dev,
+                               int sms, cudaStream_t st) {
+  CUtensorMap tmX{}, tmU{}, tmDY{}, tmT{};
+  if (p.M > 0 && (!tmap_tokens(&tmX, X, p.K, p.M, ldx) || !tmap_tokens(&tmU, U, p.r, kPoolPlanes * p.M, p.r) ||
+                  !tmap_tokens(&tmDY, dY, p.N, p.M, lddy) || !tmap_tokens(&tmT, T, p.r, kPoolPlanes * p.M, p.r)))
+    return QLORA_ERR_CUDA;
+  PoolGradArgs a;
+  a.p = p;
+  a.dA = dA;
+  a.dB = dB;
+  a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
+  // split the tokens while the tiles of dA and dB leave CTAs idle (two to an SM) and a part has whole steps of 64
+  const int64_t units = static_cast<int64_t>(p.n) * ((p.r + 63) / 64) * ((p.K + 127) / 128 + (p.N + 127) / 128);
+  int cs = 8;
+  while (cs > 1 && (units * cs > 4 * sms || cs * 64 > p.M)) cs /= 2;
+  const int64_t clusters = std::min<int64_t>(units, 2 * sms / cs);
+  static std::once_flag flags[64];
+  static qlora_status results[64];
+  return launch_pool(pool_grad_kernel<O>, clusters, cs, kPoolGradThreads, p.n, dev, flags, results, st, tmX, tmU, tmDY, tmT, a);
 }
 
 // The base products alone: Y = X W'^T, and dX = dY W'.
@@ -1070,33 +1159,33 @@ qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, cons
   if (M == 0) return QLORA_OK;
   const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
   __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
-  qlora_status s = launch_pool_down(a, X, ldx, K, false, T, sms, st);
+  qlora_status s = launch_pool_down<false>(a, X, ldx, pool->A, T, dev, sms, st);
   // The base product comes between T and the adapters' term: its decode kernel reads X before it waits for the
   // kernel ahead of it, which is right only behind one that has itself waited for X, as T has.
   if (s == QLORA_OK && W) s = base_fwd(W, X, M, Y, y_dtype, ws, dev, sms, st);
-  return s != QLORA_OK ? s : launch_pool_up(a, T, true, N, Y, ldy, y_dtype, sms, st);
+  return s != QLORA_OK ? s : launch_pool_up<false>(a, T, pool->B, Y, ldy, y_dtype, dev, sms, st);
 }
 
 qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
                       int64_t ldx, const void *dY, int64_t lddy, int64_t M, int64_t N, int64_t K, const void *T_saved,
                       void *dX, int64_t lddx, qlora_dtype dx_dtype, void *dA, void *dB, qlora_dtype grad_dtype, void *ws,
-                      int sms, cudaStream_t st) {
+                      int dev, int sms, cudaStream_t st) {
   const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
   __nv_bfloat16 *U = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
   const __nv_bfloat16 *T = static_cast<const __nv_bfloat16 *>(T_saved);
   qlora_status s;
   if (M > 0) {
-    if ((s = launch_pool_down(a, dY, lddy, N, true, U, sms, st)) != QLORA_OK) return s;
-    if (dX && (s = launch_pool_up(a, U, false, K, dX, lddx, dx_dtype, sms, st)) != QLORA_OK) return s;
+    if ((s = launch_pool_down<true>(a, dY, lddy, pool->B, U, dev, sms, st)) != QLORA_OK) return s;
+    if (dX && (s = launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, dev, sms, st)) != QLORA_OK) return s;
     if (dA && !T) {
       __nv_bfloat16 *Tw = U + align256(static_cast<size_t>(kPoolPlanes) * M * a.r * 2) / 2;
-      if ((s = launch_pool_down(a, X, ldx, K, false, Tw, sms, st)) != QLORA_OK) return s;
+      if ((s = launch_pool_down<false>(a, X, ldx, pool->A, Tw, dev, sms, st)) != QLORA_OK) return s;
       T = Tw;
     }
   }
   if (!dA) return QLORA_OK;
-  return grad_dtype == QLORA_F32 ? launch_pool_grads<float>(a, U, X, ldx, T, dY, lddy, dA, dB, sms, st)
-                                 : launch_pool_grads<__nv_bfloat16>(a, U, X, ldx, T, dY, lddy, dA, dB, sms, st);
+  return grad_dtype == QLORA_F32 ? launch_pool_grads<float>(a, U, X, ldx, T, dY, lddy, dA, dB, dev, sms, st)
+                                 : launch_pool_grads<__nv_bfloat16>(a, U, X, ldx, T, dY, lddy, dA, dB, dev, sms, st);
 }
 
 qlora_status check_out(const void *p, int64_t ld, int64_t cols, qlora_dtype dt) {
@@ -1161,7 +1250,7 @@ qlora_status qlora_adapters_bwd(const qlora_adapter_pool *pool, const int32_t *o
   int dev, sms;
   if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
   return pool_bwd(pool, order, offsets, X, ldx, dY, lddy, M, N, K, T_saved, dX, lddx, dx_dtype, dA, dB, grad_dtype, ws,
-                  sms, reinterpret_cast<cudaStream_t>(stream));
+                  dev, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 qlora_status qlora_linear_fwd_pool(const qlora_nf4_tensor *W, const qlora_adapter_pool *pool, const int32_t *order,
@@ -1197,7 +1286,7 @@ qlora_status qlora_linear_bwd_pool(const qlora_nf4_tensor *W, const qlora_adapte
   if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if ((s = base_bwd(W, dY, M, dX, dx_dtype, ws, dev, sms, st)) != QLORA_OK) return s;
-  return pool_bwd(pool, order, offsets, X, K, dY, N, M, N, K, T_saved, dX, K, dx_dtype, dA, dB, grad_dtype, ws, sms, st);
+  return pool_bwd(pool, order, offsets, X, K, dY, N, M, N, K, T_saved, dX, K, dx_dtype, dA, dB, grad_dtype, ws, dev, sms, st);
 }
 
 // ---------------------------------------------------------------------------

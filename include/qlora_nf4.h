@@ -328,7 +328,7 @@ typedef struct {
 /* Groups M tokens by adapter: order [M] lists the tokens of adapter 0 in token
  * order, then those of adapter 1, ..., and last the tokens without an adapter;
  * adapter i's tokens are order[offsets[i] .. offsets[i + 1]) (offsets [n + 1]).
- * All three are int32 device arrays.  M >= 0, below 2^30.  A value outside
+ * All three are int32 device arrays.  M >= 0, below 2^29.  A value outside
  * [-1, n) counts as -1 and sets QLORA_ERR_INVALID_ARGUMENT in the status word of
  * ws (at least QLORA_STATUS_BYTES). */
 QLORA_API qlora_status qlora_adapter_groups(const int32_t *adapter_of_token, int64_t M, int32_t n, int32_t *order,
@@ -349,9 +349,10 @@ QLORA_API size_t qlora_workspace_bytes_adapters(int64_t M, int64_t N, int64_t K,
  *       the backward pass as three planes, each the bf16 rounding of what the ones
  *       before leave, so that their sum carries 24 bits (columns past the adapter's
  *       rank as zeros; rows of tokens without an adapter are not written)
- * K and N multiples of 8, M >= 0.  An entry of order outside [0, M) is skipped,
- * and, like a rank that is not a multiple of 8 in [0, r] (rounded down and
- * clamped), sets QLORA_ERR_INVALID_ARGUMENT in the status word. */
+ * K and N multiples of 8, 0 <= M < 2^29.  An entry of order outside [0, M) is
+ * skipped (the backward's dA and dB are then unspecified), and, like a rank that is
+ * not a multiple of 8 in [0, r] (rounded down and clamped), sets
+ * QLORA_ERR_INVALID_ARGUMENT in the status word. */
 QLORA_API qlora_status qlora_adapters_fwd(const qlora_adapter_pool *pool, const int32_t *order,
                                           const int32_t *offsets, const void *X, int64_t ldx, int64_t M, int64_t N,
                                           int64_t K, void *Y, int64_t ldy, qlora_dtype y_dtype, void *T_save, void *ws,

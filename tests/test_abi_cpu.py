@@ -242,7 +242,7 @@ def test_adapters_argument_checks_without_gpu(L):
     for bad in (_pool(A=0x4008), _pool(B=0x5008), _pool(ranks=0x7002)):
         assert fwd(pool=bad) == 3
     assert fwd(order=None) == 1 and fwd(off=None) == 1 and fwd(X=None) == 1 and fwd(Y=None) == 1 and fwd(ws=None) == 1
-    assert fwd(M=-1) == 1 and fwd(M=(1 << 30) + 1) == 1 and fwd(dt=2) == 1
+    assert fwd(M=-1) == 1 and fwd(M=1 << 29) == 1 and fwd(dt=2) == 1
     assert fwd(K=124, ldx=128) == 2 and fwd(N=60) == 2 and fwd(N=0) == 2 and fwd(ldx=120) == 2 and fwd(ldx=132) == 2
     assert fwd(ldy=63) == 2
     assert fwd(X=X + 8) == 3 and fwd(Y=Y + 1) == 3 and fwd(Y=Y + 2, dt=0) == 3 and fwd(T=T + 8) == 3 and fwd(ws=ws + 16) == 3
