@@ -197,7 +197,7 @@ __device__ __forceinline__ void ring_drain(uint64_t *full, RingPos pos, uint32_t
 }
 
 // Shared memory of one CTA: two share an SM's 227 KB, whatever the rank.
-constexpr uint32_t kPoolRingBytes = 96 * 1024;
+constexpr uint32_t kPoolRingBytes = 98 * 1024;
 __host__ __device__ constexpr uint32_t pool_smem_bytes(int n) {
   return 1024 + kPoolRingBytes + 512 + (static_cast<uint32_t>(n) + 1) * 4;
 }
@@ -409,9 +409,13 @@ __global__ void __launch_bounds__(kPoolDownThreads) pool_down_kernel(const __gri
 // ---------------------------------------------------------------------------
 // up: one unit is a tile of tokens and a run of 128-feature blocks.  P's rows of the tile
 // are loaded once, the blocks of W stream through the ring, and the accumulator of one
-// block is computed while the one before is added to Out: lanes hold features, so a
-// warp reads and writes 32 consecutive elements of each token's row, whatever the
-// row stride, the alignment and the number of columns.
+// block is computed while the one before is added to Out.  A warp of the epilogue takes 32
+// features x half of the tile's tokens.  Its lanes hold features; where Out's rows are
+// 16-byte aligned, 16 tokens at a time pass through shared memory, so that four lanes (bf16;
+// eight for float32) then share a token's 32 features in 16-byte pieces, all loaded before the accumulator is waited
+// for (64 KB in flight on an SM; element by element the epilogue took 47 instructions an
+// element and warp and bound the kernel on issue).  Other outputs, odd strides or columns of a
+// wider tensor, go element by element.
 //   warp 0  loads; warp 1  products; warps 2..9  Out += s_a accumulator
 // W_MN false: W is [n][cols][r] (Y: B); true: [n][r][cols] (dX: A).
 // ---------------------------------------------------------------------------
@@ -426,10 +430,17 @@ struct PoolUpArgs {
   int tn;  // tokens a tile: 128, 64 or 32
 };
 
-// Tokens of an up tile: as many as keep P's planes within 64 KB.
+// Tokens of an up tile: as many as keep P's planes within 48 KB, which leaves the ring two stages or more.
+constexpr uint32_t kPoolUpPlaneBytes = 48 * 1024, kPoolUpRingBytes = 80 * 1024;
 __host__ __device__ constexpr int pool_up_tile(int r, int planes) {
-  return (r + 63) / 64 * planes * 128 * 128 <= 65536 ? 128 : (r + 63) / 64 * planes * 64 * 128 <= 65536 ? 64 : 32;
+  const uint32_t row = (r + 63) / 64 * planes * 128u;
+  return row * 128 <= kPoolUpPlaneBytes ? 128 : row * 64 <= kPoolUpPlaneBytes ? 64 : 32;
 }
+static_assert(pool_up_tile(256, 3) == 32 && 4 * 3 * 32 * 128 <= kPoolUpPlaneBytes, "the largest rank fits");
+// Shared memory of a warp's 16 tokens x 32 features: a pitch of 36 floats keeps 16-byte pieces aligned and both
+// directions without bank conflicts.
+constexpr int kPoolUpPitch = 36, kPoolUpBuf = 16 * kPoolUpPitch;
+static_assert(kPoolUpRingBytes + 8 * kPoolUpBuf * 4 <= kPoolRingBytes, "shared memory");
 
 __device__ __forceinline__ float pool_load(const float *p) { return __ldcg(p); }
 __device__ __forceinline__ float pool_load(const __nv_bfloat16 *p) {
@@ -438,7 +449,37 @@ __device__ __forceinline__ float pool_load(const __nv_bfloat16 *p) {
 __device__ __forceinline__ void pool_store(float *p, float v) { *p = v; }
 __device__ __forceinline__ void pool_store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <bool W_MN, typename O>
+// 16 bytes of Out: y + s v, rounded once.  kElems elements; a row's 32 features take 32 / kElems lanes, so that each
+// instruction covers whole sectors.  kTokens: loaded ahead by a warp, 4 KB.
+template <typename O>
+struct PoolPiece;
+template <>
+struct PoolPiece<float> {
+  static constexpr int kElems = 4, kTokens = 32;
+  float4 y;
+  __device__ __forceinline__ void zero() { y = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void load(const float *p) { y = __ldcg(reinterpret_cast<const float4 *>(p)); }
+  __device__ __forceinline__ void add_store(float *p, float s, const float *v) const {
+    const float4 u = *reinterpret_cast<const float4 *>(v);
+    *reinterpret_cast<float4 *>(p) = make_float4(fmaf(s, u.x, y.x), fmaf(s, u.y, y.y), fmaf(s, u.z, y.z), fmaf(s, u.w, y.w));
+  }
+};
+template <>
+struct PoolPiece<__nv_bfloat16> {
+  static constexpr int kElems = 8, kTokens = 64;
+  uint4 y;
+  __device__ __forceinline__ void zero() { y = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { y = __ldcg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void add_store(__nv_bfloat16 *p, float s, const float *v) const {
+    const float4 u = reinterpret_cast<const float4 *>(v)[0], w = reinterpret_cast<const float4 *>(v)[1];
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(fmaf(s, u.x, bf16lo_to_f32(y.x)), fmaf(s, u.y, bf16hi_to_f32(y.x))),
+                                               pack_bf16x2(fmaf(s, u.z, bf16lo_to_f32(y.y)), fmaf(s, u.w, bf16hi_to_f32(y.y))),
+                                               pack_bf16x2(fmaf(s, w.x, bf16lo_to_f32(y.z)), fmaf(s, w.y, bf16hi_to_f32(y.z))),
+                                               pack_bf16x2(fmaf(s, w.z, bf16lo_to_f32(y.w)), fmaf(s, w.w, bf16hi_to_f32(y.w))));
+  }
+};
+
+template <bool W_MN, typename O, bool VEC>
 __global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                     const __grid_constant__ CUtensorMap tmP,
                                                                     const PoolUpArgs a) {
@@ -448,7 +489,7 @@ __global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid
   const PoolArgs &p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tn = a.tn;
   const uint32_t plane_bytes = tn * 128u, p_bytes = (p.r + 63) / 64 * a.planes * plane_bytes;
-  const uint32_t stages = min((kPoolRingBytes - p_bytes) / 16384u, 4u);
+  const uint32_t stages = min((kPoolUpRingBytes - p_bytes) / 16384u, 4u);
   uint8_t *ring = sm.ring + p_bytes;
   uint64_t *full = sm.bars, *empty = sm.bars + 4, *acc_full = sm.bars + 8, *acc_empty = sm.bars + 10, *p_full = sm.bars + 12;
   const uint32_t tmem = pool_setup(sm, kPoolUpTmem, 10, 8);
@@ -562,26 +603,66 @@ __global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid
         const int64_t f = static_cast<int64_t>(b) * 128 + quad * 32 + lane;
         O *out = static_cast<O *>(a.out) + f;
         bool ready = false;
-        for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-          float y[32];
+        if (VEC) {
+          float *buf = reinterpret_cast<float *>(sm.ring + kPoolUpRingBytes) + (warp - 2) * kPoolUpBuf;
+          constexpr int kGroup = PoolPiece<O>::kTokens, kElems = PoolPiece<O>::kElems, kLanes = 32 / kElems, kRows = 32 / kLanes;
+          const int tr = lane / kLanes, part = lane % kLanes;
+          const int64_t f8 = static_cast<int64_t>(b) * 128 + quad * 32 + part * kElems;
+          O *out8 = static_cast<O *>(a.out) + f8;
+          for (int g0 = c_lo; g0 < c_hi; g0 += kGroup) {
+            PoolPiece<O> y[kGroup / kRows];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int t = c0 + j < c_hi ? token[c0 + j] : -1;
-            y[j] = t >= 0 && f < a.cols ? pool_load(out + t * a.ldo) : 0.0f;
-          }
-          if (!ready) {
-            ready = true;
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 1) & 1, sm.abort_flag));
-            if (!ok) break;
-            ptx::tc_fence_after();
-          }
-          uint32_t v[32];
-          ptx::tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128 + c0, v);
-          ptx::tmem_ld_wait();
+            for (int i = 0; i < kGroup / kRows; ++i) {
+              const int c = g0 + kRows * i + tr, t = c < c_hi ? token[c] : -1;
+              if (t >= 0 && f8 < a.cols) y[i].load(out8 + t * a.ldo);
+              else y[i].zero();
+            }
+            if (!ready) {
+              ready = true;
+              ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 1) & 1, sm.abort_flag));
+              if (!ok) break;
+              ptx::tc_fence_after();
+            }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int t = c0 + j < c_hi ? token[c0 + j] : -1;
-            if (t >= 0 && f < a.cols) pool_store(out + t * a.ldo, fmaf(s, __uint_as_float(v[j]), y[j]));
+            for (int k = 0; k < kGroup / 16; ++k) {
+              if (g0 + 16 * k >= c_hi) break;
+              uint32_t v[16];
+              ptx::tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128 + g0 + 16 * k, v);
+              ptx::tmem_ld_wait();
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) buf[j * kPoolUpPitch + lane] = __uint_as_float(v[j]);
+              __syncwarp();
+#pragma unroll
+              for (int h = 0; h < 16 / kRows; ++h) {
+                const int c = g0 + 16 * k + kRows * h + tr, t = c < c_hi ? token[c] : -1;
+                if (t >= 0 && f8 < a.cols)
+                  y[16 / kRows * k + h].add_store(out8 + t * a.ldo, s, buf + (kRows * h + tr) * kPoolUpPitch + part * kElems);
+              }
+            }
+          }
+        } else {
+          for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+            float y[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int t = c0 + j < c_hi ? token[c0 + j] : -1;
+              y[j] = t >= 0 && f < a.cols ? pool_load(out + t * a.ldo) : 0.0f;
+            }
+            if (!ready) {
+              ready = true;
+              ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 1) & 1, sm.abort_flag));
+              if (!ok) break;
+              ptx::tc_fence_after();
+            }
+            uint32_t v[32];
+            ptx::tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128 + c0, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int t = c0 + j < c_hi ? token[c0 + j] : -1;
+              if (t >= 0 && f < a.cols) pool_store(out + t * a.ldo, fmaf(s, __uint_as_float(v[j]), y[j]));
+            }
           }
         }
         if (!ready && ok)  // no tokens in this half

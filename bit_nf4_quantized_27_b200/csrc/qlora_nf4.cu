@@ -1045,10 +1045,12 @@ qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const v
   a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
   a.tn = pool_up_tile(p.r, a.planes);
   const int64_t units = pool_most_tiles(p.M, p.n, a.tn) * ((cols + 127) / 128);
-  static std::once_flag flags[64];
-  static qlora_status results[64];
-  return launch_pool(pool_up_kernel<W_MN, O>, std::min<int64_t>(units, 2 * sms), 1, kPoolUpThreads, p.n, dev, flags, results,
-                     st, tmW, tmP, a);
+  const int64_t grid = std::min<int64_t>(units, 2 * sms);
+  static std::once_flag flags[2][64];
+  static qlora_status results[2][64];
+  const bool vec = aligned(Out, 16) && ldo * sizeof(O) % 16 == 0;
+  return vec ? launch_pool(pool_up_kernel<W_MN, O, true>, grid, 1, kPoolUpThreads, p.n, dev, flags[0], results[0], st, tmW, tmP, a)
+             : launch_pool(pool_up_kernel<W_MN, O, false>, grid, 1, kPoolUpThreads, p.n, dev, flags[1], results[1], st, tmW, tmP, a);
 }
 template <bool W_MN>
 qlora_status launch_pool_up(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo,
