@@ -140,6 +140,20 @@ __device__ __forceinline__ int4 pool_rows(const PoolArgs &p, int i, int last) {
   return y;
 }
 
+// Loads of token rows into a stage: 32 consecutive rows of memory come with one tiled load (box 64 x 32), other rows
+// four to a gather.  A gather costs the loading thread as much as a tiled load eight times its size (the down kernel
+// took 46 us to read 67 MB by gathers alone), and requests of a packed batch are runs of rows.
+// Whether the eight lanes from lane & ~7, with four rows each, hold 32 consecutive rows.  valid: rows of the tile; those
+// past it may be any rows where `loose` (at least half of the 32 must be wanted).
+__device__ __forceinline__ bool pool_run32(const int4 &y, int lane, int first, int valid, bool loose) {
+  const int base = __shfl_sync(0xffffffffu, y.x, lane & ~7) + 4 * (lane & 7), left = valid - first;
+  const bool seq = (y.x == base || left < 1) && (y.y == base + 1 || left < 2) && (y.z == base + 2 || left < 3) &&
+                   (y.w == base + 3 || left < 4);
+  const uint32_t all = __ballot_sync(0xffffffffu, seq);
+  const int wanted = valid - (first - 4 * (lane & 7));
+  return ((all >> (lane & ~7)) & 0xffu) == 0xffu && wanted >= (loose ? 16 : 32);
+}
+
 // pre[a] = tiles of tn tokens of the adapters before a, a = 0 .. n; returns pre[n].  The whole block.
 __device__ __forceinline__ int pool_scan(const PoolArgs &p, int tn, int *pre) {
   __shared__ int warp_sum[32];
@@ -282,6 +296,7 @@ struct PoolDownArgs {
 template <bool W_MN>
 __global__ void __launch_bounds__(kPoolDownThreads) pool_down_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                      const __grid_constant__ CUtensorMap tmV,
+                                                                     const __grid_constant__ CUtensorMap tmVt,
                                                                      const PoolDownArgs a) {
   extern __shared__ uint8_t pool_raw[];
   const PoolSmem sm = pool_smem(pool_raw);
@@ -310,10 +325,13 @@ __global__ void __launch_bounds__(kPoolDownThreads) pool_down_kernel(const __gri
     const int rw = min(128, p.r - rb * 128);
     const int kb = live > 0 ? min(q * k_per, a.k_steps) : 0, ke = live > 0 ? min(a.k_steps, kb + k_per) : 0;
     if (warp == 0) {
-      const int groups = (cnt + 3) / 4;
       const int4 rows = pool_rows(p, lo + 4 * lane, lo + cnt - 1);
+      const bool run = pool_run32(rows, lane, 4 * lane, cnt, true), tile_load = run && (lane & 7) == 0;
+      const bool gather = !run && 4 * lane < cnt;
       const int w_loads = W_MN ? (rw + 63) / 64 : 1;
-      const uint32_t bytes = (W_MN ? w_loads * 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u) + groups * 512u;
+      const uint32_t bytes = (W_MN ? w_loads * 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u) +
+                             __popc(__ballot_sync(0xffffffffu, tile_load)) * 4096u +
+                             __popc(__ballot_sync(0xffffffffu, gather)) * 512u;
       for (int ks = kb; ks < ke && ok; ++ks) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
         if (!ok) break;
@@ -326,7 +344,8 @@ __global__ void __launch_bounds__(kPoolDownThreads) pool_down_kernel(const __gri
             ptx::tma_load_3d(st, &tmW, &full[pos.s], ks * 64, rb * 128, ad);
         }
         __syncwarp();
-        if (lane < groups) ptx::tma_gather4(st + w_bytes + lane * 512, &tmV, &full[pos.s], ks * 64, rows);
+        if (tile_load) ptx::tma_load_2d(st + w_bytes + lane * 512, &tmVt, &full[pos.s], ks * 64, rows.x);
+        if (gather) ptx::tma_gather4(st + w_bytes + lane * 512, &tmV, &full[pos.s], ks * 64, rows);
         ++issued;
         pos.next(stages);
       }
@@ -482,6 +501,7 @@ struct PoolPiece<__nv_bfloat16> {
 template <bool W_MN, typename O, bool VEC>
 __global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                     const __grid_constant__ CUtensorMap tmP,
+                                                                    const __grid_constant__ CUtensorMap tmPt,
                                                                     const PoolUpArgs a) {
   extern __shared__ uint8_t pool_raw[];
   __shared__ int token[128];
@@ -517,18 +537,19 @@ __global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid
     }
     __syncthreads();
     if (warp == 0) {
-      const int groups = (cnt + 3) / 4;
       const int4 rows = pool_rows(p, lo + 4 * lane, lo + cnt - 1);
+      const bool run_32 = pool_run32(rows, lane, 4 * lane, cnt, true), tile_load = run_32 && (lane & 7) == 0;
+      const bool gather = !run_32 && 4 * lane < cnt;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, tile_load)) * 4096u + __popc(__ballot_sync(0xffffffffu, gather)) * 512u;
       if (ok) {
-        if (lane == 0) ptx::mbar_arrive_expect_tx(p_full, nch * a.planes * groups * 512u);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(p_full, nch * a.planes * bytes);
         __syncwarp();
-        if (lane < groups)
-          for (int ch = 0; ch < nch; ++ch)
-            for (int pl = 0; pl < a.planes; ++pl) {
-              const int o = pl * static_cast<int>(p.M);
-              ptx::tma_gather4(sm.ring + (ch * a.planes + pl) * plane_bytes + lane * 512, &tmP, p_full, ch * 64,
-                               make_int4(rows.x + o, rows.y + o, rows.z + o, rows.w + o));
-            }
+        for (int i = 0; i < nch * a.planes; ++i) {
+          const int o = i % a.planes * static_cast<int>(p.M), x = i / a.planes * 64;
+          uint8_t *d = sm.ring + i * plane_bytes + lane * 512;
+          if (tile_load) ptx::tma_load_2d(d, &tmPt, p_full, x, rows.x + o);
+          if (gather) ptx::tma_gather4(d, &tmP, p_full, x, make_int4(rows.x + o, rows.y + o, rows.z + o, rows.w + o));
+        }
         __syncwarp();
       }
       for (int b = b0; b < b1 && ok; ++b)
@@ -704,6 +725,10 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
                                                                      const __grid_constant__ CUtensorMap tmU,
                                                                      const __grid_constant__ CUtensorMap tmDY,
                                                                      const __grid_constant__ CUtensorMap tmT,
+                                                                     const __grid_constant__ CUtensorMap tmXt,
+                                                                     const __grid_constant__ CUtensorMap tmUt,
+                                                                     const __grid_constant__ CUtensorMap tmDYt,
+                                                                     const __grid_constant__ CUtensorMap tmTt,
                                                                      const PoolGradArgs a) {
   extern __shared__ uint8_t pool_raw[];
   const PoolSmem sm = pool_smem(pool_raw);
@@ -733,6 +758,7 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
     const int s_per = (steps + cs - 1) / cs, sb = min(q * s_per, steps), se = min(steps, sb + s_per);
     if (warp == 0) {
       const CUtensorMap *tmV = is_a ? &tmX : &tmDY, *tmP = is_a ? &tmU : &tmT;
+      const CUtensorMap *tmVt = is_a ? &tmXt : &tmDYt, *tmPt = is_a ? &tmUt : &tmTt;
       const int g = lane & 15;
       int4 rows = make_int4(0, 0, 0, 0);
       if (sb < se) rows = pool_rows(p, grp.x + sb * 64 + 4 * g, grp.y - 1);
@@ -741,15 +767,20 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
         if (!ok) break;
         uint8_t *d = sm.ring + pos.s * stage_bytes;
+        // a group of 32 that is not whole is gathered: rows of other adapters' tokens must not meet the padding
+        const bool run = pool_run32(rows, lane, 4 * g, cnt - st * 64, false), tile_load = run && (lane & 7) == 0;
+        const bool gather = !run && g < groups;
         if (lane == 0) ptx::mbar_arrive_expect_tx(&full[pos.s], groups * 512u * (2 + a.planes));
         __syncwarp();
-        if (g < groups) {
-          ptx::tma_gather4(d + (lane >> 4) * 8192 + g * 512, tmV, &full[pos.s], fb * 128 + (lane >> 4) * 64, rows);
-          for (int pl = lane >> 4; pl < a.planes; pl += 2) {
-            const int o = pl * static_cast<int>(p.M);
-            ptx::tma_gather4(d + 16384 + pl * 8192 + g * 512, tmP, &full[pos.s], rb * 64,
-                             make_int4(rows.x + o, rows.y + o, rows.z + o, rows.w + o));
-          }
+        uint8_t *dv = d + (lane >> 4) * 8192 + g * 512;
+        const int xv = fb * 128 + (lane >> 4) * 64;
+        if (tile_load) ptx::tma_load_2d(dv, tmVt, &full[pos.s], xv, rows.x);
+        if (gather) ptx::tma_gather4(dv, tmV, &full[pos.s], xv, rows);
+        for (int pl = lane >> 4; pl < a.planes; pl += 2) {
+          const int o = pl * static_cast<int>(p.M);
+          uint8_t *dp = d + 16384 + pl * 8192 + g * 512;
+          if (tile_load) ptx::tma_load_2d(dp, tmPt, &full[pos.s], rb * 64, rows.x + o);
+          if (gather) ptx::tma_gather4(dp, tmP, &full[pos.s], rb * 64, make_int4(rows.x + o, rows.y + o, rows.z + o, rows.w + o));
         }
         if (st + 1 < se) rows = pool_rows(p, grp.x + (st + 1) * 64 + 4 * g, grp.y - 1);
         __syncwarp();

@@ -969,9 +969,10 @@ bool tmap_pool(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Token rows to gather: [rows, inner] bf16 with row stride ld, one row a box.
-bool tmap_tokens(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, int64_t ld) {
-  return make_tmap(m, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, rows, ld, 64, 1, true);
+// Token rows [rows, inner] bf16 with row stride ld: one row a box to gather, and 32 for runs of rows.
+bool tmap_tokens(CUtensorMap *gather, CUtensorMap *tile, const void *ptr, int64_t inner, int64_t rows, int64_t ld) {
+  return make_tmap(gather, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, rows, ld, 64, 1, true) &&
+         make_tmap(tile, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, rows, ld, 64, 32, true);
 }
 
 // Launch of `clusters` clusters of `cs` CTAs, allowed to begin while the kernel ahead ends.
@@ -1009,9 +1010,9 @@ template <bool W_MN>
 qlora_status launch_pool_down(const PoolArgs &p, const void *V, int64_t ldv, const void *W, __nv_bfloat16 *P, int dev,
                               int sms, cudaStream_t st) {
   const int64_t len = W_MN ? p.N : p.K;
-  CUtensorMap tmW, tmV;
+  CUtensorMap tmW, tmV, tmVt;
   if (!(W_MN ? tmap_pool(&tmW, W, p.r, len, p.n, 64) : tmap_pool(&tmW, W, len, p.r, p.n, std::min(p.r, 128))) ||
-      !tmap_tokens(&tmV, V, len, p.M, ldv))
+      !tmap_tokens(&tmV, &tmVt, V, len, p.M, ldv))
     return QLORA_ERR_CUDA;
   PoolDownArgs a;
   a.p = p;
@@ -1025,7 +1026,8 @@ qlora_status launch_pool_down(const PoolArgs &p, const void *V, int64_t ldv, con
   const int64_t clusters = std::min<int64_t>(pool_most_tiles(p.M, p.n, kPoolDownTile) * nrb, target / cs);
   static std::once_flag flags[64];
   static qlora_status results[64];
-  return launch_pool(pool_down_kernel<W_MN>, clusters, cs, kPoolDownThreads, p.n, dev, flags, results, st, tmW, tmV, a);
+  return launch_pool(pool_down_kernel<W_MN>, clusters, cs, kPoolDownThreads, p.n, dev, flags, results, st, tmW, tmV, tmVt,
+                     a);
 }
 
 // Out[t] += s_a P[t] W_a for every grouped token.  Y: W = B; dX: W = A (MN-major).
@@ -1033,9 +1035,9 @@ template <bool W_MN, typename O>
 qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo, int dev,
                               int sms, cudaStream_t st) {
   const int64_t cols = W_MN ? p.K : p.N;
-  CUtensorMap tmW, tmP;
+  CUtensorMap tmW, tmP, tmPt;
   if (!(W_MN ? tmap_pool(&tmW, W, cols, p.r, p.n, 64) : tmap_pool(&tmW, W, p.r, cols, p.n, 128)) ||
-      !tmap_tokens(&tmP, P, p.r, kPoolPlanes * p.M, p.r))
+      !tmap_tokens(&tmP, &tmPt, P, p.r, kPoolPlanes * p.M, p.r))
     return QLORA_ERR_CUDA;
   PoolUpArgs a;
   a.p = p;
@@ -1049,8 +1051,10 @@ qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const v
   static std::once_flag flags[2][64];
   static qlora_status results[2][64];
   const bool vec = aligned(Out, 16) && ldo * sizeof(O) % 16 == 0;
-  return vec ? launch_pool(pool_up_kernel<W_MN, O, true>, grid, 1, kPoolUpThreads, p.n, dev, flags[0], results[0], st, tmW, tmP, a)
-             : launch_pool(pool_up_kernel<W_MN, O, false>, grid, 1, kPoolUpThreads, p.n, dev, flags[1], results[1], st, tmW, tmP, a);
+  return vec ? launch_pool(pool_up_kernel<W_MN, O, true>, grid, 1, kPoolUpThreads, p.n, dev, flags[0], results[0], st, tmW, tmP,
+                           tmPt, a)
+             : launch_pool(pool_up_kernel<W_MN, O, false>, grid, 1, kPoolUpThreads, p.n, dev, flags[1], results[1], st, tmW, tmP,
+                           tmPt, a);
 }
 template <bool W_MN>
 qlora_status launch_pool_up(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo,
@@ -1063,9 +1067,10 @@ template <typename O>
 qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const void *X, int64_t ldx,
                                const __nv_bfloat16 *T, const void *dY, int64_t lddy, void *dA, void *dB, int dev,
                                int sms, cudaStream_t st) {
-  CUtensorMap tmX{}, tmU{}, tmDY{}, tmT{};
-  if (p.M > 0 && (!tmap_tokens(&tmX, X, p.K, p.M, ldx) || !tmap_tokens(&tmU, U, p.r, kPoolPlanes * p.M, p.r) ||
-                  !tmap_tokens(&tmDY, dY, p.N, p.M, lddy) || !tmap_tokens(&tmT, T, p.r, kPoolPlanes * p.M, p.r)))
+  CUtensorMap tmX{}, tmU{}, tmDY{}, tmT{}, tmXt{}, tmUt{}, tmDYt{}, tmTt{};
+  if (p.M > 0 &&
+      (!tmap_tokens(&tmX, &tmXt, X, p.K, p.M, ldx) || !tmap_tokens(&tmU, &tmUt, U, p.r, kPoolPlanes * p.M, p.r) ||
+       !tmap_tokens(&tmDY, &tmDYt, dY, p.N, p.M, lddy) || !tmap_tokens(&tmT, &tmTt, T, p.r, kPoolPlanes * p.M, p.r)))
     return QLORA_ERR_CUDA;
   PoolGradArgs a;
   a.p = p;
@@ -1079,7 +1084,8 @@ qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const 
   const int64_t clusters = std::min<int64_t>(units, 2 * sms / cs);
   static std::once_flag flags[64];
   static qlora_status results[64];
-  return launch_pool(pool_grad_kernel<O>, clusters, cs, kPoolGradThreads, p.n, dev, flags, results, st, tmX, tmU, tmDY, tmT, a);
+  return launch_pool(pool_grad_kernel<O>, clusters, cs, kPoolGradThreads, p.n, dev, flags, results, st, tmX, tmU, tmDY, tmT,
+                     tmXt, tmUt, tmDYt, tmTt, a);
 }
 
 // The base products alone: Y = X W'^T, and dX = dY W'.
