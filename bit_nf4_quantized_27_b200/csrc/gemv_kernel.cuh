@@ -1135,7 +1135,9 @@ inline uint32_t dyn_smem_base(int dev) {
   return base[dev];
 }
 
-inline qlora_status launch_gemv(GemvArgs g, const CUtensorMap *tm_codes, int dev, int sms, cudaStream_t st) {
+// overlap: the kernel may start while the one ahead of it in the stream, which must itself have waited for X, ends.
+inline qlora_status launch_gemv(GemvArgs g, const CUtensorMap *tm_codes, int dev, int sms, cudaStream_t st,
+                                bool overlap = true) {
   const int num_rg = static_cast<int>((g.N + 15) / 16);
   bool bulk = tm_codes != nullptr && gemv_bulk_ok(g.N, g.K);
   const int cap = bulk ? kBulkMaxRG : kGemvMaxRG;
@@ -1177,7 +1179,7 @@ inline qlora_status launch_gemv(GemvArgs g, const CUtensorMap *tm_codes, int dev
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = overlap ? 1 : 0;
   cudaError_t e;
   if (bulk) {
     auto kernel = two ? nf4_gemv_bulk_kernel<2> : nf4_gemv_bulk_kernel<1>;

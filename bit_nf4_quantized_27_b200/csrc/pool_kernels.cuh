@@ -75,23 +75,22 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_groups_kernel(const int
 }
 
 // ---------------------------------------------------------------------------
-// The products.  Three kernels, all on the tensor cores (tcgen05, accumulators in
-// TMEM) with the adapters' matrices, or features, in the 128 rows of the
-// accumulator and tokens, or ranks, in its columns:
+// The products.  Two kernels, on the tensor cores (tcgen05, accumulators in TMEM) with
+// ranks, or features, in the 128 rows of the accumulator and tokens, or ranks, in its
+// columns:
 //
-//   down  P = V W_a over the long dimension: T = X A^T, U = dY B     [rank x token]
-//   up    Out += s_a P W_a over the rank: Y with B^T, dX with A      [feature x token]
-//   grad  s_a P^T V over the tokens of an adapter: dA, dB            [feature x rank]
+//   term  P = V W1_a over the long dimension, then Out += s_a P W2_a: T and Y in the
+//         forward, U and dX in the backward
+//   grad  s_a P^T V over the tokens of an adapter: dA, dB
 //
-// A tile holds tokens of one adapter, wherever their rows lie: one warp gathers them,
-// four rows to an instruction (TMA gather, 128-byte swizzle), and a short tile loads
-// only the rows it has.  Columns of the accumulator are independent, so a short
-// tile's unused columns need no zeros, and neither do rows past an adapter's rank.
-// How the tiles fall follows from offsets, which only the device knows: each CTA sums
-// the adapters' tile counts into shared memory first, and walks tiles from there.
+// A tile holds tokens of one adapter, wherever their rows lie: runs of 32 rows come
+// with one tiled load, others four rows to a gather, and a short tile loads only the
+// rows it has.  Columns of the accumulator are independent, so a short tile's unused
+// columns need no zeros, and neither do rows past an adapter's rank.  How the tiles
+// fall follows from offsets, which only the device knows: each CTA adds up the
+// adapters' tile counts first and walks the tiles from there.
 //
-// All three are bound by HBM at ranks up to about 128 (r flops a byte of X, dY, Y or
-// dX), so the loads run ahead in a ring of 64-column stages and two CTAs share an SM.
+// Both are bound by HBM at ranks up to about 128 (r flops a byte of X, dY, Y or dX).
 // ---------------------------------------------------------------------------
 // The intermediates T = X A^T and U = dY B are [M, r] in float32 and kept as three bf16 planes [3, M, r], each the rounding
 // of what the ones before leave: 24 bits together, in the type the tensor cores take beside bf16 operands.  A bf16 result
@@ -130,7 +129,7 @@ __device__ __forceinline__ int pool_token(const PoolArgs &p, int i) {
   return -1;
 }
 
-// The same for a gather, which needs some row in range: row 0 then, whose result is not written.
+// The same for a load of four rows, which needs some row in range: row 0 then, whose result is not written.
 __device__ __forceinline__ int4 pool_rows(const PoolArgs &p, int i, int last) {
   int4 y;
   y.x = max(pool_token(p, min(i, last)), 0);
@@ -141,8 +140,9 @@ __device__ __forceinline__ int4 pool_rows(const PoolArgs &p, int i, int last) {
 }
 
 // Loads of token rows into a stage: 32 consecutive rows of memory come with one tiled load (box 64 x 32), other rows
-// four to a gather.  A gather costs the loading thread as much as a tiled load eight times its size (the down kernel
-// took 46 us to read 67 MB by gathers alone), and requests of a packed batch are runs of rows.
+// four to a gather.  A gather costs the loading thread as much as a tiled load eight times its size (reading 67 MB by
+// gathers alone took 46 us), and requests of a packed batch are runs of rows.
+//
 // Whether the eight lanes from lane & ~7, with four rows each, hold 32 consecutive rows.  valid: rows of the tile; those
 // past it may be any rows where `loose` (at least half of the 32 must be wanted).
 __device__ __forceinline__ bool pool_run32(const int4 &y, int lane, int first, int valid, bool loose) {
@@ -152,46 +152,6 @@ __device__ __forceinline__ bool pool_run32(const int4 &y, int lane, int first, i
   const uint32_t all = __ballot_sync(0xffffffffu, seq);
   const int wanted = valid - (first - 4 * (lane & 7));
   return ((all >> (lane & ~7)) & 0xffu) == 0xffu && wanted >= (loose ? 16 : 32);
-}
-
-// pre[a] = tiles of tn tokens of the adapters before a, a = 0 .. n; returns pre[n].  The whole block.
-__device__ __forceinline__ int pool_scan(const PoolArgs &p, int tn, int *pre) {
-  __shared__ int warp_sum[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.n + blockDim.x - 1) / blockDim.x, a0 = tid * per, a1 = min(p.n, a0 + per);
-  int sum = 0;
-  for (int a = a0; a < a1; ++a) {
-    const int2 g = pool_group(p, a);
-    sum += (g.y - g.x + tn - 1) / tn;
-  }
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
-  int at = inc - sum;
-  for (int w = 0; w < warp; ++w) at += warp_sum[w];
-  for (int a = a0; a < a1; ++a) {
-    pre[a] = at;
-    const int2 g = pool_group(p, a);
-    at += (g.y - g.x + tn - 1) / tn;
-  }
-  if (tid == static_cast<int>(blockDim.x) - 1) pre[p.n] = at;
-  __syncthreads();
-  return pre[p.n];
-}
-
-// The adapter of a tile: the last one with pre[a] <= tile.
-__device__ __forceinline__ int pool_find(const int *pre, int n, int tile) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= tile) lo = mid; else hi = mid - 1;
-  }
-  return lo;
 }
 
 // Position in a ring of stages, with the phase of its barriers.
@@ -210,35 +170,32 @@ __device__ __forceinline__ void ring_drain(uint64_t *full, RingPos pos, uint32_t
   }
 }
 
-// Shared memory of one CTA: two share an SM's 227 KB, whatever the rank.
-constexpr uint32_t kPoolRingBytes = 98 * 1024;
-__host__ __device__ constexpr uint32_t pool_smem_bytes(int n) {
-  return 1024 + kPoolRingBytes + 512 + (static_cast<uint32_t>(n) + 1) * 4;
-}
+// Barriers and flags of a CTA, behind its buffers.
+constexpr uint32_t kPoolBars = 24, kPoolTailBytes = 512;
+constexpr uint32_t kPoolMostStages = 6;
 struct PoolSmem {
-  uint8_t *ring;      // 1024-byte aligned
-  uint64_t *bars;     // 24
+  uint8_t *buf;   // 1024-byte aligned, `bytes` of it
+  uint64_t *bars;
   uint32_t *tmem_slot;
   volatile int *abort_flag;
-  int *pre;           // [n + 1]
 };
-__device__ __forceinline__ PoolSmem pool_smem(uint8_t *raw) {
+__device__ __forceinline__ PoolSmem pool_smem(uint8_t *raw, uint32_t bytes) {
   PoolSmem s;
-  s.ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  s.bars = reinterpret_cast<uint64_t *>(s.ring + kPoolRingBytes);
-  s.tmem_slot = reinterpret_cast<uint32_t *>(s.bars + 24);
+  s.buf = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  s.bars = reinterpret_cast<uint64_t *>(s.buf + bytes);
+  s.tmem_slot = reinterpret_cast<uint32_t *>(s.bars + kPoolBars);
   s.abort_flag = reinterpret_cast<volatile int *>(s.tmem_slot + 1);
-  s.pre = reinterpret_cast<int *>(s.ring + kPoolRingBytes + 512);
   return s;
 }
+__host__ __device__ constexpr uint32_t pool_smem_bytes(uint32_t bytes) { return 1024 + bytes + kPoolTailBytes; }
 
-// Set-up that all three share: barriers (one arrival each, but `acc_empty`), TMEM, then the wait for the kernel ahead.  The
-// next kernel may start only after that wait: one that reads early, or that waits for this kernel alone, then finds
-// everything before this kernel complete too.
-__device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_cols, int acc_empty0, int acc_empty_count) {
+// Set-up of both kernels: barriers (one arrival each, but for the accumulators' two `empty` ones), TMEM, then the wait for
+// the kernel ahead.  The next kernel may start only after that wait: one that reads early, or that waits for this kernel
+// alone, then finds everything before this kernel complete too.
+__device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_cols, int acc_empty, int acc_empty_count) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 24; ++i)
-      ptx::mbar_init(&s.bars[i], acc_empty0 >= 0 && (i == acc_empty0 || i == acc_empty0 + 1) ? acc_empty_count : 1);
+    for (int i = 0; i < static_cast<int>(kPoolBars); ++i)
+      ptx::mbar_init(&s.bars[i], acc_empty >= 0 && (i == acc_empty || i == acc_empty + 1) ? acc_empty_count : 1);
     *s.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -275,191 +232,72 @@ __device__ __forceinline__ void pool_fail(const PoolSmem &s, uint32_t *status) {
 }
 
 // ---------------------------------------------------------------------------
-// down: one unit is 128 tokens x 128 ranks; the CTAs of a cluster each sum a part of
-// the long dimension, leave their float32 partial accumulators in shared memory, and
-// each then adds a share of the tokens over all of them, in CTA order, through
-// distributed shared memory: no partial planes in HBM, no second launch, and the same
-// bits every time.
-//   warp 0  loads; warp 1  products; warps 2..5  accumulator -> shared memory; all  the sum
-// W_MN false: W is [n][r][len] (K-major); true: [n][len][r] (MN-major).
+// term: a cluster takes a tile of 64 tokens (32 above rank 128).
+//
+// 1. Its CTAs each sum a part of the long dimension, with the accumulator's rows as ranks and its columns as
+//    tokens; the steps of 64 go round four accumulators, which keeps each one's chain of float32 additions
+//    short (the tensor cores' additions cut off: one chain over 1400 elements was 3e-6 off, all to one side).
+// 2. Each CTA leaves its float32 partial sums in shared memory; each then adds up a share of the tokens over
+//    the cluster, in CTA order, splits the sums into planes, and writes them into the shared memory of
+//    every CTA of the cluster (and to HBM, where the backward needs them).  No partial planes in HBM, no
+//    second launch, and the same bits every time.
+// 3. Each CTA takes every cs-th block of 128 features: W2's block by TMA, rows of the accumulator as
+//    features, then Out += s accumulator.  Two sets of four epilogue warps take turns, each with an
+//    accumulator of its own: while one set stores a block, the other's block is loaded and multiplied.
+//    The lanes hold features; where Out's rows are 16-byte aligned, 16 tokens at a time pass through
+//    shared memory, so that four lanes (bf16; eight for float32) then share a token's 32 features in
+//    16-byte pieces, loaded before the accumulator is waited for (element by element the epilogue took 47
+//    instructions an element and warp, and bound the kernel on issue).  Other outputs, odd strides or
+//    columns of a wider tensor, go element by element.
+//
+//   warp 0  loads; warp 1  products; warps 2..9  accumulators -> shared memory, epilogue; all  the sums
+// W_MN false (forward): W1 = A [n][r][len], W2 = B [n][cols][r], both K-major; true (backward): W1 = B
+// [n][len][r], W2 = A [n][r][cols], both MN-major.
 // ---------------------------------------------------------------------------
-constexpr int kPoolDownThreads = 192;
-constexpr int kPoolDownTile = 128;
-constexpr uint32_t kPoolDownTmem = 128;
-
-struct PoolDownArgs {
-  PoolArgs p;
-  int k_steps;  // of 64
-  __nv_bfloat16 *P;
-};
-
-template <bool W_MN>
-__global__ void __launch_bounds__(kPoolDownThreads) pool_down_kernel(const __grid_constant__ CUtensorMap tmW,
-                                                                     const __grid_constant__ CUtensorMap tmV,
-                                                                     const __grid_constant__ CUtensorMap tmVt,
-                                                                     const PoolDownArgs a) {
-  extern __shared__ uint8_t pool_raw[];
-  const PoolSmem sm = pool_smem(pool_raw);
-  const PoolArgs &p = a.p;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // a stage: W's rows (64 of them when r <= 64; the accumulator's upper rows then multiply what follows in
-  // memory and are not read), then 128 token rows
-  const uint32_t w_bytes = p.r <= 64 ? 8192u : 16384u, stage_bytes = w_bytes + 16384u, stages = kPoolRingBytes / stage_bytes;
-  uint64_t *full = sm.bars, *empty = sm.bars + 4, *acc_full = sm.bars + 8;
-  const uint32_t tmem = pool_setup(sm, kPoolDownTmem, -1, 1);
-  const int tiles = pool_scan(p, kPoolDownTile, sm.pre);
-  const int nrb = (p.r + 127) / 128;
-  const int64_t units = static_cast<int64_t>(tiles) * nrb;
-  const int cs = static_cast<int>(ptx::cluster_nctarank()), q = static_cast<int>(ptx::cluster_ctarank());
-  const int k_per = (a.k_steps + cs - 1) / cs;
-  float *exch = reinterpret_cast<float *>(sm.ring);
-  RingPos pos;
-  uint32_t acc_phase = 0, issued = 0;
-  bool ok = true;
-  for (int64_t u = blockIdx.x / cs; u < units; u += gridDim.x / cs) {
-    const int tile = static_cast<int>(u / nrb), rb = static_cast<int>(u - static_cast<int64_t>(tile) * nrb);
-    const int ad = pool_find(sm.pre, p.n, tile);
-    const int2 grp = pool_group(p, ad);
-    const int lo = grp.x + (tile - sm.pre[ad]) * kPoolDownTile, cnt = min(kPoolDownTile, grp.y - lo);
-    const int live = pool_rank(p, ad) - rb * 128;  // ranks of this block that exist
-    const int rw = min(128, p.r - rb * 128);
-    const int kb = live > 0 ? min(q * k_per, a.k_steps) : 0, ke = live > 0 ? min(a.k_steps, kb + k_per) : 0;
-    if (warp == 0) {
-      const int4 rows = pool_rows(p, lo + 4 * lane, lo + cnt - 1);
-      const bool run = pool_run32(rows, lane, 4 * lane, cnt, true), tile_load = run && (lane & 7) == 0;
-      const bool gather = !run && 4 * lane < cnt;
-      const int w_loads = W_MN ? (rw + 63) / 64 : 1;
-      const uint32_t bytes = (W_MN ? w_loads * 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u) +
-                             __popc(__ballot_sync(0xffffffffu, tile_load)) * 4096u +
-                             __popc(__ballot_sync(0xffffffffu, gather)) * 512u;
-      for (int ks = kb; ks < ke && ok; ++ks) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
-        if (!ok) break;
-        uint8_t *st = sm.ring + pos.s * stage_bytes;
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&full[pos.s], bytes);
-          if (W_MN)
-            for (int i = 0; i < w_loads; ++i) ptx::tma_load_3d(st + i * 8192, &tmW, &full[pos.s], rb * 128 + i * 64, ks * 64, ad);
-          else
-            ptx::tma_load_3d(st, &tmW, &full[pos.s], ks * 64, rb * 128, ad);
-        }
-        __syncwarp();
-        if (tile_load) ptx::tma_load_2d(st + w_bytes + lane * 512, &tmVt, &full[pos.s], ks * 64, rows.x);
-        if (gather) ptx::tma_gather4(st + w_bytes + lane * 512, &tmV, &full[pos.s], ks * 64, rows);
-        ++issued;
-        pos.next(stages);
-      }
-      if (!ok && lane == 0) pool_fail(sm, p.status);
-    } else if (warp == 1) {
-      const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, W_MN ? 1 : 0, 0);
-      for (int ks = kb; ks < ke && ok; ++ks) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (lane == 0) {
-          const uint32_t w = ptx::smem_addr(sm.ring + pos.s * stage_bytes), v = w + w_bytes;
-#pragma unroll
-          for (int k16 = 0; k16 < 4; ++k16)
-            ptx::mma_bf16(tmem, W_MN ? ptx::smem_desc_sw128(w + k16 * 2048, 8192, 1024) : ptx::smem_desc_sw128(w + k16 * 32, 16, 1024),
-                          ptx::smem_desc_sw128(v + k16 * 32, 16, 1024), idesc, (ks != kb || k16) ? 1u : 0u);
-          ptx::mma_commit(&empty[pos.s]);
-        }
-        __syncwarp();
-        pos.next(stages);
-      }
-      if (ok && ke > kb && lane == 0) ptx::mma_commit(acc_full);
-      if (!ok && lane == 0) pool_fail(sm, p.status);
-      __syncwarp();
-    } else {
-      const int quad = warp & 3;
-      if (ke > kb && ok) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_full, acc_phase, sm.abort_flag));
-        acc_phase ^= 1;
-        if (!ok && lane == 0) pool_fail(sm, p.status);
-      }
-      ptx::tc_fence_after();
-      if (quad * 32 < rw)
-        for (int c0 = 0; c0 < cnt; c0 += 32) {
-          uint32_t v[32];
-          if (ke > kb && ok) {
-            ptx::tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0, v);
-            ptx::tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0u;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c0 + j < cnt) exch[(c0 + j) * 128 + quad * 32 + lane] = __uint_as_float(v[j]);
-        }
-      ptx::tc_fence_before();
-    }
-    pool_cluster_sync();
-    // this CTA's share of the tokens
-    const int per = (cnt + cs - 1) / cs, c_lo = min(cnt, q * per), c_hi = min(cnt, c_lo + per), half = rw / 2;
-    const uint32_t exch_addr = ptx::smem_addr(exch);
-    for (int e = threadIdx.x; e < (c_hi - c_lo) * half; e += kPoolDownThreads) {
-      const int c = c_lo + e / half, j = 2 * (e % half);
-      float2 s = make_float2(0.0f, 0.0f);
-      for (int r = 0; r < cs; ++r) {
-        const float2 v = ptx::ld_cluster_f32x2(ptx::mapa_shared(exch_addr + (c * 128 + j) * 4, r));
-        s.x += v.x;
-        s.y += v.y;
-      }
-      if (j >= live) s = make_float2(0.0f, 0.0f);  // a multiple of 8, so both
-      const int t = pool_token(p, lo + c);
-      if (t < 0) continue;
-      __nv_bfloat16 *out = a.P + static_cast<int64_t>(t) * p.r + rb * 128 + j;
-#pragma unroll
-      for (int pl = 0; pl < kPoolPlanes; ++pl) {
-        const uint32_t h = pack_bf16x2(s.x, s.y);
-        *reinterpret_cast<uint32_t *>(out + pl * p.M * p.r) = h;
-        s.x -= bf16lo_to_f32(h);
-        s.y -= bf16hi_to_f32(h);
-      }
-    }
-    ptx::fence_proxy_async_smem();  // the next unit's loads overwrite what was read and written here
-    pool_cluster_sync();
-  }
-  if (warp == 0 && lane == 0 && *sm.abort_flag) ring_drain(full, pos, stages, issued);
-  pool_teardown(tmem, kPoolDownTmem);
-}
-
-// ---------------------------------------------------------------------------
-// up: one unit is a tile of tokens and a run of 128-feature blocks.  P's rows of the tile
-// are loaded once, the blocks of W stream through the ring, and the accumulator of one
-// block is computed while the one before is added to Out.  A warp of the epilogue takes 32
-// features x half of the tile's tokens.  Its lanes hold features; where Out's rows are
-// 16-byte aligned, 16 tokens at a time pass through shared memory, so that four lanes (bf16;
-// eight for float32) then share a token's 32 features in 16-byte pieces, all loaded before the accumulator is waited
-// for (64 KB in flight on an SM; element by element the epilogue took 47 instructions an
-// element and warp and bound the kernel on issue).  Other outputs, odd strides or columns of a
-// wider tensor, go element by element.
-//   warp 0  loads; warp 1  products; warps 2..9  Out += s_a accumulator
-// W_MN false: W is [n][cols][r] (Y: B); true: [n][r][cols] (dX: A).
-// ---------------------------------------------------------------------------
-constexpr int kPoolUpThreads = 320;
-constexpr uint32_t kPoolUpTmem = 256;  // two accumulators of up to 128 tokens
-
-struct PoolUpArgs {
-  PoolArgs p;
-  int64_t cols, ldo;
-  void *out;
-  int planes;
-  int tn;  // tokens a tile: 128, 64 or 32
-};
-
-// Tokens of an up tile: as many as keep P's planes within 48 KB, which leaves the ring two stages or more.
-constexpr uint32_t kPoolUpPlaneBytes = 48 * 1024, kPoolUpRingBytes = 80 * 1024;
-__host__ __device__ constexpr int pool_up_tile(int r, int planes) {
-  const uint32_t row = (r + 63) / 64 * planes * 128u;
-  return row * 128 <= kPoolUpPlaneBytes ? 128 : row * 64 <= kPoolUpPlaneBytes ? 64 : 32;
-}
-static_assert(pool_up_tile(256, 3) == 32 && 4 * 3 * 32 * 128 <= kPoolUpPlaneBytes, "the largest rank fits");
+constexpr int kPoolTermThreads = 320;
+constexpr uint32_t kPoolTermTmem = 256;
 // Shared memory of a warp's 16 tokens x 32 features: a pitch of 36 floats keeps 16-byte pieces aligned and both
 // directions without bank conflicts.
-constexpr int kPoolUpPitch = 36, kPoolUpBuf = 16 * kPoolUpPitch;
-static_assert(kPoolUpRingBytes + 8 * kPoolUpBuf * 4 <= kPoolRingBytes, "shared memory");
+constexpr int kPoolPitch = 36, kPoolWarpBuf = 16 * kPoolPitch;
+
+// Sizes that follow from the rank and the planes: two CTAs share an SM up to rank 64.
+struct PoolTermLayout {
+  int tn;               // tokens a tile
+  int rpad;             // floats a token of the partial sums
+  uint32_t stage;       // bytes
+  uint32_t stages;
+  uint32_t plane;       // bytes of one 64-rank chunk of one plane
+  uint32_t planes_at, exch_at, bytes;
+};
+__host__ __device__ constexpr PoolTermLayout pool_term_layout(int r, int planes) {
+  PoolTermLayout l{};
+  l.tn = r <= 128 ? 64 : 32;
+  l.rpad = r <= 64 ? 64 : r <= 128 ? 128 : 256;
+  l.stage = l.tn * 128u + l.rpad * 128u;  // token rows and W1's; 16 KB at least, which a block of W2 takes
+  l.plane = l.tn * 128u;
+  const uint32_t budget = (r <= 64 ? 107u : 218u) * 1024u, p_bytes = (r + 63) / 64 * planes * l.plane;
+  const uint32_t exch = l.tn * l.rpad * 4u > 8 * kPoolWarpBuf * 4u ? l.tn * l.rpad * 4u : 8 * kPoolWarpBuf * 4u;
+  const uint32_t fit = (budget - p_bytes - exch) / l.stage;
+  l.stages = fit < kPoolMostStages ? fit : kPoolMostStages;
+  l.planes_at = l.stages * l.stage;
+  l.exch_at = l.planes_at + p_bytes;
+  l.bytes = l.exch_at + exch;
+  return l;
+}
+static_assert(pool_term_layout(64, 3).stages >= 3 && pool_term_layout(128, 3).stages >= 3 && pool_term_layout(256, 3).stages >= 3,
+              "a ring of three stages at least");
+static_assert(pool_smem_bytes(pool_term_layout(64, 2).bytes) + 1024 <= 113 * 1024 && pool_smem_bytes(pool_term_layout(256, 3).bytes) <= 226 * 1024,
+              "shared memory");
+
+struct PoolTermArgs {
+  PoolArgs p;
+  int64_t len;         // columns of V
+  int64_t cols, ldo;   // of Out
+  void *out;           // nullable: P alone
+  __nv_bfloat16 *P;    // nullable [3, M, r]
+  int planes;          // used for Out
+  PoolTermLayout l;
+};
 
 __device__ __forceinline__ float pool_load(const float *p) { return __ldcg(p); }
 __device__ __forceinline__ float pool_load(const __nv_bfloat16 *p) {
@@ -498,100 +336,262 @@ struct PoolPiece<__nv_bfloat16> {
   }
 };
 
+// What the CTA's threads hold of the adapters (QLORA_MAX_ADAPTERS over 320 threads: four each) and of the tile at hand.
+constexpr int kPoolPerThread = (QLORA_MAX_ADAPTERS + kPoolTermThreads - 1) / kPoolTermThreads;
+struct PoolTile {
+  int ad, lo, cnt, rank;
+  float scale;
+};
+
 template <bool W_MN, typename O, bool VEC>
-__global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid_constant__ CUtensorMap tmW,
-                                                                    const __grid_constant__ CUtensorMap tmP,
-                                                                    const __grid_constant__ CUtensorMap tmPt,
-                                                                    const PoolUpArgs a) {
+__global__ void __launch_bounds__(kPoolTermThreads, 2)
+    pool_term_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmW2,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVt, const PoolTermArgs a) {
   extern __shared__ uint8_t pool_raw[];
-  __shared__ int token[128];
-  const PoolSmem sm = pool_smem(pool_raw);
+  __shared__ int token[64];
+  __shared__ int warp_sum[kPoolTermThreads / 32];
+  __shared__ PoolTile tile_s;
   const PoolArgs &p = a.p;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tn = a.tn;
-  const uint32_t plane_bytes = tn * 128u, p_bytes = (p.r + 63) / 64 * a.planes * plane_bytes;
-  const uint32_t stages = min((kPoolUpRingBytes - p_bytes) / 16384u, 4u);
-  uint8_t *ring = sm.ring + p_bytes;
-  uint64_t *full = sm.bars, *empty = sm.bars + 4, *acc_full = sm.bars + 8, *acc_empty = sm.bars + 10, *p_full = sm.bars + 12;
-  const uint32_t tmem = pool_setup(sm, kPoolUpTmem, 10, 8);
-  const int tiles = pool_scan(p, tn, sm.pre);
-  const int nblk = static_cast<int>((a.cols + 127) / 128);
-  // runs of blocks: as many as give every CTA a unit
-  int runs = min(max(static_cast<int>(gridDim.x) / max(tiles, 1), 1), nblk);
-  const int run = (nblk + runs - 1) / runs;
-  runs = (nblk + run - 1) / run;
-  const int64_t units = static_cast<int64_t>(tiles) * runs;
+  const PoolTermLayout &l = a.l;
+  const PoolSmem sm = pool_smem(pool_raw, l.bytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tn = l.tn;
+  const uint32_t stages = l.stages, v_bytes = tn * 128u;
+  uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
+  uint64_t *acc_full = sum_full + 1, *acc_empty = acc_full + 2;
+  float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
+  uint8_t *planes = sm.buf + l.planes_at;
+  if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &tmW1 : tid == 1 ? &tmW2 : tid == 2 ? &tmV : &tmVt);
+  const uint32_t tmem = pool_setup(sm, kPoolTermTmem, 2 * kPoolMostStages + 3, 4);
+
+  // the adapters' first tiles, this thread's in registers
+  int first[kPoolPerThread], lo_of[kPoolPerThread], hi_of[kPoolPerThread];
+  const int per = (p.n + kPoolTermThreads - 1) / kPoolTermThreads;
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPoolPerThread; ++i) {
+    const int ad = tid * per + i;
+    const bool in = i < per && ad < p.n;
+    const int2 g = in ? pool_group(p, ad) : make_int2(0, 0);
+    lo_of[i] = g.x;
+    hi_of[i] = g.y;
+    first[i] = sum;
+    sum += (g.y - g.x + tn - 1) / tn;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int before = inc - sum, tiles = 0;
+#pragma unroll
+  for (int w = 0; w < kPoolTermThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    tiles += warp_sum[w];
+  }
+
+  const int cs = static_cast<int>(ptx::cluster_nctarank()), q = static_cast<int>(ptx::cluster_ctarank());
+  const int k_steps = static_cast<int>((a.len + 63) / 64), k_per = (k_steps + cs - 1) / cs;
+  const int nblk = a.out ? static_cast<int>((a.cols + 127) / 128) : 0;
+  const int nrb = (p.r + 127) / 128, acc_cols = tn * nrb;  // one of the four accumulators of the sums
   RingPos pos;
-  uint32_t p_phase = 0, issued = 0, blocks = 0;  // blocks: accumulators used so far
+  uint32_t sum_phase = 0, issued = 0, blocks = 0;  // blocks: accumulators of features used so far
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int tile = static_cast<int>(u / runs), b0 = static_cast<int>(u - static_cast<int64_t>(tile) * runs) * run;
-    const int b1 = min(nblk, b0 + run);
-    const int ad = pool_find(sm.pre, p.n, tile);
-    const int2 grp = pool_group(p, ad);
-    const int lo = grp.x + (tile - sm.pre[ad]) * tn, cnt = min(tn, grp.y - lo);
-    const int rank = pool_rank(p, ad), nch = (rank + 63) / 64;
-    if (rank == 0) continue;
-    if (warp >= 2) {
-      const int i = threadIdx.x - 64;
-      if (i < 128) token[i] = i < cnt ? pool_token(p, lo + i) : -1;
+  for (int tile = blockIdx.x / cs; tile < tiles; tile += gridDim.x / cs) {
+#pragma unroll
+    for (int i = 0; i < kPoolPerThread; ++i) {
+      const int t = tile - before - first[i];
+      const int lo = lo_of[i] + t * tn;
+      if (t >= 0 && lo < hi_of[i]) {
+        const int ad = tid * per + i;
+        tile_s.ad = ad;
+        tile_s.lo = lo;
+        tile_s.cnt = min(tn, hi_of[i] - lo);
+        tile_s.rank = pool_rank(p, ad);
+        tile_s.scale = p.scales[ad];
+      }
     }
     __syncthreads();
-    if (warp == 0) {
-      const int4 rows = pool_rows(p, lo + 4 * lane, lo + cnt - 1);
-      const bool run_32 = pool_run32(rows, lane, 4 * lane, cnt, true), tile_load = run_32 && (lane & 7) == 0;
-      const bool gather = !run_32 && 4 * lane < cnt;
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, tile_load)) * 4096u + __popc(__ballot_sync(0xffffffffu, gather)) * 512u;
-      if (ok) {
-        if (lane == 0) ptx::mbar_arrive_expect_tx(p_full, nch * a.planes * bytes);
-        __syncwarp();
-        for (int i = 0; i < nch * a.planes; ++i) {
-          const int o = i % a.planes * static_cast<int>(p.M), x = i / a.planes * 64;
-          uint8_t *d = sm.ring + i * plane_bytes + lane * 512;
-          if (tile_load) ptx::tma_load_2d(d, &tmPt, p_full, x, rows.x + o);
-          if (gather) ptx::tma_gather4(d, &tmP, p_full, x, make_int4(rows.x + o, rows.y + o, rows.z + o, rows.w + o));
-        }
-        __syncwarp();
-      }
-      for (int b = b0; b < b1 && ok; ++b)
-        for (int ch = 0; ch < nch && ok; ++ch) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
-          if (!ok) break;
-          if (lane == 0) {
-            uint8_t *st = ring + pos.s * 16384u;
-            ptx::mbar_arrive_expect_tx(&full[pos.s], 16384u);
-            if (W_MN) {
-              ptx::tma_load_3d(st, &tmW, &full[pos.s], b * 128, ch * 64, ad);
-              ptx::tma_load_3d(st + 8192, &tmW, &full[pos.s], b * 128 + 64, ch * 64, ad);
-            } else {
-              ptx::tma_load_3d(st, &tmW, &full[pos.s], ch * 64, b * 128, ad);
-            }
+    const int ad = tile_s.ad, lo = tile_s.lo, cnt = tile_s.cnt, rank = tile_s.rank;
+    const int kb = rank > 0 ? min(q * k_per, k_steps) : 0, ke = rank > 0 ? min(k_steps, kb + k_per) : 0;
+    const int nch = rank > 0 ? (rank + 63) / 64 : 0;
+    const int mine = rank > 0 && nblk > q ? (nblk - q + cs - 1) / cs : 0;  // blocks q, q + cs, ...
+    const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, W_MN ? 1 : 0, 0);
+    const int quad = warp & 3, set = (warp - 2) >> 2;
+
+    // warp 0: stages [i0, i1) of W2's blocks, 64 ranks of a block each
+    auto load_w2 = [&](int i0, int i1) {
+      for (int i = i0; i < i1 && ok; ++i) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
+        if (!ok) break;
+        if (lane == 0) {
+          const int f = (q + i / nch * cs) * 128, x = i % nch * 64;
+          uint8_t *st = sm.buf + pos.s * l.stage;
+          ptx::mbar_arrive_expect_tx(&full[pos.s], 16384u);
+          if (W_MN) {
+            ptx::tma_load_3d(st, &tmW2, &full[pos.s], f, x, ad);
+            ptx::tma_load_3d(st + 8192, &tmW2, &full[pos.s], f + 64, x, ad);
+          } else {
+            ptx::tma_load_3d(st, &tmW2, &full[pos.s], x, f, ad);
           }
-          __syncwarp();
-          ++issued;
-          pos.next(stages);
         }
+        __syncwarp();
+        ++issued;
+        pos.next(stages);
+      }
       if (!ok && lane == 0) pool_fail(sm, p.status);
+    };
+
+    // ------------------------------------------------------------ 1. the sums over the long dimension
+    if (warp == 0) {
+      const int4 rows = pool_rows(p, lo + 4 * min(lane, tn / 4 - 1), lo + cnt - 1);
+      const bool mine4 = 4 * lane < cnt;
+      const bool run = pool_run32(rows, lane, 4 * lane, cnt, true), tile_load = run && (lane & 7) == 0 && mine4;
+      const bool gather = !run && mine4;
+      // W1's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
+      const int w_loads = W_MN ? (p.r + 63) / 64 : nrb;
+      const uint32_t w_box = W_MN ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u;
+      const uint32_t bytes = w_loads * w_box + __popc(__ballot_sync(0xffffffffu, tile_load)) * 4096u +
+                             __popc(__ballot_sync(0xffffffffu, gather)) * 512u;
+      for (int ks = kb; ks < ke && ok; ++ks) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
+        if (!ok) break;
+        uint8_t *st = sm.buf + pos.s * l.stage;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&full[pos.s], bytes);
+          for (int i = 0; i < w_loads; ++i)
+            ptx::tma_load_3d(st + v_bytes + i * (W_MN ? 8192 : 16384), &tmW1, &full[pos.s], W_MN ? i * 64 : ks * 64,
+                             W_MN ? ks * 64 : i * 128, ad);
+        }
+        __syncwarp();
+        if (tile_load) ptx::tma_load_2d(st + lane * 512, &tmVt, &full[pos.s], ks * 64, rows.x);
+        if (gather) ptx::tma_gather4(st + lane * 512, &tmV, &full[pos.s], ks * 64, rows);
+        __syncwarp();
+        ++issued;
+        pos.next(stages);
+      }
+      if (!ok && lane == 0) pool_fail(sm, p.status);
+      // the first of W2's blocks follow through the ring while the sums are joined
+      load_w2(0, min(mine * nch, static_cast<int>(stages)));
     } else if (warp == 1) {
-      const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, W_MN ? 1 : 0, 0);
-      const uint32_t p_addr = ptx::smem_addr(sm.ring);
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(p_full, p_phase, sm.abort_flag));
-      uint32_t n = blocks;
-      for (int b = b0; b < b1 && ok; ++b, ++n) {
-        const uint32_t acc = n & 1;
+      for (int ks = kb; ks < ke && ok; ++ks) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (lane == 0) {
+          const uint32_t v = ptx::smem_addr(sm.buf + pos.s * l.stage), w = v + v_bytes, d = tmem + ((ks - kb) & 3) * acc_cols;
+#pragma unroll
+          for (int k16 = 0; k16 < 4; ++k16)
+            for (int rb = 0; rb < nrb; ++rb)
+              ptx::mma_bf16(d + rb * tn,
+                            W_MN ? ptx::smem_desc_sw128(w + rb * 16384 + k16 * 2048, 8192, 1024)
+                                 : ptx::smem_desc_sw128(w + rb * 16384 + k16 * 32, 16, 1024),
+                            ptx::smem_desc_sw128(v + k16 * 32, 16, 1024), idesc, (ks - kb >= 4 || k16) ? 1u : 0u);
+          ptx::mma_commit(&empty[pos.s]);
+        }
+        __syncwarp();
+        pos.next(stages);
+      }
+      if (ok && ke > kb && lane == 0) ptx::mma_commit(sum_full);
+      if (!ok && lane == 0) pool_fail(sm, p.status);
+      __syncwarp();
+    } else {
+      if (tid - 64 < tn) token[tid - 64] = tid - 64 < cnt ? pool_token(p, lo + tid - 64) : -1;
+      if (ke > kb && ok) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(sum_full, sum_phase, sm.abort_flag));
+        sum_phase ^= 1;
+        if (!ok && lane == 0) pool_fail(sm, p.status);
+      }
+      ptx::tc_fence_after();
+      const int nacc = ok ? min(4, ke - kb) : 0, c_end = min(cnt, (set + 1) * (tn / 2));
+      for (int rb = 0; rb < nrb; ++rb) {
+        if (rb * 128 + quad * 32 >= p.r) break;
+        for (int c0 = set * (tn / 2); c0 < c_end; c0 += 16) {
+          float x[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+          for (int i = 0; i < nacc; ++i) {
+            uint32_t v[16];
+            ptx::tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + i * acc_cols + rb * tn + c0, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c0 + j < c_end) exch[(c0 + j) * l.rpad + rb * 128 + quad * 32 + lane] = x[j];
+        }
+      }
+      ptx::tc_fence_before();
+    }
+
+    // ------------------------------------------------------------ 2. the sums over the cluster
+    pool_cluster_sync();
+    {
+      const int pt = (cnt + cs - 1) / cs, c_lo = min(cnt, q * pt), c_hi = min(cnt, c_lo + pt);
+      const int n8 = (p.r + 15) / 16 * 2;  // groups of 8 ranks; products take 16 at a time
+      const uint32_t exch_addr = ptx::smem_addr(exch), planes_addr = ptx::smem_addr(planes);
+      for (int e = tid; e < (c_hi - c_lo) * n8; e += kPoolTermThreads) {
+        const int c = c_lo + e / n8, j = e % n8 * 8;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+        if (j < rank) {
+          const uint32_t src = exch_addr + (c * l.rpad + j) * 4;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < cs) {
+              const uint32_t from = ptx::mapa_shared(src, r);
+              const float4 u = ptx::ld_cluster_f32x4(from), w = ptx::ld_cluster_f32x4(from + 16);
+              x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+              x[4] += w.x; x[5] += w.y; x[6] += w.z; x[7] += w.w;
+            }
+        }
+        const int t = a.P ? pool_token(p, lo + c) : -1;
+        const uint32_t dst = planes_addr + (j >> 6) * a.planes * l.plane + c * 128 + ((((j >> 3) & 7) ^ (c & 7)) << 4);
+#pragma unroll
+        for (int pl = 0; pl < kPoolPlanes; ++pl) {
+          uint4 h;
+          h.x = pack_bf16x2(x[0], x[1]);
+          h.y = pack_bf16x2(x[2], x[3]);
+          h.z = pack_bf16x2(x[4], x[5]);
+          h.w = pack_bf16x2(x[6], x[7]);
+          x[0] -= bf16lo_to_f32(h.x); x[1] -= bf16hi_to_f32(h.x);
+          x[2] -= bf16lo_to_f32(h.y); x[3] -= bf16hi_to_f32(h.y);
+          x[4] -= bf16lo_to_f32(h.z); x[5] -= bf16hi_to_f32(h.z);
+          x[6] -= bf16lo_to_f32(h.w); x[7] -= bf16hi_to_f32(h.w);
+          if (t >= 0 && j < p.r)
+            *reinterpret_cast<uint4 *>(a.P + (static_cast<int64_t>(pl) * p.M + t) * p.r + j) = h;
+          if (a.out && pl < a.planes)
+            for (int r = 0; r < cs; ++r) ptx::st_cluster_u32x4(ptx::mapa_shared(dst + pl * l.plane, r), h);
+        }
+      }
+    }
+    ptx::fence_proxy_async_all();  // the planes are read by the tensor cores
+    pool_cluster_sync();
+
+    // ------------------------------------------------------------ 3. the features
+    if (warp == 0) {
+      load_w2(min(mine * nch, static_cast<int>(stages)), mine * nch);
+    } else if (warp == 1) {
+      ptx::fence_proxy_async_all();
+      const uint32_t p_addr = ptx::smem_addr(planes);
+      for (int b = 0; b < mine && ok; ++b) {
+        const uint32_t n = blocks + b, acc = n & 1;
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_empty[acc], ((n >> 1) & 1) ^ 1, sm.abort_flag));
         for (int ch = 0; ch < nch && ok; ++ch) {
           ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
           if (!ok) break;
-          uint8_t *st = ring + pos.s * 16384u;
+          uint8_t *st = sm.buf + pos.s * l.stage;
           const int left = min(64, rank - ch * 64);  // a multiple of 8
           if ((left & 8) && rank < p.r) {
             // products go 16 ranks at a time: the 8 past the adapter's rank meet zeros in P and have to be finite
-            if (W_MN) {
-              for (int i = lane; i < 128; i += 32)
-                *reinterpret_cast<uint4 *>(st + (i >> 6) * 8192 + (left + ((i >> 3) & 7)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-            } else {
-              for (int i = lane; i < 128; i += 32)
-                *reinterpret_cast<uint4 *>(st + i * 128 + (((left >> 3) ^ (i & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+            for (int i = lane; i < 128; i += 32) {
+              const int at = W_MN ? (i >> 6) * 8192 + (left + ((i >> 3) & 7)) * 128 + (i & 7) * 16
+                                  : i * 128 + (((left >> 3) ^ (i & 7)) << 4);
+              *reinterpret_cast<uint4 *>(st + at) = make_uint4(0u, 0u, 0u, 0u);
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid
               for (int pl = 0; pl < a.planes; ++pl)
                 ptx::mma_bf16(tmem + acc * 128,
                               W_MN ? ptx::smem_desc_sw128(w + k16 * 2048, 8192, 1024) : ptx::smem_desc_sw128(w + k16 * 32, 16, 1024),
-                              ptx::smem_desc_sw128(p_addr + (ch * a.planes + pl) * plane_bytes + k16 * 32, 16, 1024), idesc,
+                              ptx::smem_desc_sw128(p_addr + (ch * a.planes + pl) * l.plane + k16 * 32, 16, 1024), idesc,
                               (ch || k16 || pl) ? 1u : 0u);
             ptx::mma_commit(&empty[pos.s]);
           }
@@ -615,94 +615,83 @@ __global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid
       }
       if (!ok && lane == 0) pool_fail(sm, p.status);
     } else {
-      const int quad = warp & 3, half = (warp - 2) >> 2;
-      const int c_lo = half * (tn / 2), c_hi = min(cnt, c_lo + tn / 2);
-      const float s = p.scales[ad];
-      uint32_t n = blocks;
-      for (int b = b0; b < b1 && ok; ++b, ++n) {
-        const uint32_t acc = n & 1;
-        const int64_t f = static_cast<int64_t>(b) * 128 + quad * 32 + lane;
-        O *out = static_cast<O *>(a.out) + f;
+      const float s = tile_s.scale;
+      float *buf = exch + (warp - 2) * kPoolWarpBuf;
+      for (int b = (set ^ blocks) & 1; b < mine && ok; b += 2) {  // the blocks whose accumulator is this set's
+        const uint32_t n = blocks + b, acc = set;
+        const int64_t f0 = static_cast<int64_t>(q + b * cs) * 128 + quad * 32;
         bool ready = false;
+        auto wait = [&]() {
+          ready = true;
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 1) & 1, sm.abort_flag));
+          ptx::tc_fence_after();
+          return ok;
+        };
+        const uint32_t d = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128;
         if (VEC) {
-          float *buf = reinterpret_cast<float *>(sm.ring + kPoolUpRingBytes) + (warp - 2) * kPoolUpBuf;
           constexpr int kGroup = PoolPiece<O>::kTokens, kElems = PoolPiece<O>::kElems, kLanes = 32 / kElems, kRows = 32 / kLanes;
           const int tr = lane / kLanes, part = lane % kLanes;
-          const int64_t f8 = static_cast<int64_t>(b) * 128 + quad * 32 + part * kElems;
-          O *out8 = static_cast<O *>(a.out) + f8;
-          for (int g0 = c_lo; g0 < c_hi; g0 += kGroup) {
+          const bool in = f0 + part * kElems < a.cols;
+          O *out = static_cast<O *>(a.out) + f0 + part * kElems;
+          for (int g0 = 0; g0 < cnt; g0 += kGroup) {
             PoolPiece<O> y[kGroup / kRows];
 #pragma unroll
             for (int i = 0; i < kGroup / kRows; ++i) {
-              const int c = g0 + kRows * i + tr, t = c < c_hi ? token[c] : -1;
-              if (t >= 0 && f8 < a.cols) y[i].load(out8 + t * a.ldo);
+              const int c = g0 + kRows * i + tr, t = c < cnt ? token[c] : -1;
+              if (t >= 0 && in) y[i].load(out + t * a.ldo);
               else y[i].zero();
             }
-            if (!ready) {
-              ready = true;
-              ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 1) & 1, sm.abort_flag));
-              if (!ok) break;
-              ptx::tc_fence_after();
-            }
+            if (!ready && !wait()) break;
 #pragma unroll
             for (int k = 0; k < kGroup / 16; ++k) {
-              if (g0 + 16 * k >= c_hi) break;
+              if (g0 + 16 * k >= cnt) break;
               uint32_t v[16];
-              ptx::tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128 + g0 + 16 * k, v);
+              ptx::tmem_ld16(d + g0 + 16 * k, v);
               ptx::tmem_ld_wait();
               __syncwarp();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) buf[j * kPoolUpPitch + lane] = __uint_as_float(v[j]);
+              for (int j = 0; j < 16; ++j) buf[j * kPoolPitch + lane] = __uint_as_float(v[j]);
               __syncwarp();
 #pragma unroll
               for (int h = 0; h < 16 / kRows; ++h) {
-                const int c = g0 + 16 * k + kRows * h + tr, t = c < c_hi ? token[c] : -1;
-                if (t >= 0 && f8 < a.cols)
-                  y[16 / kRows * k + h].add_store(out8 + t * a.ldo, s, buf + (kRows * h + tr) * kPoolUpPitch + part * kElems);
+                const int c = g0 + 16 * k + kRows * h + tr, t = c < cnt ? token[c] : -1;
+                if (t >= 0 && in)
+                  y[16 / kRows * k + h].add_store(out + t * a.ldo, s, buf + (kRows * h + tr) * kPoolPitch + part * kElems);
               }
             }
           }
         } else {
-          for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-            float y[32];
+          const bool in = f0 + lane < a.cols;
+          O *out = static_cast<O *>(a.out) + f0 + lane;
+          for (int c0 = 0; c0 < cnt; c0 += 16) {
+            float y[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int t = c0 + j < c_hi ? token[c0 + j] : -1;
-              y[j] = t >= 0 && f < a.cols ? pool_load(out + t * a.ldo) : 0.0f;
+            for (int j = 0; j < 16; ++j) {
+              const int t = c0 + j < cnt ? token[c0 + j] : -1;
+              y[j] = t >= 0 && in ? pool_load(out + t * a.ldo) : 0.0f;
             }
-            if (!ready) {
-              ready = true;
-              ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 1) & 1, sm.abort_flag));
-              if (!ok) break;
-              ptx::tc_fence_after();
-            }
-            uint32_t v[32];
-            ptx::tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128 + c0, v);
+            if (!ready && !wait()) break;
+            uint32_t v[16];
+            ptx::tmem_ld16(d + c0, v);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int t = c0 + j < c_hi ? token[c0 + j] : -1;
-              if (t >= 0 && f < a.cols) pool_store(out + t * a.ldo, fmaf(s, __uint_as_float(v[j]), y[j]));
+            for (int j = 0; j < 16; ++j) {
+              const int t = c0 + j < cnt ? token[c0 + j] : -1;
+              if (t >= 0 && in) pool_store(out + t * a.ldo, fmaf(s, __uint_as_float(v[j]), y[j]));
             }
           }
         }
-        if (!ready && ok)  // no tokens in this half
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 1) & 1, sm.abort_flag));
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&acc_empty[acc]);
       }
       if (!ok && lane == 0) pool_fail(sm, p.status);
     }
-    p_phase ^= 1;
-    blocks += b1 - b0;
-    __syncthreads();  // the tile's rows of P and its tokens are done with
+    blocks += mine;
+    __syncthreads();  // the tile's tokens, planes and buffers are done with
   }
-  if (warp == 0 && lane == 0 && *sm.abort_flag) {
-    ring_drain(full, pos, stages, issued);
-    ptx::mbar_wait(p_full, p_phase ^ 1, nullptr);
-  }
-  pool_teardown(tmem, kPoolUpTmem);
+  if (warp == 0 && lane == 0 && *sm.abort_flag) ring_drain(full, pos, stages, issued);
+  pool_teardown(tmem, kPoolTermTmem);
 }
 
 // ---------------------------------------------------------------------------
@@ -713,6 +702,7 @@ __global__ void __launch_bounds__(kPoolUpThreads, 2) pool_up_kernel(const __grid
 // ---------------------------------------------------------------------------
 constexpr int kPoolGradThreads = 192;
 constexpr uint32_t kPoolGradTmem = 64;
+constexpr uint32_t kPoolGradBytes = 98 * 1024;  // two CTAs share an SM
 
 struct PoolGradArgs {
   PoolArgs p;
@@ -731,17 +721,17 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
                                                                      const __grid_constant__ CUtensorMap tmTt,
                                                                      const PoolGradArgs a) {
   extern __shared__ uint8_t pool_raw[];
-  const PoolSmem sm = pool_smem(pool_raw);
+  const PoolSmem sm = pool_smem(pool_raw, kPoolGradBytes);
   const PoolArgs &p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t stage_bytes = 16384u + a.planes * 8192u, stages = min(kPoolRingBytes / stage_bytes, 4u);
-  uint64_t *full = sm.bars, *empty = sm.bars + 4, *acc_full = sm.bars + 8;
+  const uint32_t stage_bytes = 16384u + a.planes * 8192u, stages = min(kPoolGradBytes / stage_bytes, kPoolMostStages);
+  uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *acc_full = sm.bars + 2 * kPoolMostStages;
   const uint32_t tmem = pool_setup(sm, kPoolGradTmem, -1, 1);
   const int nrb = (p.r + 63) / 64;
   const int in_a = static_cast<int>((p.K + 127) / 128) * nrb, per_adapter = in_a + static_cast<int>((p.N + 127) / 128) * nrb;
   const int64_t units = static_cast<int64_t>(p.n) * per_adapter;
   const int cs = static_cast<int>(ptx::cluster_nctarank()), q = static_cast<int>(ptx::cluster_ctarank());
-  float *exch = reinterpret_cast<float *>(sm.ring);
+  float *exch = reinterpret_cast<float *>(sm.buf);
   RingPos pos;
   uint32_t acc_phase = 0, issued = 0;
   bool ok = true;
@@ -766,7 +756,7 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
         const int groups = (min(64, cnt - st * 64) + 15) / 16 * 4;  // whole steps of 16 tokens
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
         if (!ok) break;
-        uint8_t *d = sm.ring + pos.s * stage_bytes;
+        uint8_t *d = sm.buf + pos.s * stage_bytes;
         // a group of 32 that is not whole is gathered: rows of other adapters' tokens must not meet the padding
         const bool run = pool_run32(rows, lane, 4 * g, cnt - st * 64, false), tile_load = run && (lane & 7) == 0;
         const bool gather = !run && g < groups;
@@ -793,7 +783,7 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
       for (int st = sb; st < se && ok; ++st) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
         if (!ok) break;
-        uint8_t *d = sm.ring + pos.s * stage_bytes;
+        uint8_t *d = sm.buf + pos.s * stage_bytes;
         const int valid = min(64, cnt - st * 64);
         if (valid & 15) {
           // the last 16 tokens are not all there: zero rows of P meet repeated rows of V

@@ -936,7 +936,7 @@ qlora_status check_pool_call(const qlora_adapter_pool *pool, const int32_t *orde
 }
 
 size_t pool_ws_bytes(int64_t M, int32_t r, int for_backward) {
-  return QLORA_STATUS_BYTES + (for_backward ? 2 : 1) * align256(static_cast<size_t>(kPoolPlanes) * M * r * 2);
+  return QLORA_STATUS_BYTES + (for_backward ? 2 * align256(static_cast<size_t>(kPoolPlanes) * M * r * 2) : 0);
 }
 
 PoolArgs pool_args(const qlora_adapter_pool *p, const int32_t *order, const int32_t *offsets, int64_t M, int64_t N,
@@ -977,14 +977,14 @@ bool tmap_tokens(CUtensorMap *gather, CUtensorMap *tile, const void *ptr, int64_
 
 // Launch of `clusters` clusters of `cs` CTAs, allowed to begin while the kernel ahead ends.
 template <typename... KArgs, typename... Args>
-qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int threads, int n, int dev, std::once_flag *flags,
-                         qlora_status *results, cudaStream_t st, Args &&...args) {
-  const qlora_status s = set_smem(kernel, static_cast<int>(pool_smem_bytes(QLORA_MAX_ADAPTERS)), dev, flags, results);
+qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int threads, uint32_t bytes, uint32_t most_bytes,
+                         int dev, std::once_flag *flags, qlora_status *results, cudaStream_t st, Args &&...args) {
+  const qlora_status s = set_smem(kernel, static_cast<int>(pool_smem_bytes(most_bytes)), dev, flags, results);
   if (s != QLORA_OK) return s;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * cs));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = pool_smem_bytes(n);
+  cfg.dynamicSmemBytes = pool_smem_bytes(bytes);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1002,65 +1002,45 @@ qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int
   return QLORA_OK;
 }
 
-// Most tiles of tn tokens that M tokens of n adapters can make.
-int64_t pool_most_tiles(int64_t M, int n, int tn) { return M / tn + std::min<int64_t>(n, M); }
-
-// P = V W_a for every grouped token.  T: V = X, W = A; U: V = dY, W = B (MN-major).
-template <bool W_MN>
-qlora_status launch_pool_down(const PoolArgs &p, const void *V, int64_t ldv, const void *W, __nv_bfloat16 *P, int dev,
-                              int sms, cudaStream_t st) {
-  const int64_t len = W_MN ? p.N : p.K;
-  CUtensorMap tmW, tmV, tmVt;
-  if (!(W_MN ? tmap_pool(&tmW, W, p.r, len, p.n, 64) : tmap_pool(&tmW, W, len, p.r, p.n, std::min(p.r, 128))) ||
-      !tmap_tokens(&tmV, &tmVt, V, len, p.M, ldv))
-    return QLORA_ERR_CUDA;
-  PoolDownArgs a;
-  a.p = p;
-  a.k_steps = static_cast<int>((len + 63) / 64);
-  a.P = P;
-  // split the long dimension while the tiles that full groups make would leave CTAs idle (two to an SM)
-  const int nrb = (p.r + 127) / 128, target = 2 * sms;
-  const int64_t tiles = (p.M + kPoolDownTile - 1) / kPoolDownTile * nrb;
-  int cs = 8;
-  while (cs > 1 && (tiles * cs > target || cs * 2 > a.k_steps)) cs /= 2;
-  const int64_t clusters = std::min<int64_t>(pool_most_tiles(p.M, p.n, kPoolDownTile) * nrb, target / cs);
-  static std::once_flag flags[64];
-  static qlora_status results[64];
-  return launch_pool(pool_down_kernel<W_MN>, clusters, cs, kPoolDownThreads, p.n, dev, flags, results, st, tmW, tmV, tmVt,
-                     a);
-}
-
-// Out[t] += s_a P[t] W_a for every grouped token.  Y: W = B; dX: W = A (MN-major).
+// P = V W1_a for every grouped token, then, with Out, Out[t] += s_a P[t] W2_a.  Forward (W_MN false): V = X, W1 = A,
+// W2 = B, Out = Y; backward: V = dY, W1 = B, W2 = A, Out = dX.  P: nullable [3, M, r] in HBM.
 template <bool W_MN, typename O>
-qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo, int dev,
-                              int sms, cudaStream_t st) {
-  const int64_t cols = W_MN ? p.K : p.N;
-  CUtensorMap tmW, tmP, tmPt;
-  if (!(W_MN ? tmap_pool(&tmW, W, cols, p.r, p.n, 64) : tmap_pool(&tmW, W, p.r, cols, p.n, 128)) ||
-      !tmap_tokens(&tmP, &tmPt, P, p.r, kPoolPlanes * p.M, p.r))
-    return QLORA_ERR_CUDA;
-  PoolUpArgs a;
+qlora_status launch_pool_term_t(const PoolArgs &p, const qlora_adapter_pool *pool, const void *V, int64_t ldv, __nv_bfloat16 *P,
+                                void *Out, int64_t ldo, int dev, int sms, cudaStream_t st) {
+  PoolTermArgs a;
   a.p = p;
-  a.cols = cols;
+  a.len = W_MN ? p.N : p.K;
+  a.cols = W_MN ? p.K : p.N;
   a.ldo = ldo;
   a.out = Out;
+  a.P = P;
   a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
-  a.tn = pool_up_tile(p.r, a.planes);
-  const int64_t units = pool_most_tiles(p.M, p.n, a.tn) * ((cols + 127) / 128);
-  const int64_t grid = std::min<int64_t>(units, 2 * sms);
+  a.l = pool_term_layout(p.r, a.planes);
+  CUtensorMap tmW1, tmW2, tmV, tmVt;
+  if (!(W_MN ? tmap_pool(&tmW1, pool->B, p.r, p.N, p.n, 64) : tmap_pool(&tmW1, pool->A, p.K, p.r, p.n, std::min(p.r, 128))) ||
+      !(W_MN ? tmap_pool(&tmW2, pool->A, p.K, p.r, p.n, 64) : tmap_pool(&tmW2, pool->B, p.r, p.N, p.n, 128)) ||
+      !tmap_tokens(&tmV, &tmVt, V, a.len, p.M, ldv))
+    return QLORA_ERR_CUDA;
+  // as many CTAs a tile as give the SMs what they hold, by the tiles that full groups make (more are walked in turn)
+  const int resident = (p.r <= 64 ? 2 : 1) * sms;
+  const int64_t tiles = (p.M + a.l.tn - 1) / a.l.tn, most = p.M / a.l.tn + std::min<int64_t>(p.n, p.M);
+  int cs = 8;
+  while (cs > 1 && tiles * cs > resident) cs /= 2;
+  const int64_t clusters = std::min<int64_t>(most, resident / cs);
+  const uint32_t most_bytes = 218 * 1024;
   static std::once_flag flags[2][64];
   static qlora_status results[2][64];
   const bool vec = aligned(Out, 16) && ldo * sizeof(O) % 16 == 0;
-  return vec ? launch_pool(pool_up_kernel<W_MN, O, true>, grid, 1, kPoolUpThreads, p.n, dev, flags[0], results[0], st, tmW, tmP,
-                           tmPt, a)
-             : launch_pool(pool_up_kernel<W_MN, O, false>, grid, 1, kPoolUpThreads, p.n, dev, flags[1], results[1], st, tmW, tmP,
-                           tmPt, a);
+  return vec ? launch_pool(pool_term_kernel<W_MN, O, true>, clusters, cs, kPoolTermThreads, a.l.bytes, most_bytes, dev, flags[0],
+                           results[0], st, tmW1, tmW2, tmV, tmVt, a)
+             : launch_pool(pool_term_kernel<W_MN, O, false>, clusters, cs, kPoolTermThreads, a.l.bytes, most_bytes, dev, flags[1],
+                           results[1], st, tmW1, tmW2, tmV, tmVt, a);
 }
 template <bool W_MN>
-qlora_status launch_pool_up(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo,
-                            qlora_dtype dt, int dev, int sms, cudaStream_t st) {
-  return dt == QLORA_F32 ? launch_pool_up_t<W_MN, float>(p, P, W, Out, ldo, dev, sms, st)
-                         : launch_pool_up_t<W_MN, __nv_bfloat16>(p, P, W, Out, ldo, dev, sms, st);
+qlora_status launch_pool_term(const PoolArgs &p, const qlora_adapter_pool *pool, const void *V, int64_t ldv, __nv_bfloat16 *P,
+                              void *Out, int64_t ldo, qlora_dtype dt, int dev, int sms, cudaStream_t st) {
+  return dt == QLORA_F32 ? launch_pool_term_t<W_MN, float>(p, pool, V, ldv, P, Out, ldo, dev, sms, st)
+                         : launch_pool_term_t<W_MN, __nv_bfloat16>(p, pool, V, ldv, P, Out, ldo, dev, sms, st);
 }
 
 template <typename O>
@@ -1084,8 +1064,8 @@ qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const 
   const int64_t clusters = std::min<int64_t>(units, 2 * sms / cs);
   static std::once_flag flags[64];
   static qlora_status results[64];
-  return launch_pool(pool_grad_kernel<O>, clusters, cs, kPoolGradThreads, p.n, dev, flags, results, st, tmX, tmU, tmDY, tmT,
-                     tmXt, tmUt, tmDYt, tmTt, a);
+  return launch_pool(pool_grad_kernel<O>, clusters, cs, kPoolGradThreads, kPoolGradBytes, kPoolGradBytes, dev, flags, results, st,
+                     tmX, tmU, tmDY, tmT, tmXt, tmUt, tmDYt, tmTt, a);
 }
 
 // The base products alone: Y = X W'^T, and dX = dY W'.
@@ -1103,7 +1083,8 @@ qlora_status base_fwd(const qlora_nf4_tensor *W, const void *X, int64_t M, void 
     g.y_f32 = y_dtype == QLORA_F32;
     g.status = status_ptr(ws);
     g.multi = 2;  // no adapter term
-    const qlora_status s = launch_gemv(g, &tmc, dev, sms, st);
+    // this kernel reads X before it waits for the kernel ahead of it, so it starts only when that one, which may be X's, is done
+    const qlora_status s = launch_gemv(g, &tmc, dev, sms, st, false);
     if (s != QLORA_ERR_UNSUPPORTED_SHAPE) return s;
   }
   CUtensorMap tmX, tmCodes, tmCodesPair;
@@ -1166,12 +1147,11 @@ qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, cons
                       void *T_save, void *ws, int dev, int sms, cudaStream_t st, const qlora_nf4_tensor *W = nullptr) {
   if (M == 0) return QLORA_OK;
   const PoolArgs a = pool_args(pool, order, offsets, M, N, K, ws);
-  __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
-  qlora_status s = launch_pool_down<false>(a, X, ldx, pool->A, T, dev, sms, st);
-  // The base product comes between T and the adapters' term: its decode kernel reads X before it waits for the
-  // kernel ahead of it, which is right only behind one that has itself waited for X, as T has.
-  if (s == QLORA_OK && W) s = base_fwd(W, X, M, Y, y_dtype, ws, dev, sms, st);
-  return s != QLORA_OK ? s : launch_pool_up<false>(a, T, pool->B, Y, ldy, y_dtype, dev, sms, st);
+  if (W) {
+    const qlora_status s = base_fwd(W, X, M, Y, y_dtype, ws, dev, sms, st);
+    if (s != QLORA_OK) return s;
+  }
+  return launch_pool_term<false>(a, pool, X, ldx, static_cast<__nv_bfloat16 *>(T_save), Y, ldy, y_dtype, dev, sms, st);
 }
 
 qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
@@ -1183,11 +1163,12 @@ qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, cons
   const __nv_bfloat16 *T = static_cast<const __nv_bfloat16 *>(T_saved);
   qlora_status s;
   if (M > 0) {
-    if ((s = launch_pool_down<true>(a, dY, lddy, pool->B, U, dev, sms, st)) != QLORA_OK) return s;
-    if (dX && (s = launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, dev, sms, st)) != QLORA_OK) return s;
+    if ((dX || dA) &&
+        (s = launch_pool_term<true>(a, pool, dY, lddy, dA ? U : nullptr, dX, lddx, dx_dtype, dev, sms, st)) != QLORA_OK)
+      return s;
     if (dA && !T) {
       __nv_bfloat16 *Tw = U + align256(static_cast<size_t>(kPoolPlanes) * M * a.r * 2) / 2;
-      if ((s = launch_pool_down<false>(a, X, ldx, pool->A, Tw, dev, sms, st)) != QLORA_OK) return s;
+      if ((s = launch_pool_term<false>(a, pool, X, ldx, Tw, nullptr, 0, QLORA_F32, dev, sms, st)) != QLORA_OK) return s;
       T = Tw;
     }
   }
