@@ -171,8 +171,7 @@ __device__ __forceinline__ void ring_drain(uint64_t *full, RingPos pos, uint32_t
 }
 
 // Barriers and flags of a CTA, behind its buffers.
-constexpr uint32_t kPoolBars = 24, kPoolTailBytes = 512;
-constexpr uint32_t kPoolMostStages = 6;
+constexpr uint32_t kPoolMostStages = 12, kPoolBars = 2 * kPoolMostStages + 8, kPoolTailBytes = 512;
 struct PoolSmem {
   uint8_t *buf;   // 1024-byte aligned, `bytes` of it
   uint64_t *bars;
@@ -232,16 +231,17 @@ __device__ __forceinline__ void pool_fail(const PoolSmem &s, uint32_t *status) {
 }
 
 // ---------------------------------------------------------------------------
-// term: a cluster takes a tile of 64 tokens (32 above rank 128).
+// term: g CTAs of a cluster take a tile of 64 tokens (32 above rank 128); g, at most the cluster, follows on the device from
+// the number of tiles.
 //
 // 1. Its CTAs each sum a part of the long dimension, with the accumulator's rows as ranks and its columns as
 //    tokens; the steps of 64 go round four accumulators, which keeps each one's chain of float32 additions
 //    short (the tensor cores' additions cut off: one chain over 1400 elements was 3e-6 off, all to one side).
 // 2. Each CTA leaves its float32 partial sums in shared memory; each then adds up a share of the tokens over
-//    the cluster, in CTA order, splits the sums into planes, and writes them into the shared memory of
-//    every CTA of the cluster (and to HBM, where the backward needs them).  No partial planes in HBM, no
+//    the g CTAs, in CTA order, splits the sums into planes, and writes them into the shared memory of
+//    every CTA of the tile (and to HBM, where the backward needs them).  No partial planes in HBM, no
 //    second launch, and the same bits every time.
-// 3. Each CTA takes every cs-th block of 128 features: W2's block by TMA, rows of the accumulator as
+// 3. Each CTA takes every g-th block of 128 features: W2's block by TMA, rows of the accumulator as
 //    features, then Out += s accumulator.  Two sets of four epilogue warps take turns, each with an
 //    accumulator of its own: while one set stores a block, the other's block is loaded and multiplied.
 //    The lanes hold features; where Out's rows are 16-byte aligned, 16 tokens at a time pass through
@@ -260,7 +260,9 @@ constexpr uint32_t kPoolTermTmem = 256;
 // directions without bank conflicts.
 constexpr int kPoolPitch = 36, kPoolWarpBuf = 16 * kPoolPitch;
 
-// Sizes that follow from the rank and the planes: two CTAs share an SM up to rank 64.
+// Sizes that follow from the rank and the planes.  Two CTAs share an SM up to rank 64, unless the call is `roomy`: too
+// small to give every SM one, so that a deeper ring is worth more.  `narrow`: 32 tokens a tile rather than 64, for calls
+// whose tiles of 64 would leave half of the CTAs that fit without work.
 struct PoolTermLayout {
   int tn;               // tokens a tile
   int rpad;             // floats a token of the partial sums
@@ -269,13 +271,14 @@ struct PoolTermLayout {
   uint32_t plane;       // bytes of one 64-rank chunk of one plane
   uint32_t planes_at, exch_at, bytes;
 };
-__host__ __device__ constexpr PoolTermLayout pool_term_layout(int r, int planes) {
+__host__ __device__ constexpr PoolTermLayout pool_term_layout(int r, int planes, bool roomy, bool narrow) {
   PoolTermLayout l{};
-  l.tn = r <= 128 ? 64 : 32;
+  l.tn = r <= 128 && !narrow ? 64 : 32;
   l.rpad = r <= 64 ? 64 : r <= 128 ? 128 : 256;
-  l.stage = l.tn * 128u + l.rpad * 128u;  // token rows and W1's; 16 KB at least, which a block of W2 takes
+  l.stage = l.tn * 128u + l.rpad * 128u;  // token rows and W1's
+  if (l.stage < 16384u) l.stage = 16384u;  // a block of W2
   l.plane = l.tn * 128u;
-  const uint32_t budget = (r <= 64 ? 107u : 218u) * 1024u, p_bytes = (r + 63) / 64 * planes * l.plane;
+  const uint32_t budget = (r <= 64 && !roomy ? 107u : 218u) * 1024u, p_bytes = (r + 63) / 64 * planes * l.plane;
   const uint32_t exch = l.tn * l.rpad * 4u > 8 * kPoolWarpBuf * 4u ? l.tn * l.rpad * 4u : 8 * kPoolWarpBuf * 4u;
   const uint32_t fit = (budget - p_bytes - exch) / l.stage;
   l.stages = fit < kPoolMostStages ? fit : kPoolMostStages;
@@ -284,9 +287,11 @@ __host__ __device__ constexpr PoolTermLayout pool_term_layout(int r, int planes)
   l.bytes = l.exch_at + exch;
   return l;
 }
-static_assert(pool_term_layout(64, 3).stages >= 3 && pool_term_layout(128, 3).stages >= 3 && pool_term_layout(256, 3).stages >= 3,
+static_assert(pool_term_layout(64, 3, false, false).stages >= 3 && pool_term_layout(128, 3, false, false).stages >= 3 &&
+                  pool_term_layout(256, 3, false, false).stages >= 3,
               "a ring of three stages at least");
-static_assert(pool_smem_bytes(pool_term_layout(64, 2).bytes) + 1024 <= 113 * 1024 && pool_smem_bytes(pool_term_layout(256, 3).bytes) <= 226 * 1024,
+static_assert(pool_smem_bytes(pool_term_layout(64, 3, false, false).bytes) + 2048 <= 114 * 1024 &&
+                  pool_smem_bytes(pool_term_layout(256, 3, false, false).bytes) <= 225 * 1024,
               "shared memory");
 
 struct PoolTermArgs {
@@ -307,37 +312,36 @@ __device__ __forceinline__ void pool_store(float *p, float v) { *p = v; }
 __device__ __forceinline__ void pool_store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // 16 bytes of Out: y + s v, rounded once.  kElems elements; a row's 32 features take 32 / kElems lanes, so that each
-// instruction covers whole sectors.  kTokens: loaded ahead by a warp, 4 KB.
+// instruction covers whole sectors.  kTokens: one item of a warp, 2 KB; two are in flight.
 template <typename O>
 struct PoolPiece;
 template <>
 struct PoolPiece<float> {
-  static constexpr int kElems = 4, kTokens = 32;
+  static constexpr int kElems = 4, kTokens = 16;
   float4 y;
-  __device__ __forceinline__ void zero() { y = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
   __device__ __forceinline__ void load(const float *p) { y = __ldcg(reinterpret_cast<const float4 *>(p)); }
-  __device__ __forceinline__ void add_store(float *p, float s, const float *v) const {
+  __device__ __forceinline__ void add(float s, const float *v) {
     const float4 u = *reinterpret_cast<const float4 *>(v);
-    *reinterpret_cast<float4 *>(p) = make_float4(fmaf(s, u.x, y.x), fmaf(s, u.y, y.y), fmaf(s, u.z, y.z), fmaf(s, u.w, y.w));
+    y = make_float4(fmaf(s, u.x, y.x), fmaf(s, u.y, y.y), fmaf(s, u.z, y.z), fmaf(s, u.w, y.w));
   }
+  __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = y; }
 };
 template <>
 struct PoolPiece<__nv_bfloat16> {
-  static constexpr int kElems = 8, kTokens = 64;
+  static constexpr int kElems = 8, kTokens = 32;
   uint4 y;
-  __device__ __forceinline__ void zero() { y = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) { y = __ldcg(reinterpret_cast<const uint4 *>(p)); }
-  __device__ __forceinline__ void add_store(__nv_bfloat16 *p, float s, const float *v) const {
+  __device__ __forceinline__ void add(float s, const float *v) {
     const float4 u = reinterpret_cast<const float4 *>(v)[0], w = reinterpret_cast<const float4 *>(v)[1];
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(fmaf(s, u.x, bf16lo_to_f32(y.x)), fmaf(s, u.y, bf16hi_to_f32(y.x))),
-                                               pack_bf16x2(fmaf(s, u.z, bf16lo_to_f32(y.y)), fmaf(s, u.w, bf16hi_to_f32(y.y))),
-                                               pack_bf16x2(fmaf(s, w.x, bf16lo_to_f32(y.z)), fmaf(s, w.y, bf16hi_to_f32(y.z))),
-                                               pack_bf16x2(fmaf(s, w.z, bf16lo_to_f32(y.w)), fmaf(s, w.w, bf16hi_to_f32(y.w))));
+    y.x = pack_bf16x2(fmaf(s, u.x, bf16lo_to_f32(y.x)), fmaf(s, u.y, bf16hi_to_f32(y.x)));
+    y.y = pack_bf16x2(fmaf(s, u.z, bf16lo_to_f32(y.y)), fmaf(s, u.w, bf16hi_to_f32(y.y)));
+    y.z = pack_bf16x2(fmaf(s, w.x, bf16lo_to_f32(y.z)), fmaf(s, w.y, bf16hi_to_f32(y.z)));
+    y.w = pack_bf16x2(fmaf(s, w.z, bf16lo_to_f32(y.w)), fmaf(s, w.w, bf16hi_to_f32(y.w)));
   }
+  __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = y; }
 };
 
-// What the CTA's threads hold of the adapters (QLORA_MAX_ADAPTERS over 320 threads: four each) and of the tile at hand.
-constexpr int kPoolPerThread = (QLORA_MAX_ADAPTERS + kPoolTermThreads - 1) / kPoolTermThreads;
+// The tile at hand.
 struct PoolTile {
   int ad, lo, cnt, rank;
   float scale;
@@ -348,9 +352,15 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
     pool_term_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmW2,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVt, const PoolTermArgs a) {
   extern __shared__ uint8_t pool_raw[];
-  __shared__ int token[64];
+  __shared__ int64_t row_at[64];  // of the tile's tokens in Out, in elements; -1: not a token
+  __shared__ int4 row4[16];
   __shared__ int warp_sum[kPoolTermThreads / 32];
   __shared__ PoolTile tile_s;
+  // descriptor words (128-byte swizzle, groups of eight rows 1024 bytes apart): the high one is the same for all operands,
+  // the low one is the address and the distance of 64-element blocks, which MN-major operands use (8192 bytes); 16
+  // elements on, a K-major operand is 32 bytes away and an MN-major one 2048
+  constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  constexpr uint32_t kWLbo = W_MN ? ((8192u >> 4) - (16u >> 4)) << 16 : 0u, kW16 = W_MN ? 128u : 2u;
   const PoolArgs &p = a.p;
   const PoolTermLayout &l = a.l;
   const PoolSmem sm = pool_smem(pool_raw, l.bytes);
@@ -363,19 +373,20 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
   if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &tmW1 : tid == 1 ? &tmW2 : tid == 2 ? &tmV : &tmVt);
   const uint32_t tmem = pool_setup(sm, kPoolTermTmem, 2 * kPoolMostStages + 3, 4);
 
-  // the adapters' first tiles, this thread's in registers
-  int first[kPoolPerThread], lo_of[kPoolPerThread], hi_of[kPoolPerThread];
-  const int per = (p.n + kPoolTermThreads - 1) / kPoolTermThreads;
-  int sum = 0;
-#pragma unroll
-  for (int i = 0; i < kPoolPerThread; ++i) {
-    const int ad = tid * per + i;
-    const bool in = i < per && ad < p.n;
-    const int2 g = in ? pool_group(p, ad) : make_int2(0, 0);
-    lo_of[i] = g.x;
-    hi_of[i] = g.y;
-    first[i] = sum;
-    sum += (g.y - g.x + tn - 1) / tn;
+  // this thread's adapters, ad0 .. ad0 + per: what is known of the first stays in registers
+  const int per = (p.n + kPoolTermThreads - 1) / kPoolTermThreads, ad0 = tid * per;
+  int2 group0 = make_int2(0, 0);
+  int sum = 0, rank0 = 0;
+  float scale0 = 0.0f;
+  if (ad0 < p.n) {
+    group0 = pool_group(p, ad0);
+    rank0 = pool_rank(p, ad0);
+    scale0 = p.scales[ad0];
+    sum = (group0.y - group0.x + tn - 1) / tn;
+    for (int i = 1; i < per && ad0 + i < p.n; ++i) {
+      const int2 grp = pool_group(p, ad0 + i);
+      sum += (grp.y - grp.x + tn - 1) / tn;
+    }
   }
   int inc = sum;
 #pragma unroll
@@ -392,113 +403,152 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
     tiles += warp_sum[w];
   }
 
-  const int cs = static_cast<int>(ptx::cluster_nctarank()), q = static_cast<int>(ptx::cluster_ctarank());
-  const int k_steps = static_cast<int>((a.len + 63) / 64), k_per = (k_steps + cs - 1) / cs;
+  // a tile is shared by g CTAs of the cluster: as many as keep all CTAs of the grid in use
+  const int cluster = static_cast<int>(ptx::cluster_nctarank()), crank = static_cast<int>(ptx::cluster_ctarank());
+  int g = cluster;
+  while (g > 1 && static_cast<int64_t>(tiles) * g > gridDim.x) g >>= 1;
+  const int q = crank & (g - 1), peers = crank - q;  // the g CTAs from rank `peers` of the cluster
+  const int k_steps = static_cast<int>((a.len + 63) / 64), k_per = (k_steps + g - 1) / g;
   const int nblk = a.out ? static_cast<int>((a.cols + 127) / 128) : 0;
   const int nrb = (p.r + 127) / 128, acc_cols = tn * nrb;  // one of the four accumulators of the sums
   RingPos pos;
   uint32_t sum_phase = 0, issued = 0, blocks = 0;  // blocks: accumulators of features used so far
   bool ok = true;
-  for (int tile = blockIdx.x / cs; tile < tiles; tile += gridDim.x / cs) {
-#pragma unroll
-    for (int i = 0; i < kPoolPerThread; ++i) {
-      const int t = tile - before - first[i];
-      const int lo = lo_of[i] + t * tn;
-      if (t >= 0 && lo < hi_of[i]) {
-        const int ad = tid * per + i;
-        tile_s.ad = ad;
-        tile_s.lo = lo;
-        tile_s.cnt = min(tn, hi_of[i] - lo);
-        tile_s.rank = pool_rank(p, ad);
-        tile_s.scale = p.scales[ad];
+  // all CTAs of a cluster walk as long as the first of its tiles exists
+  for (int lead = (blockIdx.x - crank) / g; lead < tiles; lead += gridDim.x / g) {
+    const int tile = lead + crank / g;
+    if (tile >= tiles && tid == 0) {
+      tile_s.ad = tile_s.lo = tile_s.cnt = tile_s.rank = 0;
+      tile_s.scale = 0.0f;
+    }
+    if (tile >= before && tile < before + sum) {  // among this thread's
+      int2 grp = group0;
+      int ad = ad0, t = tile - before, nt;
+      while (t >= (nt = (grp.y - grp.x + tn - 1) / tn)) {
+        t -= nt;
+        grp = pool_group(p, ++ad);
       }
+      tile_s.ad = ad;
+      tile_s.lo = grp.x + t * tn;
+      tile_s.cnt = min(tn, grp.y - tile_s.lo);
+      tile_s.rank = ad > ad0 ? pool_rank(p, ad) : rank0;
+      tile_s.scale = ad > ad0 ? p.scales[ad] : scale0;
     }
     __syncthreads();
     const int ad = tile_s.ad, lo = tile_s.lo, cnt = tile_s.cnt, rank = tile_s.rank;
     const int kb = rank > 0 ? min(q * k_per, k_steps) : 0, ke = rank > 0 ? min(k_steps, kb + k_per) : 0;
     const int nch = rank > 0 ? (rank + 63) / 64 : 0;
-    const int mine = rank > 0 && nblk > q ? (nblk - q + cs - 1) / cs : 0;  // blocks q, q + cs, ...
+    const int mine = rank > 0 && nblk > q ? (nblk - q + g - 1) / g : 0;  // blocks q, q + g, ...
     const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, W_MN ? 1 : 0, 0);
     const int quad = warp & 3, set = (warp - 2) >> 2;
 
-    // warp 0: stages [i0, i1) of W2's blocks, 64 ranks of a block each
+    // epilogue: a warp's items are (block, group of tokens), the blocks being those whose accumulator is its set's
+    constexpr int kGroup = PoolPiece<O>::kTokens, kElems = PoolPiece<O>::kElems, kLanes = 32 / kElems, kRows = 32 / kLanes;
+    constexpr int kPieces = kGroup / kRows;
+    const int tr = lane / kLanes, part = lane % kLanes;
+    const int b_first = (set ^ blocks) & 1;
+    const bool few = cnt <= 4;  // a column of the accumulator is then a token's feature of each lane, straight to Out
+    const bool pieces = VEC && !few && warp >= 2;
+    PoolPiece<O> y0[kPieces], y1[kPieces];
+    // an item's loads: rows that are not tokens, and columns past the last, load something that is and are not stored
+    auto load_y = [&](PoolPiece<O>(&y)[kPieces], int b, int g0) {
+      const int64_t f = static_cast<int64_t>(q + b * g) * 128 + quad * 32 + part * kElems;
+      const O *out = static_cast<const O *>(a.out) + (f < a.cols ? f : 0);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int64_t at = row_at[min(g0 + kRows * i + tr, cnt - 1)];
+        y[i].load(out + (at < 0 ? 0 : at));
+      }
+    };
+
+    // warp 0's thread: stages [i0, i1) of W2's blocks, 64 ranks of a block each
     auto load_w2 = [&](int i0, int i1) {
-      for (int i = i0; i < i1 && ok; ++i) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
-        if (!ok) break;
-        if (lane == 0) {
-          const int f = (q + i / nch * cs) * 128, x = i % nch * 64;
-          uint8_t *st = sm.buf + pos.s * l.stage;
-          ptx::mbar_arrive_expect_tx(&full[pos.s], 16384u);
-          if (W_MN) {
-            ptx::tma_load_3d(st, &tmW2, &full[pos.s], f, x, ad);
-            ptx::tma_load_3d(st + 8192, &tmW2, &full[pos.s], f + 64, x, ad);
-          } else {
-            ptx::tma_load_3d(st, &tmW2, &full[pos.s], x, f, ad);
-          }
+      int b = i0 / max(nch, 1), ch = i0 - b * nch;
+      for (int i = i0; i < i1; ++i) {
+        if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
+        const int f = (q + b * g) * 128, x = ch * 64;
+        uint8_t *st = sm.buf + pos.s * l.stage;
+        ptx::mbar_arrive_expect_tx(&full[pos.s], 16384u);
+        if (W_MN) {
+          ptx::tma_load_3d(st, &tmW2, &full[pos.s], f, x, ad);
+          ptx::tma_load_3d(st + 8192, &tmW2, &full[pos.s], f + 64, x, ad);
+        } else {
+          ptx::tma_load_3d(st, &tmW2, &full[pos.s], x, f, ad);
         }
-        __syncwarp();
+        if (++ch == nch) { ch = 0; ++b; }
         ++issued;
         pos.next(stages);
       }
-      if (!ok && lane == 0) pool_fail(sm, p.status);
     };
 
     // ------------------------------------------------------------ 1. the sums over the long dimension
     if (warp == 0) {
-      const int4 rows = pool_rows(p, lo + 4 * min(lane, tn / 4 - 1), lo + cnt - 1);
+      const int4 rows = cnt > 0 ? pool_rows(p, lo + 4 * min(lane, tn / 4 - 1), lo + cnt - 1) : make_int4(0, 0, 0, 0);
       const bool mine4 = 4 * lane < cnt;
-      const bool run = pool_run32(rows, lane, 4 * lane, cnt, true), tile_load = run && (lane & 7) == 0 && mine4;
-      const bool gather = !run && mine4;
-      // W1's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
-      const int w_loads = W_MN ? (p.r + 63) / 64 : nrb;
-      const uint32_t w_box = W_MN ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u;
-      const uint32_t bytes = w_loads * w_box + __popc(__ballot_sync(0xffffffffu, tile_load)) * 4096u +
-                             __popc(__ballot_sync(0xffffffffu, gather)) * 512u;
-      for (int ks = kb; ks < ke && ok; ++ks) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
-        if (!ok) break;
-        uint8_t *st = sm.buf + pos.s * l.stage;
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&full[pos.s], bytes);
+      const bool run = pool_run32(rows, lane, 4 * lane, cnt, true);
+      const uint32_t tile_loads = __ballot_sync(0xffffffffu, run && (lane & 7) == 0 && mine4);
+      const uint32_t gathers = __ballot_sync(0xffffffffu, !run && mine4);
+      if (lane < 16) row4[lane] = rows;
+      __syncwarp();
+      if (ok && ptx::elect_one()) {
+        // W1's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
+        const int w_loads = W_MN ? (p.r + 63) / 64 : nrb;
+        const uint32_t w_box = W_MN ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u;
+        const uint32_t bytes = w_loads * w_box + __popc(tile_loads) * 4096u + __popc(gathers) * 512u;
+        for (int ks = kb; ks < ke; ++ks) {
+          if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
+          uint8_t *st = sm.buf + pos.s * l.stage;
+          uint64_t *bar = &full[pos.s];
+          ptx::mbar_arrive_expect_tx(bar, bytes);
           for (int i = 0; i < w_loads; ++i)
-            ptx::tma_load_3d(st + v_bytes + i * (W_MN ? 8192 : 16384), &tmW1, &full[pos.s], W_MN ? i * 64 : ks * 64,
-                             W_MN ? ks * 64 : i * 128, ad);
+            ptx::tma_load_3d(st + v_bytes + i * (W_MN ? 8192 : 16384), &tmW1, bar, W_MN ? i * 64 : ks * 64, W_MN ? ks * 64 : i * 128,
+                             ad);
+          for (uint32_t m = tile_loads; m; m &= m - 1) {
+            const int i = __ffs(m) - 1;
+            ptx::tma_load_2d(st + i * 512, &tmVt, bar, ks * 64, row4[i].x);
+          }
+          for (uint32_t m = gathers; m; m &= m - 1) {
+            const int i = __ffs(m) - 1;
+            ptx::tma_gather4(st + i * 512, &tmV, bar, ks * 64, row4[i]);
+          }
+          ++issued;
+          pos.next(stages);
         }
-        __syncwarp();
-        if (tile_load) ptx::tma_load_2d(st + lane * 512, &tmVt, &full[pos.s], ks * 64, rows.x);
-        if (gather) ptx::tma_gather4(st + lane * 512, &tmV, &full[pos.s], ks * 64, rows);
-        __syncwarp();
-        ++issued;
-        pos.next(stages);
+        // the first of W2's blocks follow through the ring while the sums are joined
+        if (ok) load_w2(0, min(mine * nch, static_cast<int>(stages)));
+        if (!ok) pool_fail(sm, p.status);
       }
-      if (!ok && lane == 0) pool_fail(sm, p.status);
-      // the first of W2's blocks follow through the ring while the sums are joined
-      load_w2(0, min(mine * nch, static_cast<int>(stages)));
+      __syncwarp();
     } else if (warp == 1) {
-      for (int ks = kb; ks < ke && ok; ++ks) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (lane == 0) {
-          const uint32_t v = ptx::smem_addr(sm.buf + pos.s * l.stage), w = v + v_bytes, d = tmem + ((ks - kb) & 3) * acc_cols;
+      if (ok && ptx::elect_one()) {
+        const uint32_t v_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
+        for (int ks = kb; ks < ke; ++ks) {
+          if (!ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t v = v_lo + pos.s * (l.stage >> 4), w = v + (v_bytes >> 4) + kWLbo, d = tmem + ((ks - kb) & 3) * acc_cols;
+          const uint32_t more = ks - kb >= 4 ? 1u : 0u;
 #pragma unroll
           for (int k16 = 0; k16 < 4; ++k16)
-            for (int rb = 0; rb < nrb; ++rb)
-              ptx::mma_bf16(d + rb * tn,
-                            W_MN ? ptx::smem_desc_sw128(w + rb * 16384 + k16 * 2048, 8192, 1024)
-                                 : ptx::smem_desc_sw128(w + rb * 16384 + k16 * 32, 16, 1024),
-                            ptx::smem_desc_sw128(v + k16 * 32, 16, 1024), idesc, (ks - kb >= 4 || k16) ? 1u : 0u);
+            ptx::mma_bf16_lohi(d, w + k16 * kW16, kDescHi, v + k16 * 2, kDescHi, idesc, k16 ? 1u : more);
+          if (nrb > 1) {  // ranks 128 and up
+#pragma unroll
+            for (int k16 = 0; k16 < 4; ++k16)
+              ptx::mma_bf16_lohi(d + tn, w + 1024 + k16 * kW16, kDescHi, v + k16 * 2, kDescHi, idesc, k16 ? 1u : more);
+          }
           ptx::mma_commit(&empty[pos.s]);
+          pos.next(stages);
         }
-        __syncwarp();
-        pos.next(stages);
+        if (ok && ke > kb) ptx::mma_commit(sum_full);
+        if (!ok) pool_fail(sm, p.status);
       }
-      if (ok && ke > kb && lane == 0) ptx::mma_commit(sum_full);
-      if (!ok && lane == 0) pool_fail(sm, p.status);
       __syncwarp();
     } else {
-      if (tid - 64 < tn) token[tid - 64] = tid - 64 < cnt ? pool_token(p, lo + tid - 64) : -1;
+      if (tid - 64 < tn) {
+        const int t = tid - 64 < cnt ? pool_token(p, lo + tid - 64) : -1;
+        row_at[tid - 64] = t < 0 ? -1 : t * a.ldo;
+      }
+      ptx::named_bar_sync(1, kPoolTermThreads - 64);
+      if (pieces && b_first < mine) load_y(y0, b_first, 0);  // the first one's, while the sums are formed
       if (ke > kb && ok) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(sum_full, sum_phase, sm.abort_flag));
         sum_phase ^= 1;
@@ -509,15 +559,19 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
       for (int rb = 0; rb < nrb; ++rb) {
         if (rb * 128 + quad * 32 >= p.r) break;
         for (int c0 = set * (tn / 2); c0 < c_end; c0 += 16) {
+          const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + rb * tn + c0;
           float x[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[j] = 0.0f;
-          for (int i = 0; i < nacc; ++i) {
-            uint32_t v[16];
-            ptx::tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + i * acc_cols + rb * tn + c0, v);
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            if (i >= nacc) break;
+            uint32_t v[16], w[16];
+            ptx::tmem_ld16(from + i * acc_cols, v);
+            if (i + 1 < nacc) ptx::tmem_ld16(from + (i + 1) * acc_cols, w);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]);
+            for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]) + (i + 1 < nacc ? __uint_as_float(w[j]) : 0.0f);
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -530,42 +584,41 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
     // ------------------------------------------------------------ 2. the sums over the cluster
     pool_cluster_sync();
     {
-      const int pt = (cnt + cs - 1) / cs, c_lo = min(cnt, q * pt), c_hi = min(cnt, c_lo + pt);
-      const int n8 = (p.r + 15) / 16 * 2;  // groups of 8 ranks; products take 16 at a time
+      const int pt = (cnt + g - 1) / g, c_lo = min(cnt, q * pt), c_hi = min(cnt, c_lo + pt);
+      const int n4 = (p.r + 15) / 16 * 4;  // groups of 4 ranks; products take 16 at a time
       const uint32_t exch_addr = ptx::smem_addr(exch), planes_addr = ptx::smem_addr(planes);
-      for (int e = tid; e < (c_hi - c_lo) * n8; e += kPoolTermThreads) {
-        const int c = c_lo + e / n8, j = e % n8 * 8;
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+      for (int e = tid; e < (c_hi - c_lo) * n4; e += kPoolTermThreads) {
+        const int c = c_lo + e / n4, j = e % n4 * 4;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (j < rank) {
           const uint32_t src = exch_addr + (c * l.rpad + j) * 4;
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (r < cs) {
-              const uint32_t from = ptx::mapa_shared(src, r);
-              const float4 u = ptx::ld_cluster_f32x4(from), w = ptx::ld_cluster_f32x4(from + 16);
-              x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
-              x[4] += w.x; x[5] += w.y; x[6] += w.z; x[7] += w.w;
-            }
+          for (int r0 = 0; r0 < 8; r0 += 4) {
+            if (r0 >= g) break;
+            float4 u[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (r0 + r < g) u[r] = ptx::ld_cluster_f32x4(ptx::mapa_shared(src, peers + r0 + r));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (r0 + r < g) { x.x += u[r].x; x.y += u[r].y; x.z += u[r].z; x.w += u[r].w; }
+          }
         }
         const int t = a.P ? pool_token(p, lo + c) : -1;
-        const uint32_t dst = planes_addr + (j >> 6) * a.planes * l.plane + c * 128 + ((((j >> 3) & 7) ^ (c & 7)) << 4);
+        const uint32_t dst = planes_addr + (j >> 6) * a.planes * l.plane + c * 128 + ((((j >> 3) & 7) ^ (c & 7)) << 4) + (j & 4) * 2;
 #pragma unroll
         for (int pl = 0; pl < kPoolPlanes; ++pl) {
-          uint4 h;
-          h.x = pack_bf16x2(x[0], x[1]);
-          h.y = pack_bf16x2(x[2], x[3]);
-          h.z = pack_bf16x2(x[4], x[5]);
-          h.w = pack_bf16x2(x[6], x[7]);
-          x[0] -= bf16lo_to_f32(h.x); x[1] -= bf16hi_to_f32(h.x);
-          x[2] -= bf16lo_to_f32(h.y); x[3] -= bf16hi_to_f32(h.y);
-          x[4] -= bf16lo_to_f32(h.z); x[5] -= bf16hi_to_f32(h.z);
-          x[6] -= bf16lo_to_f32(h.w); x[7] -= bf16hi_to_f32(h.w);
-          if (t >= 0 && j < p.r)
-            *reinterpret_cast<uint4 *>(a.P + (static_cast<int64_t>(pl) * p.M + t) * p.r + j) = h;
-          if (a.out && pl < a.planes)
-            for (int r = 0; r < cs; ++r) ptx::st_cluster_u32x4(ptx::mapa_shared(dst + pl * l.plane, r), h);
+          const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+          x.x -= bf16lo_to_f32(h.x);
+          x.y -= bf16hi_to_f32(h.x);
+          x.z -= bf16lo_to_f32(h.y);
+          x.w -= bf16hi_to_f32(h.y);
+          if (t >= 0 && j < p.r) *reinterpret_cast<uint2 *>(a.P + (static_cast<int64_t>(pl) * p.M + t) * p.r + j) = h;
+          if (a.out && pl < a.planes) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              if (r < g) ptx::st_cluster_u32x2(ptx::mapa_shared(dst + pl * l.plane, peers + r), h);
+          }
         }
       }
     }
@@ -574,123 +627,164 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
 
     // ------------------------------------------------------------ 3. the features
     if (warp == 0) {
-      load_w2(min(mine * nch, static_cast<int>(stages)), mine * nch);
+      if (ok && ptx::elect_one()) {
+        load_w2(min(mine * nch, static_cast<int>(stages)), mine * nch);
+        if (!ok) pool_fail(sm, p.status);
+      }
+      __syncwarp();
     } else if (warp == 1) {
       ptx::fence_proxy_async_all();
-      const uint32_t p_addr = ptx::smem_addr(planes);
-      for (int b = 0; b < mine && ok; ++b) {
-        const uint32_t n = blocks + b, acc = n & 1;
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_empty[acc], ((n >> 1) & 1) ^ 1, sm.abort_flag));
-        for (int ch = 0; ch < nch && ok; ++ch) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
-          if (!ok) break;
-          uint8_t *st = sm.buf + pos.s * l.stage;
-          const int left = min(64, rank - ch * 64);  // a multiple of 8
-          if ((left & 8) && rank < p.r) {
-            // products go 16 ranks at a time: the 8 past the adapter's rank meet zeros in P and have to be finite
-            for (int i = lane; i < 128; i += 32) {
-              const int at = W_MN ? (i >> 6) * 8192 + (left + ((i >> 3) & 7)) * 128 + (i & 7) * 16
-                                  : i * 128 + (((left >> 3) ^ (i & 7)) << 4);
-              *reinterpret_cast<uint4 *>(st + at) = make_uint4(0u, 0u, 0u, 0u);
+      if (ok && ptx::elect_one()) {
+        const uint32_t p_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
+        for (int b = 0; b < mine && ok; ++b) {
+          const uint32_t n = blocks + b, acc = n & 1;
+          if (!ptx::mbar_wait(&acc_empty[acc], ((n >> 1) & 1) ^ 1, sm.abort_flag)) { ok = false; break; }
+          for (int ch = 0; ch < nch; ++ch) {
+            if (!ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag)) { ok = false; break; }
+            uint8_t *st = sm.buf + pos.s * l.stage;
+            const int left = min(64, rank - ch * 64);  // a multiple of 8
+            if ((left & 8) && rank < p.r) {
+              // products go 16 ranks at a time: the 8 past the adapter's rank meet zeros in P and have to be finite
+              for (int i = 0; i < 128; ++i) {
+                const int at = W_MN ? (i >> 6) * 8192 + (left + ((i >> 3) & 7)) * 128 + (i & 7) * 16
+                                    : i * 128 + (((left >> 3) ^ (i & 7)) << 4);
+                *reinterpret_cast<uint4 *>(st + at) = make_uint4(0u, 0u, 0u, 0u);
+              }
+              ptx::fence_proxy_async_smem();
             }
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-          }
-          ptx::tc_fence_after();
-          if (lane == 0) {
-            const uint32_t w = ptx::smem_addr(st);
-            for (int k16 = 0; k16 * 16 < left; ++k16)
-              for (int pl = 0; pl < a.planes; ++pl)
-                ptx::mma_bf16(tmem + acc * 128,
-                              W_MN ? ptx::smem_desc_sw128(w + k16 * 2048, 8192, 1024) : ptx::smem_desc_sw128(w + k16 * 32, 16, 1024),
-                              ptx::smem_desc_sw128(p_addr + (ch * a.planes + pl) * l.plane + k16 * 32, 16, 1024), idesc,
-                              (ch || k16 || pl) ? 1u : 0u);
+            ptx::tc_fence_after();
+            const uint32_t w = p_lo + ((st - sm.buf) >> 4) + kWLbo, pc = p_lo + ((l.planes_at + ch * a.planes * l.plane) >> 4);
+#pragma unroll
+            for (int k16 = 0; k16 < 4; ++k16) {
+              if (k16 * 16 >= left) break;
+#pragma unroll
+              for (int pl = 0; pl < kPoolPlanes; ++pl)
+                if (pl < a.planes)
+                  ptx::mma_bf16_lohi(tmem + acc * 128, w + k16 * kW16, kDescHi, pc + pl * (l.plane >> 4) + k16 * 2, kDescHi, idesc,
+                                     (ch || k16 || pl) ? 1u : 0u);
+            }
             ptx::mma_commit(&empty[pos.s]);
+            pos.next(stages);
           }
-          __syncwarp();
-          pos.next(stages);
+          if (ok) ptx::mma_commit(&acc_full[acc]);
         }
-        if (ok && lane == 0) ptx::mma_commit(&acc_full[acc]);
-        __syncwarp();
+        if (!ok) pool_fail(sm, p.status);
       }
-      if (!ok && lane == 0) pool_fail(sm, p.status);
+      __syncwarp();
     } else {
       const float s = tile_s.scale;
-      float *buf = exch + (warp - 2) * kPoolWarpBuf;
-      for (int b = (set ^ blocks) & 1; b < mine && ok; b += 2) {  // the blocks whose accumulator is this set's
-        const uint32_t n = blocks + b, acc = set;
-        const int64_t f0 = static_cast<int64_t>(q + b * cs) * 128 + quad * 32;
-        bool ready = false;
-        auto wait = [&]() {
-          ready = true;
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 1) & 1, sm.abort_flag));
-          ptx::tc_fence_after();
-          return ok;
+      const uint32_t acc = set, d = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128;
+      auto wait = [&](int b) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], ((blocks + b) >> 1) & 1, sm.abort_flag));
+        ptx::tc_fence_after();
+        return ok;
+      };
+      auto done = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&acc_empty[acc]);
+      };
+      if (few) {
+        const int64_t f0 = static_cast<int64_t>(q) * 128 + quad * 32 + lane;
+        float y[4], next[4];
+        auto load_few = [&](float(&z)[4], int b) {
+          const int64_t f = f0 + static_cast<int64_t>(b) * g * 128;
+          const O *out = static_cast<const O *>(a.out) + (f < a.cols ? f : 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t at = row_at[min(j, cnt - 1)];
+            z[j] = pool_load(out + (at < 0 ? 0 : at));
+          }
         };
-        const uint32_t d = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128;
-        if (VEC) {
-          constexpr int kGroup = PoolPiece<O>::kTokens, kElems = PoolPiece<O>::kElems, kLanes = 32 / kElems, kRows = 32 / kLanes;
-          const int tr = lane / kLanes, part = lane % kLanes;
-          const bool in = f0 + part * kElems < a.cols;
-          O *out = static_cast<O *>(a.out) + f0 + part * kElems;
-          for (int g0 = 0; g0 < cnt; g0 += kGroup) {
-            PoolPiece<O> y[kGroup / kRows];
+        if (b_first < mine) load_few(y, b_first);
+        for (int b = b_first; b < mine && ok; b += 2) {
+          if (b + 2 < mine) load_few(next, b + 2);
+          if (!wait(b)) break;
+          uint32_t v[4];
+          ptx::tmem_ld4(d, v);
+          ptx::tmem_ld_wait();
+          done();
+          const int64_t f = f0 + static_cast<int64_t>(b) * g * 128;
 #pragma unroll
-            for (int i = 0; i < kGroup / kRows; ++i) {
-              const int c = g0 + kRows * i + tr, t = c < cnt ? token[c] : -1;
-              if (t >= 0 && in) y[i].load(out + t * a.ldo);
-              else y[i].zero();
-            }
-            if (!ready && !wait()) break;
+          for (int j = 0; j < 4; ++j) {
+            const int64_t at = j < cnt && f < a.cols ? row_at[j] : -1;
+            if (at >= 0) pool_store(static_cast<O *>(a.out) + f + at, fmaf(s, __uint_as_float(v[j]), y[j]));
+            y[j] = next[j];
+          }
+        }
+      } else if (VEC) {
+        float *buf = exch + (warp - 2) * kPoolWarpBuf;
+        auto add_store = [&](PoolPiece<O>(&y)[kPieces], int b, int g0) {
+          if (g0 == 0 && !wait(b)) return;
+          const int64_t f = static_cast<int64_t>(q + b * g) * 128 + quad * 32 + part * kElems;
+          O *out = static_cast<O *>(a.out) + f;
 #pragma unroll
-            for (int k = 0; k < kGroup / 16; ++k) {
-              if (g0 + 16 * k >= cnt) break;
-              uint32_t v[16];
-              ptx::tmem_ld16(d + g0 + 16 * k, v);
-              ptx::tmem_ld_wait();
-              __syncwarp();
+          for (int k = 0; k < kGroup / 16; ++k) {
+            if (g0 + 16 * k >= cnt) break;
+            uint32_t v[16];
+            ptx::tmem_ld16(d + g0 + 16 * k, v);
+            ptx::tmem_ld_wait();
+            __syncwarp();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) buf[j * kPoolPitch + lane] = __uint_as_float(v[j]);
-              __syncwarp();
+            for (int j = 0; j < 16; ++j) buf[j * kPoolPitch + lane] = __uint_as_float(v[j]);
+            __syncwarp();
 #pragma unroll
-              for (int h = 0; h < 16 / kRows; ++h) {
-                const int c = g0 + 16 * k + kRows * h + tr, t = c < cnt ? token[c] : -1;
-                if (t >= 0 && in)
-                  y[16 / kRows * k + h].add_store(out + t * a.ldo, s, buf + (kRows * h + tr) * kPoolPitch + part * kElems);
-              }
+            for (int h = 0; h < 16 / kRows; ++h) {
+              const int i = 16 / kRows * k + h, c = g0 + kRows * i + tr;
+              y[i].add(s, buf + (kRows * h + tr) * kPoolPitch + part * kElems);
+              const int64_t at = c < cnt && f < a.cols ? row_at[c] : -1;
+              if (at >= 0) y[i].store(out + at);
             }
           }
-        } else {
+          if (g0 + kGroup >= cnt) done();
+        };
+        // (block, group of tokens) after (block, group of tokens), the next one's loads ahead
+        int b = b_first, g0 = 0;
+        auto step = [&](PoolPiece<O>(&y)[kPieces], PoolPiece<O>(&next)[kPieces]) {
+          int nb = b, ng = g0 + kGroup;
+          if (ng >= cnt) { ng = 0; nb += 2; }
+          if (nb < mine) load_y(next, nb, ng);
+          add_store(y, b, g0);
+          b = nb;
+          g0 = ng;
+          return ok && b < mine;
+        };
+        if (b < mine && ok)
+          while (step(y0, y1) && step(y1, y0)) {
+          }
+      } else {
+        for (int b = b_first; b < mine && ok; b += 2) {
+          const int64_t f0 = static_cast<int64_t>(q + b * g) * 128 + quad * 32;
+          bool ready = false;
           const bool in = f0 + lane < a.cols;
           O *out = static_cast<O *>(a.out) + f0 + lane;
           for (int c0 = 0; c0 < cnt; c0 += 16) {
             float y[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int t = c0 + j < cnt ? token[c0 + j] : -1;
-              y[j] = t >= 0 && in ? pool_load(out + t * a.ldo) : 0.0f;
+              const int64_t at = c0 + j < cnt ? row_at[c0 + j] : -1;
+              y[j] = at >= 0 && in ? pool_load(out + at) : 0.0f;
             }
-            if (!ready && !wait()) break;
+            if (!ready && !wait(b)) break;
+            ready = true;
             uint32_t v[16];
             ptx::tmem_ld16(d + c0, v);
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int t = c0 + j < cnt ? token[c0 + j] : -1;
-              if (t >= 0 && in) pool_store(out + t * a.ldo, fmaf(s, __uint_as_float(v[j]), y[j]));
+              const int64_t at = c0 + j < cnt ? row_at[c0 + j] : -1;
+              if (at >= 0 && in) pool_store(out + at, fmaf(s, __uint_as_float(v[j]), y[j]));
             }
           }
+          done();
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&acc_empty[acc]);
       }
       if (!ok && lane == 0) pool_fail(sm, p.status);
     }
     blocks += mine;
     __syncthreads();  // the tile's tokens, planes and buffers are done with
   }
-  if (warp == 0 && lane == 0 && *sm.abort_flag) ring_drain(full, pos, stages, issued);
+  if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the thread that loads
   pool_teardown(tmem, kPoolTermTmem);
 }
 

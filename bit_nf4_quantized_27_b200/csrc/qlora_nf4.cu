@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -975,14 +976,68 @@ bool tmap_tokens(CUtensorMap *gather, CUtensorMap *tile, const void *ptr, int64_
          make_tmap(tile, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, rows, ld, 64, 32, true);
 }
 
-// Launch of `clusters` clusters of `cs` CTAs, allowed to begin while the kernel ahead ends.
+// A pool kernel on one device: its attributes are set at the first call, and how many clusters of a size fit the GPU at once
+// is asked once for each size and amount of shared memory.
+struct PoolKernelState {
+  std::once_flag flag;
+  qlora_status result;
+  std::atomic<uint64_t> fit[16];  // (bytes << 16 | size << 12 | clusters), in the order asked
+};
+
+template <typename... KArgs>
+qlora_status pool_clusters_that_fit(void (*kernel)(KArgs...), cudaLaunchConfig_t cfg, cudaLaunchAttribute cluster,
+                                    PoolKernelState &ks, int dev, int *out) {
+  const uint64_t key = static_cast<uint64_t>(cfg.dynamicSmemBytes) << 16 | cluster.val.clusterDim.x << 12;
+  for (auto &f : ks.fit) {
+    uint64_t v = f.load(std::memory_order_relaxed);
+    if (v == 0) {
+      cfg.attrs = &cluster;
+      cfg.numAttrs = 1;
+      cfg.gridDim = dim3(cluster.val.clusterDim.x);
+      int n = 0, sm_bytes = 0;
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess ||
+          cudaDeviceGetAttribute(&sm_bytes, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return QLORA_ERR_CUDA;
+      }
+      // CTAs that share an SM, by the shared memory that bounds it (1 KB more goes to the system for each)
+      const int per_sm = std::max(1, std::min(2, static_cast<int>(sm_bytes / (cfg.dynamicSmemBytes + fa.sharedSizeBytes + 1024))));
+      // The query answers for one CTA an SM (148 for clusters of one) even where two are seen to run side by side: two
+      // to an SM, a cluster takes the SMs of one half its size.
+      cluster.val.clusterDim.x = std::max<unsigned>(1, cluster.val.clusterDim.x / per_sm);
+      const int copies = static_cast<int>(cluster.val.clusterDim.x) * per_sm > static_cast<int>(cfg.gridDim.x) ? per_sm : 1;
+      cfg.gridDim = dim3(cluster.val.clusterDim.x);
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return QLORA_ERR_CUDA;
+      }
+      n *= copies;
+      f.store(v = key | static_cast<uint64_t>(std::min(n, 4095)), std::memory_order_relaxed);
+    }
+    if ((v & ~uint64_t(4095)) == key) {
+      *out = static_cast<int>(v & 4095);
+      return QLORA_OK;
+    }
+  }
+  return QLORA_ERR_CUDA;
+}
+
+// Launch of at most `most` clusters of `cs` CTAs, and no more than fit at once, allowed to begin while the kernel ahead ends.
 template <typename... KArgs, typename... Args>
-qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int threads, uint32_t bytes, uint32_t most_bytes,
-                         int dev, std::once_flag *flags, qlora_status *results, cudaStream_t st, Args &&...args) {
-  const qlora_status s = set_smem(kernel, static_cast<int>(pool_smem_bytes(most_bytes)), dev, flags, results);
-  if (s != QLORA_OK) return s;
+qlora_status launch_pool(void (*kernel)(KArgs...), int64_t most, int cs, int threads, uint32_t bytes, uint32_t most_bytes,
+                         PoolKernelState &ks, int dev, cudaStream_t st, Args &&...args) {
+  std::call_once(ks.flag, [&] {
+    ks.result = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(pool_smem_bytes(most_bytes))) == cudaSuccess &&
+                        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared) == cudaSuccess
+                    ? QLORA_OK
+                    : QLORA_ERR_CUDA;
+    cudaGetLastError();
+  });
+  if (ks.result != QLORA_OK) return ks.result;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cs));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = pool_smem_bytes(bytes);
   cfg.stream = st;
@@ -993,6 +1048,10 @@ qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int
   attr[1].val.clusterDim.x = cs;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
+  int fit = 0;
+  const qlora_status s = pool_clusters_that_fit(kernel, cfg, attr[1], ks, dev, &fit);
+  if (s != QLORA_OK) return s;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most, fit) * cs));
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) {
@@ -1015,26 +1074,27 @@ qlora_status launch_pool_term_t(const PoolArgs &p, const qlora_adapter_pool *poo
   a.out = Out;
   a.P = P;
   a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
-  a.l = pool_term_layout(p.r, a.planes);
+  // Clusters of eight CTAs where the tiles that full groups make cannot fill the SMs otherwise, else of four, of which
+  // more fit at once (GPCs do not divide by eight); the kernel splits a cluster over several tiles when there are more.
+  // Tiles of 32 tokens where 64 would leave half of the CTAs (two to an SM) idle.
+  const bool narrow = (p.M + 63) / 64 * 4 <= sms;
+  const int tn = pool_term_layout(p.r, a.planes, false, narrow).tn;
+  const int64_t tiles = (p.M + tn - 1) / tn, most = p.M / tn + std::min<int64_t>(p.n, p.M);
+  a.l = pool_term_layout(p.r, a.planes, most * 8 <= sms, narrow);
+  const int cs = tiles * 8 <= sms ? 8 : 4;
   CUtensorMap tmW1, tmW2, tmV, tmVt;
   if (!(W_MN ? tmap_pool(&tmW1, pool->B, p.r, p.N, p.n, 64) : tmap_pool(&tmW1, pool->A, p.K, p.r, p.n, std::min(p.r, 128))) ||
       !(W_MN ? tmap_pool(&tmW2, pool->A, p.K, p.r, p.n, 64) : tmap_pool(&tmW2, pool->B, p.r, p.N, p.n, 128)) ||
       !tmap_tokens(&tmV, &tmVt, V, a.len, p.M, ldv))
     return QLORA_ERR_CUDA;
-  // as many CTAs a tile as give the SMs what they hold, by the tiles that full groups make (more are walked in turn)
-  const int resident = (p.r <= 64 ? 2 : 1) * sms;
-  const int64_t tiles = (p.M + a.l.tn - 1) / a.l.tn, most = p.M / a.l.tn + std::min<int64_t>(p.n, p.M);
-  int cs = 8;
-  while (cs > 1 && tiles * cs > resident) cs /= 2;
-  const int64_t clusters = std::min<int64_t>(most, resident / cs);
   const uint32_t most_bytes = 218 * 1024;
-  static std::once_flag flags[2][64];
-  static qlora_status results[2][64];
+  static PoolKernelState states[2][64];
   const bool vec = aligned(Out, 16) && ldo * sizeof(O) % 16 == 0;
-  return vec ? launch_pool(pool_term_kernel<W_MN, O, true>, clusters, cs, kPoolTermThreads, a.l.bytes, most_bytes, dev, flags[0],
-                           results[0], st, tmW1, tmW2, tmV, tmVt, a)
-             : launch_pool(pool_term_kernel<W_MN, O, false>, clusters, cs, kPoolTermThreads, a.l.bytes, most_bytes, dev, flags[1],
-                           results[1], st, tmW1, tmW2, tmV, tmVt, a);
+  const int64_t clusters = (most * 8 + cs - 1) / cs;  // of a tile's eight CTAs at most
+  return vec ? launch_pool(pool_term_kernel<W_MN, O, true>, clusters, cs, kPoolTermThreads, a.l.bytes, most_bytes, states[0][dev], dev, st,
+                           tmW1, tmW2, tmV, tmVt, a)
+             : launch_pool(pool_term_kernel<W_MN, O, false>, clusters, cs, kPoolTermThreads, a.l.bytes, most_bytes, states[1][dev], dev, st,
+                           tmW1, tmW2, tmV, tmVt, a);
 }
 template <bool W_MN>
 qlora_status launch_pool_term(const PoolArgs &p, const qlora_adapter_pool *pool, const void *V, int64_t ldv, __nv_bfloat16 *P,
@@ -1061,11 +1121,9 @@ qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const 
   const int64_t units = static_cast<int64_t>(p.n) * ((p.r + 63) / 64) * ((p.K + 127) / 128 + (p.N + 127) / 128);
   int cs = 8;
   while (cs > 1 && (units * cs > 4 * sms || cs * 64 > p.M)) cs /= 2;
-  const int64_t clusters = std::min<int64_t>(units, 2 * sms / cs);
-  static std::once_flag flags[64];
-  static qlora_status results[64];
-  return launch_pool(pool_grad_kernel<O>, clusters, cs, kPoolGradThreads, kPoolGradBytes, kPoolGradBytes, dev, flags, results, st,
-                     tmX, tmU, tmDY, tmT, tmXt, tmUt, tmDYt, tmTt, a);
+  static PoolKernelState states[64];
+  return launch_pool(pool_grad_kernel<O>, units, cs, kPoolGradThreads, kPoolGradBytes, kPoolGradBytes, states[dev], dev, st, tmX, tmU,
+                     tmDY, tmT, tmXt, tmUt, tmDYt, tmTt, a);
 }
 
 // The base products alone: Y = X W'^T, and dX = dY W'.
