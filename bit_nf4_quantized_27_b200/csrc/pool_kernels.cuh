@@ -171,7 +171,7 @@ __device__ __forceinline__ void ring_drain(uint64_t *full, RingPos pos, uint32_t
 }
 
 // Barriers and flags of a CTA, behind its buffers.
-constexpr uint32_t kPoolMostStages = 12, kPoolBars = 2 * kPoolMostStages + 8, kPoolTailBytes = 512;
+constexpr uint32_t kPoolMostStages = 12, kPoolBars = 2 * kPoolMostStages + 9, kPoolTailBytes = 512;
 struct PoolSmem {
   uint8_t *buf;   // 1024-byte aligned, `bytes` of it
   uint64_t *bars;
@@ -188,13 +188,12 @@ __device__ __forceinline__ PoolSmem pool_smem(uint8_t *raw, uint32_t bytes) {
 }
 __host__ __device__ constexpr uint32_t pool_smem_bytes(uint32_t bytes) { return 1024 + bytes + kPoolTailBytes; }
 
-// Set-up of both kernels: barriers (one arrival each, but for the accumulators' two `empty` ones), TMEM, then the wait for
-// the kernel ahead.  The next kernel may start only after that wait: one that reads early, or that waits for this kernel
-// alone, then finds everything before this kernel complete too.
-__device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_cols, int acc_empty, int acc_empty_count) {
+// Set-up of both kernels: barriers (one arrival each; four, one of each warp of a set, from place `four` on), TMEM, then
+// the wait for the kernel ahead.  The next kernel may start only after that wait: one that reads early, or that waits for
+// this kernel alone, then finds everything before this kernel complete too.
+__device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_cols, uint32_t four) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < static_cast<int>(kPoolBars); ++i)
-      ptx::mbar_init(&s.bars[i], acc_empty >= 0 && (i == acc_empty || i == acc_empty + 1) ? acc_empty_count : 1);
+    for (uint32_t i = 0; i < kPoolBars; ++i) ptx::mbar_init(&s.bars[i], i < four ? 1 : 4);
     *s.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -242,8 +241,8 @@ __device__ __forceinline__ void pool_fail(const PoolSmem &s, uint32_t *status) {
 //    every CTA of the tile (and to HBM, where the backward needs them).  No partial planes in HBM, no
 //    second launch, and the same bits every time.
 // 3. Each CTA takes every g-th block of 128 features: W2's block by TMA, rows of the accumulator as
-//    features, then Out += s accumulator.  Two sets of four epilogue warps take turns, each with an
-//    accumulator of its own: while one set stores a block, the other's block is loaded and multiplied.
+//    features, then Out += s accumulator.  Two sets of four epilogue warps take turns, each with two of four
+//    accumulators: while one is stored, the next is multiplied.
 //    The lanes hold features; where Out's rows are 16-byte aligned, 16 tokens at a time pass through
 //    shared memory, so that four lanes (bf16; eight for float32) then share a token's 32 features in
 //    16-byte pieces, loaded before the accumulator is waited for (element by element the epilogue took 47
@@ -367,11 +366,11 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tn = l.tn;
   const uint32_t stages = l.stages, v_bytes = tn * 128u;
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
-  uint64_t *acc_full = sum_full + 1, *acc_empty = acc_full + 2;
+  uint64_t *acc_full = sum_full + 1, *acc_empty = acc_full + 4;
   float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
   uint8_t *planes = sm.buf + l.planes_at;
   if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &tmW1 : tid == 1 ? &tmW2 : tid == 2 ? &tmV : &tmVt);
-  const uint32_t tmem = pool_setup(sm, kPoolTermTmem, 2 * kPoolMostStages + 3, 4);
+  const uint32_t tmem = pool_setup(sm, kPoolTermTmem, 2 * kPoolMostStages + 5);
 
   // this thread's adapters, ad0 .. ad0 + per: what is known of the first stays in registers
   const int per = (p.n + kPoolTermThreads - 1) / kPoolTermThreads, ad0 = tid * per;
@@ -622,7 +621,7 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
         }
       }
     }
-    ptx::fence_proxy_async_all();  // the planes are read by the tensor cores
+    ptx::fence_proxy_async_cluster();  // the planes are read by the tensor cores
     pool_cluster_sync();
 
     // ------------------------------------------------------------ 3. the features
@@ -633,49 +632,79 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
       }
       __syncwarp();
     } else if (warp == 1) {
-      ptx::fence_proxy_async_all();
-      if (ok && ptx::elect_one()) {
-        const uint32_t p_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
+      ptx::fence_proxy_async_cluster();
+      const uint32_t p_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
+      // one thread issues a chunk of a block's products
+      auto issue = [&](uint32_t acc, int ch) {
+        ptx::tc_fence_after();
+        const int left = min(64, rank - ch * 64);  // a multiple of 8; products go 16 ranks at a time
+        const uint32_t w = p_lo + pos.s * (l.stage >> 4) + kWLbo, pc = p_lo + ((l.planes_at + ch * a.planes * l.plane) >> 4);
+#pragma unroll
+        for (int k16 = 0; k16 < 4; ++k16) {
+          if (k16 * 16 >= left) break;
+#pragma unroll
+          for (int pl = 0; pl < kPoolPlanes; ++pl)
+            if (pl < a.planes)
+              ptx::mma_bf16_lohi(tmem + acc * 64, w + k16 * kW16, kDescHi, pc + pl * (l.plane >> 4) + k16 * 2, kDescHi, idesc,
+                                 (ch || k16 || pl) ? 1u : 0u);
+        }
+        ptx::mma_commit(&empty[pos.s]);
+        if (ch == nch - 1) ptx::mma_commit(&acc_full[acc]);
+      };
+      const bool one = ptx::elect_one();
+      if (!(rank & 8) || rank == p.r) {
+        if (ok && one) {
+          for (int b = 0; b < mine && ok; ++b) {
+            const uint32_t n = blocks + b, acc = n & 3;
+            ok = ptx::mbar_wait(&acc_empty[acc], ((n >> 2) & 1) ^ 1, sm.abort_flag);
+            for (int ch = 0; ch < nch && ok; ++ch) {
+              if (!(ok = ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag))) break;
+              issue(acc, ch);
+              pos.next(stages);
+            }
+          }
+          if (!ok) pool_fail(sm, p.status);
+        }
+      } else {
+        // The 8 ranks past the adapter's meet zeros in P and have to be finite: the warp clears them in each last chunk.
+        const int leader = __ffs(__ballot_sync(0xffffffffu, one)) - 1;
+        pos.s = __shfl_sync(0xffffffffu, pos.s, leader);
+        pos.ph = __shfl_sync(0xffffffffu, pos.ph, leader);
+        ok = __all_sync(0xffffffffu, ok);
         for (int b = 0; b < mine && ok; ++b) {
-          const uint32_t n = blocks + b, acc = n & 1;
-          if (!ptx::mbar_wait(&acc_empty[acc], ((n >> 1) & 1) ^ 1, sm.abort_flag)) { ok = false; break; }
-          for (int ch = 0; ch < nch; ++ch) {
-            if (!ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag)) { ok = false; break; }
-            uint8_t *st = sm.buf + pos.s * l.stage;
-            const int left = min(64, rank - ch * 64);  // a multiple of 8
-            if ((left & 8) && rank < p.r) {
-              // products go 16 ranks at a time: the 8 past the adapter's rank meet zeros in P and have to be finite
-              for (int i = 0; i < 128; ++i) {
-                const int at = W_MN ? (i >> 6) * 8192 + (left + ((i >> 3) & 7)) * 128 + (i & 7) * 16
-                                    : i * 128 + (((left >> 3) ^ (i & 7)) << 4);
+          const uint32_t n = blocks + b, acc = n & 3;
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_empty[acc], ((n >> 2) & 1) ^ 1, sm.abort_flag));
+          for (int ch = 0; ch < nch && ok; ++ch) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
+            if (!ok) break;
+            if (ch == nch - 1) {
+              uint8_t *st = sm.buf + pos.s * l.stage;
+              const int at_rank = rank & 63;
+#pragma unroll
+              for (int i = lane; i < 128; i += 32) {
+                const int at = W_MN ? (i >> 6) * 8192 + (at_rank + ((i >> 3) & 7)) * 128 + (i & 7) * 16
+                                    : i * 128 + (((at_rank >> 3) ^ (i & 7)) << 4);
                 *reinterpret_cast<uint4 *>(st + at) = make_uint4(0u, 0u, 0u, 0u);
               }
               ptx::fence_proxy_async_smem();
+              __syncwarp();
             }
-            ptx::tc_fence_after();
-            const uint32_t w = p_lo + ((st - sm.buf) >> 4) + kWLbo, pc = p_lo + ((l.planes_at + ch * a.planes * l.plane) >> 4);
-#pragma unroll
-            for (int k16 = 0; k16 < 4; ++k16) {
-              if (k16 * 16 >= left) break;
-#pragma unroll
-              for (int pl = 0; pl < kPoolPlanes; ++pl)
-                if (pl < a.planes)
-                  ptx::mma_bf16_lohi(tmem + acc * 128, w + k16 * kW16, kDescHi, pc + pl * (l.plane >> 4) + k16 * 2, kDescHi, idesc,
-                                     (ch || k16 || pl) ? 1u : 0u);
-            }
-            ptx::mma_commit(&empty[pos.s]);
+            if (one) issue(acc, ch);
+            __syncwarp();
             pos.next(stages);
           }
-          if (ok) ptx::mma_commit(&acc_full[acc]);
         }
-        if (!ok) pool_fail(sm, p.status);
+        if (!ok && lane == 0) pool_fail(sm, p.status);
       }
       __syncwarp();
     } else {
       const float s = tile_s.scale;
-      const uint32_t acc = set, d = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 128;
+      uint32_t acc = 0, d = 0;
       auto wait = [&](int b) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], ((blocks + b) >> 1) & 1, sm.abort_flag));
+        const uint32_t n = blocks + b;
+        acc = n & 3;
+        d = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 64;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], (n >> 2) & 1, sm.abort_flag));
         ptx::tc_fence_after();
         return ok;
       };
@@ -820,7 +849,7 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t stage_bytes = 16384u + a.planes * 8192u, stages = min(kPoolGradBytes / stage_bytes, kPoolMostStages);
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *acc_full = sm.bars + 2 * kPoolMostStages;
-  const uint32_t tmem = pool_setup(sm, kPoolGradTmem, -1, 1);
+  const uint32_t tmem = pool_setup(sm, kPoolGradTmem, kPoolBars);
   const int nrb = (p.r + 63) / 64;
   const int in_a = static_cast<int>((p.K + 127) / 128) * nrb, per_adapter = in_a + static_cast<int>((p.N + 127) / 128) * nrb;
   const int64_t units = static_cast<int64_t>(p.n) * per_adapter;
