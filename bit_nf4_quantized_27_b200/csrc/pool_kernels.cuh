@@ -460,6 +460,16 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
       }
     };
 
+    // the lines of this warp's features in a whole block, towards L2: a block ahead of the loads (16 KB an item's warp)
+    auto prefetch_block = [&](int b) {
+      const int64_t f = static_cast<int64_t>(q + b * g) * 128 + quad * 32;
+      if (f >= a.cols || (sizeof(O) == 2 && (quad & 1))) return;  // two warps' bf16 features share a line
+      for (int c = lane; c < cnt; c += 32) {
+        const int64_t at = row_at[c];
+        if (at >= 0) ptx::prefetch_line_l2(static_cast<const O *>(a.out) + f + at);
+      }
+    };
+
     // warp 0's thread: stages [i0, i1) of W2's blocks, 64 ranks of a block each
     auto load_w2 = [&](int i0, int i1) {
       int b = i0 / max(nch, 1), ch = i0 - b * nch;
@@ -547,7 +557,10 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
         row_at[tid - 64] = t < 0 ? -1 : t * a.ldo;
       }
       ptx::named_bar_sync(1, kPoolTermThreads - 64);
-      if (pieces && b_first < mine) load_y(y0, b_first, 0);  // the first one's, while the sums are formed
+      if (pieces && b_first < mine) {  // the first ones', while the sums are formed
+        load_y(y0, b_first, 0);
+        prefetch_block(b_first);
+      }
       if (ke > kb && ok) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(sum_full, sum_phase, sm.abort_flag));
         sum_phase ^= 1;
@@ -773,6 +786,7 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
           int nb = b, ng = g0 + kGroup;
           if (ng >= cnt) { ng = 0; nb += 2; }
           if (nb < mine) load_y(next, nb, ng);
+          if (g0 == 0 && b + 2 < mine) prefetch_block(b + 2);
           add_store(y, b, g0);
           b = nb;
           g0 = ng;

@@ -177,6 +177,11 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// The 128-byte line at src (any address within it), into L2.
+__device__ __forceinline__ void prefetch_line_l2(const void *src) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
+}
+
 // L2 policy for data that is read once (weights streamed by a decode step):
 // its lines are the first to be evicted, so they do not push out the small
 // operands, code and constants that the next call reads again.
