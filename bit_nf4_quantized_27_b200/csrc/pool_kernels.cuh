@@ -255,13 +255,13 @@ __device__ __forceinline__ void pool_fail(const PoolSmem &s, uint32_t *status) {
 // ---------------------------------------------------------------------------
 constexpr int kPoolTermThreads = 320;
 constexpr uint32_t kPoolTermTmem = 256;
+constexpr uint32_t kPoolTermMostBytes = 218 * 1024;
 // Shared memory of a warp's 16 tokens x 32 features: a pitch of 36 floats keeps 16-byte pieces aligned and both
 // directions without bank conflicts.
 constexpr int kPoolPitch = 36, kPoolWarpBuf = 16 * kPoolPitch;
 
 // Sizes that follow from the rank and the planes.  Two CTAs share an SM up to rank 64, unless the call is `roomy`: too
-// small to give every SM one, so that a deeper ring is worth more.  `narrow`: 32 tokens a tile rather than 64, for calls
-// whose tiles of 64 would leave half of the CTAs that fit without work.
+// small to give every SM one, so that a deeper ring is worth more. 
 struct PoolTermLayout {
   int tn;               // tokens a tile
   int rpad;             // floats a token of the partial sums
@@ -270,14 +270,14 @@ struct PoolTermLayout {
   uint32_t plane;       // bytes of one 64-rank chunk of one plane
   uint32_t planes_at, exch_at, bytes;
 };
-__host__ __device__ constexpr PoolTermLayout pool_term_layout(int r, int planes, bool roomy, bool narrow) {
+__host__ __device__ constexpr PoolTermLayout pool_term_layout(int r, int planes, bool roomy) {
   PoolTermLayout l{};
-  l.tn = r <= 128 && !narrow ? 64 : 32;
+  l.tn = r <= 128 ? 64 : 32;
   l.rpad = r <= 64 ? 64 : r <= 128 ? 128 : 256;
   l.stage = l.tn * 128u + l.rpad * 128u;  // token rows and W1's
   if (l.stage < 16384u) l.stage = 16384u;  // a block of W2
   l.plane = l.tn * 128u;
-  const uint32_t budget = (r <= 64 && !roomy ? 107u : 218u) * 1024u, p_bytes = (r + 63) / 64 * planes * l.plane;
+  const uint32_t budget = r <= 64 && !roomy ? 107u * 1024u : kPoolTermMostBytes, p_bytes = (r + 63) / 64 * planes * l.plane;
   const uint32_t exch = l.tn * l.rpad * 4u > 8 * kPoolWarpBuf * 4u ? l.tn * l.rpad * 4u : 8 * kPoolWarpBuf * 4u;
   const uint32_t fit = (budget - p_bytes - exch) / l.stage;
   l.stages = fit < kPoolMostStages ? fit : kPoolMostStages;
@@ -286,11 +286,11 @@ __host__ __device__ constexpr PoolTermLayout pool_term_layout(int r, int planes,
   l.bytes = l.exch_at + exch;
   return l;
 }
-static_assert(pool_term_layout(64, 3, false, false).stages >= 3 && pool_term_layout(128, 3, false, false).stages >= 3 &&
-                  pool_term_layout(256, 3, false, false).stages >= 3,
+static_assert(pool_term_layout(64, 3, false).stages >= 3 && pool_term_layout(128, 3, false).stages >= 3 &&
+                  pool_term_layout(256, 3, false).stages >= 3,
               "a ring of three stages at least");
-static_assert(pool_smem_bytes(pool_term_layout(64, 3, false, false).bytes) + 2048 <= 114 * 1024 &&
-                  pool_smem_bytes(pool_term_layout(256, 3, false, false).bytes) <= 225 * 1024,
+static_assert(pool_smem_bytes(pool_term_layout(64, 3, false).bytes) + 2048 <= 114 * 1024 &&
+                  pool_smem_bytes(pool_term_layout(256, 3, false).bytes) <= 225 * 1024,
               "shared memory");
 
 struct PoolTermArgs {
@@ -402,11 +402,11 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
     tiles += warp_sum[w];
   }
 
-  // a tile is shared by g CTAs of the cluster: as many as keep all CTAs of the grid in use
+  // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
   const int cluster = static_cast<int>(ptx::cluster_nctarank()), crank = static_cast<int>(ptx::cluster_ctarank());
   int g = cluster;
-  while (g > 1 && static_cast<int64_t>(tiles) * g > gridDim.x) g >>= 1;
-  const int q = crank & (g - 1), peers = crank - q;  // the g CTAs from rank `peers` of the cluster
+  while (g > 1 && (static_cast<int64_t>(tiles) * g > gridDim.x || cluster % g)) --g;
+  const int q = crank % g, peers = crank - q;  // the g CTAs from rank `peers` of the cluster
   const int k_steps = static_cast<int>((a.len + 63) / 64), k_per = (k_steps + g - 1) / g;
   const int nblk = a.out ? static_cast<int>((a.cols + 127) / 128) : 0;
   const int nrb = (p.r + 127) / 128, acc_cols = tn * nrb;  // one of the four accumulators of the sums

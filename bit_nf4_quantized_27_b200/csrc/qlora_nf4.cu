@@ -981,52 +981,11 @@ bool tmap_tokens(CUtensorMap *gather, CUtensorMap *tile, const void *ptr, int64_
 struct PoolKernelState {
   std::once_flag flag;
   qlora_status result;
-  std::atomic<uint64_t> fit[16];  // (bytes << 16 | size << 12 | clusters), in the order asked
+  std::atomic<uint64_t> fit[32];  // bytes << 16 | size << 12 | clusters, in the order asked
 };
 
 template <typename... KArgs>
-qlora_status pool_clusters_that_fit(void (*kernel)(KArgs...), cudaLaunchConfig_t cfg, cudaLaunchAttribute cluster,
-                                    PoolKernelState &ks, int dev, int *out) {
-  const uint64_t key = static_cast<uint64_t>(cfg.dynamicSmemBytes) << 16 | cluster.val.clusterDim.x << 12;
-  for (auto &f : ks.fit) {
-    uint64_t v = f.load(std::memory_order_relaxed);
-    if (v == 0) {
-      cfg.attrs = &cluster;
-      cfg.numAttrs = 1;
-      cfg.gridDim = dim3(cluster.val.clusterDim.x);
-      int n = 0, sm_bytes = 0;
-      cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess ||
-          cudaDeviceGetAttribute(&sm_bytes, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return QLORA_ERR_CUDA;
-      }
-      // CTAs that share an SM, by the shared memory that bounds it (1 KB more goes to the system for each)
-      const int per_sm = std::max(1, std::min(2, static_cast<int>(sm_bytes / (cfg.dynamicSmemBytes + fa.sharedSizeBytes + 1024))));
-      // The query answers for one CTA an SM (148 for clusters of one) even where two are seen to run side by side: two
-      // to an SM, a cluster takes the SMs of one half its size.
-      cluster.val.clusterDim.x = std::max<unsigned>(1, cluster.val.clusterDim.x / per_sm);
-      const int copies = static_cast<int>(cluster.val.clusterDim.x) * per_sm > static_cast<int>(cfg.gridDim.x) ? per_sm : 1;
-      cfg.gridDim = dim3(cluster.val.clusterDim.x);
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return QLORA_ERR_CUDA;
-      }
-      n *= copies;
-      f.store(v = key | static_cast<uint64_t>(std::min(n, 4095)), std::memory_order_relaxed);
-    }
-    if ((v & ~uint64_t(4095)) == key) {
-      *out = static_cast<int>(v & 4095);
-      return QLORA_OK;
-    }
-  }
-  return QLORA_ERR_CUDA;
-}
-
-// Launch of at most `most` clusters of `cs` CTAs, and no more than fit at once, allowed to begin while the kernel ahead ends.
-template <typename... KArgs, typename... Args>
-qlora_status launch_pool(void (*kernel)(KArgs...), int64_t most, int cs, int threads, uint32_t bytes, uint32_t most_bytes,
-                         PoolKernelState &ks, int dev, cudaStream_t st, Args &&...args) {
+qlora_status pool_attributes(void (*kernel)(KArgs...), uint32_t most_bytes, PoolKernelState &ks) {
   std::call_once(ks.flag, [&] {
     ks.result = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(pool_smem_bytes(most_bytes))) == cudaSuccess &&
@@ -1036,8 +995,58 @@ qlora_status launch_pool(void (*kernel)(KArgs...), int64_t most, int cs, int thr
                     : QLORA_ERR_CUDA;
     cudaGetLastError();
   });
-  if (ks.result != QLORA_OK) return ks.result;
+  return ks.result;
+}
+
+// Clusters of cs CTAs that run at once; 0 on an error.
+template <typename... KArgs>
+int pool_fit(void (*kernel)(KArgs...), int threads, uint32_t bytes, int cs, PoolKernelState &ks, int dev) {
+  const uint64_t key = static_cast<uint64_t>(pool_smem_bytes(bytes)) << 16 | static_cast<uint64_t>(cs) << 12;
+  std::atomic<uint64_t> *slot = nullptr;
+  for (auto &f : ks.fit) {
+    const uint64_t v = f.load(std::memory_order_relaxed);
+    if ((v & ~uint64_t(4095)) == key) return static_cast<int>(v & 4095);
+    if (v == 0) { slot = &f; break; }
+  }
+  int n = 0, sm_bytes = 0;
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sm_bytes, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  // CTAs that share an SM, by the shared memory that bounds it (1 KB more goes to the system for each).  The query below
+  // answers for one CTA an SM (148 clusters of one) even where two are seen to run side by side; with two to an SM, a
+  // cluster takes the SMs of one half its size.
+  const int per_sm = std::max(1, std::min(2, static_cast<int>(sm_bytes / (pool_smem_bytes(bytes) + fa.sharedSizeBytes + 1024))));
+  const int sms_of_one = (cs + per_sm - 1) / per_sm;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms_of_one);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = pool_smem_bytes(bytes);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = sms_of_one;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (cs < per_sm) n *= per_sm / cs;
+  n = std::min(n, 4095);
+  if (slot) slot->store(key | static_cast<uint64_t>(n), std::memory_order_relaxed);
+  return n;
+}
+
+// Launch of clusters of cs CTAs, allowed to begin while the kernel ahead ends.
+template <typename... KArgs, typename... Args>
+qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int threads, uint32_t bytes, cudaStream_t st,
+                         Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cs));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = pool_smem_bytes(bytes);
   cfg.stream = st;
@@ -1048,10 +1057,6 @@ qlora_status launch_pool(void (*kernel)(KArgs...), int64_t most, int cs, int thr
   attr[1].val.clusterDim.x = cs;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  int fit = 0;
-  const qlora_status s = pool_clusters_that_fit(kernel, cfg, attr[1], ks, dev, &fit);
-  if (s != QLORA_OK) return s;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most, fit) * cs));
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) {
@@ -1074,27 +1079,30 @@ qlora_status launch_pool_term_t(const PoolArgs &p, const qlora_adapter_pool *poo
   a.out = Out;
   a.P = P;
   a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
-  // Clusters of eight CTAs where the tiles that full groups make cannot fill the SMs otherwise, else of four, of which
-  // more fit at once (GPCs do not divide by eight); the kernel splits a cluster over several tiles when there are more.
-  // Tiles of 32 tokens where 64 would leave half of the CTAs (two to an SM) idle.
-  const bool narrow = (p.M + 63) / 64 * 4 <= sms;
-  const int tn = pool_term_layout(p.r, a.planes, false, narrow).tn;
-  const int64_t tiles = (p.M + tn - 1) / tn, most = p.M / tn + std::min<int64_t>(p.n, p.M);
-  a.l = pool_term_layout(p.r, a.planes, most * 8 <= sms, narrow);
-  const int cs = tiles * 8 <= sms ? 8 : 4;
+  const int64_t adapters = std::min<int64_t>(p.n, p.M), most = p.M / 64 + adapters;  // tiles at most
+  a.l = pool_term_layout(p.r, a.planes, most * 8 <= sms);
   CUtensorMap tmW1, tmW2, tmV, tmVt;
   if (!(W_MN ? tmap_pool(&tmW1, pool->B, p.r, p.N, p.n, 64) : tmap_pool(&tmW1, pool->A, p.K, p.r, p.n, std::min(p.r, 128))) ||
       !(W_MN ? tmap_pool(&tmW2, pool->A, p.K, p.r, p.n, 64) : tmap_pool(&tmW2, pool->B, p.r, p.N, p.n, 128)) ||
       !tmap_tokens(&tmV, &tmVt, V, a.len, p.M, ldv))
     return QLORA_ERR_CUDA;
-  const uint32_t most_bytes = 218 * 1024;
+  auto launch = [&](auto kernel, PoolKernelState &ks) -> qlora_status {
+    const qlora_status s = pool_attributes(kernel, kPoolTermMostBytes, ks);
+    if (s != QLORA_OK) return s;
+    // CTAs a tile: as many as let the tiles run at once, taken that three of four adapters that may have tokens have a
+    // short tile.  The kernel splits a cluster over several tiles, or walks, where there are more.
+    const int64_t tiles = (p.M + a.l.tn - 1) / a.l.tn + adapters * 3 / 4;
+    int cs = 8, fit = 0;
+    for (;; cs = cs > 2 ? cs - 2 : 1) {
+      if ((fit = pool_fit(kernel, kPoolTermThreads, a.l.bytes, cs, ks, dev)) == 0) return QLORA_ERR_CUDA;
+      if (cs == 1 || fit >= tiles) break;
+    }
+    return launch_pool(kernel, std::min<int64_t>(p.M / a.l.tn + adapters, fit), cs, kPoolTermThreads, a.l.bytes, st, tmW1, tmW2, tmV,
+                       tmVt, a);
+  };
   static PoolKernelState states[2][64];
   const bool vec = aligned(Out, 16) && ldo * sizeof(O) % 16 == 0;
-  const int64_t clusters = (most * 8 + cs - 1) / cs;  // of a tile's eight CTAs at most
-  return vec ? launch_pool(pool_term_kernel<W_MN, O, true>, clusters, cs, kPoolTermThreads, a.l.bytes, most_bytes, states[0][dev], dev, st,
-                           tmW1, tmW2, tmV, tmVt, a)
-             : launch_pool(pool_term_kernel<W_MN, O, false>, clusters, cs, kPoolTermThreads, a.l.bytes, most_bytes, states[1][dev], dev, st,
-                           tmW1, tmW2, tmV, tmVt, a);
+  return vec ? launch(pool_term_kernel<W_MN, O, true>, states[0][dev]) : launch(pool_term_kernel<W_MN, O, false>, states[1][dev]);
 }
 template <bool W_MN>
 qlora_status launch_pool_term(const PoolArgs &p, const qlora_adapter_pool *pool, const void *V, int64_t ldv, __nv_bfloat16 *P,
@@ -1122,8 +1130,13 @@ qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const 
   int cs = 8;
   while (cs > 1 && (units * cs > 4 * sms || cs * 64 > p.M)) cs /= 2;
   static PoolKernelState states[64];
-  return launch_pool(pool_grad_kernel<O>, units, cs, kPoolGradThreads, kPoolGradBytes, kPoolGradBytes, states[dev], dev, st, tmX, tmU,
-                     tmDY, tmT, tmXt, tmUt, tmDYt, tmTt, a);
+  auto kernel = pool_grad_kernel<O>;
+  const qlora_status s = pool_attributes(kernel, kPoolGradBytes, states[dev]);
+  if (s != QLORA_OK) return s;
+  const int fit = pool_fit(kernel, kPoolGradThreads, kPoolGradBytes, cs, states[dev], dev);
+  if (fit == 0) return QLORA_ERR_CUDA;
+  return launch_pool(kernel, std::min<int64_t>(units, fit), cs, kPoolGradThreads, kPoolGradBytes, st, tmX, tmU, tmDY, tmT, tmXt,
+                     tmUt, tmDYt, tmTt, a);
 }
 
 // The base products alone: Y = X W'^T, and dX = dY W'.
