@@ -75,12 +75,12 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_groups_kernel(const int
 }
 
 // ---------------------------------------------------------------------------
-// The products.  Two kernels, on the tensor cores (tcgen05, accumulators in TMEM) with
+// The products.  Three kernels, on the tensor cores (tcgen05, accumulators in TMEM) with
 // ranks, or features, in the 128 rows of the accumulator and tokens, or ranks, in its
 // columns:
 //
-//   term  P = V W1_a over the long dimension, then Out += s_a P W2_a: T and Y in the
-//         forward, U and dX in the backward
+//   down  P = V W_a over the long dimension: T = X A^T, U = dY B
+//   up    Out += s_a P W_a over the rank: Y with B^T, dX with A
 //   grad  s_a P^T V over the tokens of an adapter: dA, dB
 //
 // A tile holds tokens of one adapter, wherever their rows lie: runs of 32 rows come
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_groups_kernel(const int
 // fall follows from offsets, which only the device knows: each CTA adds up the
 // adapters' tile counts first and walks the tiles from there.
 //
-// Both are bound by HBM at ranks up to about 128 (r flops a byte of X, dY, Y or dX).
+// All are bound by HBM at ranks up to about 128 (r flops a byte of X, dY, Y or dX).
 // ---------------------------------------------------------------------------
 // The intermediates T = X A^T and U = dY B are [M, r] in float32 and kept as three bf16 planes [3, M, r], each the rounding
 // of what the ones before leave: 24 bits together, in the type the tensor cores take beside bf16 operands.  A bf16 result
@@ -188,7 +188,7 @@ __device__ __forceinline__ PoolSmem pool_smem(uint8_t *raw, uint32_t bytes) {
 }
 __host__ __device__ constexpr uint32_t pool_smem_bytes(uint32_t bytes) { return 1024 + bytes + kPoolTailBytes; }
 
-// Set-up of both kernels: barriers (one arrival each; four, one of each warp of a set, from place `four` on), TMEM, then
+// Set-up of the kernels: barriers (one arrival each; four, one of each warp of a set, from place `four` on), TMEM, then
 // the wait for the kernel ahead.  The next kernel may start only after that wait: one that reads early, or that waits for
 // this kernel alone, then finds everything before this kernel complete too.
 __device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_cols, uint32_t four) {
@@ -230,77 +230,359 @@ __device__ __forceinline__ void pool_fail(const PoolSmem &s, uint32_t *status) {
 }
 
 // ---------------------------------------------------------------------------
-// term: g CTAs of a cluster take a tile of 64 tokens (32 above rank 128); g, at most the cluster, follows on the device from
-// the number of tiles.
-//
-// 1. Its CTAs each sum a part of the long dimension, with the accumulator's rows as ranks and its columns as
-//    tokens; the steps of 64 go round four accumulators, which keeps each one's chain of float32 additions
-//    short (the tensor cores' additions cut off: one chain over 1400 elements was 3e-6 off, all to one side).
-// 2. Each CTA leaves its float32 partial sums in shared memory; each then adds up a share of the tokens over
-//    the g CTAs, in CTA order, splits the sums into planes, and writes them into the shared memory of
-//    every CTA of the tile (and to HBM, where the backward needs them).  No partial planes in HBM, no
-//    second launch, and the same bits every time.
-// 3. Each CTA takes every g-th block of 128 features: W2's block by TMA, rows of the accumulator as
-//    features, then Out += s accumulator.  Two sets of four epilogue warps take turns, each with two of four
-//    accumulators: while one is stored, the next is multiplied.
-//    The lanes hold features; where Out's rows are 16-byte aligned, 16 tokens at a time pass through
-//    shared memory, so that four lanes (bf16; eight for float32) then share a token's 32 features in
-//    16-byte pieces, loaded before the accumulator is waited for (element by element the epilogue took 47
-//    instructions an element and warp, and bound the kernel on issue).  Other outputs, odd strides or
-//    columns of a wider tensor, go element by element.
-//
-//   warp 0  loads; warp 1  products; warps 2..9  accumulators -> shared memory, epilogue; all  the sums
-// W_MN false (forward): W1 = A [n][r][len], W2 = B [n][cols][r], both K-major; true (backward): W1 = B
-// [n][len][r], W2 = A [n][r][cols], both MN-major.
+// How both kernels below find their tiles: every thread holds some of the adapters (in order) and the number of
+// tiles before them; the thread whose adapters a tile is among publishes it.
 // ---------------------------------------------------------------------------
-constexpr int kPoolTermThreads = 320;
-constexpr uint32_t kPoolTermTmem = 256;
-constexpr uint32_t kPoolTermMostBytes = 218 * 1024;
-// Shared memory of a warp's 16 tokens x 32 features: a pitch of 36 floats keeps 16-byte pieces aligned and both
-// directions without bank conflicts.
-constexpr int kPoolPitch = 36, kPoolWarpBuf = 16 * kPoolPitch;
+constexpr int kPoolThreads = 320;
 
-// Sizes that follow from the rank and the planes.  Two CTAs share an SM up to rank 64, unless the call is `roomy`: too
-// small to give every SM one, so that a deeper ring is worth more. 
-struct PoolTermLayout {
-  int tn;               // tokens a tile
-  int rpad;             // floats a token of the partial sums
-  uint32_t stage;       // bytes
-  uint32_t stages;
-  uint32_t plane;       // bytes of one 64-rank chunk of one plane
-  uint32_t planes_at, exch_at, bytes;
+struct PoolTile {
+  int ad, lo, cnt, rank;
+  float scale;
 };
-__host__ __device__ constexpr PoolTermLayout pool_term_layout(int r, int planes, bool roomy) {
-  PoolTermLayout l{};
+struct PoolWalk {
+  int per, ad0;      // this thread's adapters: ad0 .. ad0 + per
+  int before, sum;   // tiles before them, and theirs
+  int tiles;         // of all
+  int2 group0;       // what is known of ad0
+  int rank0;
+  float scale0;
+};
+
+__device__ __forceinline__ PoolWalk pool_walk(const PoolArgs &p, int tn, int *warp_sum) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  PoolWalk w;
+  w.per = (p.n + kPoolThreads - 1) / kPoolThreads;
+  w.ad0 = tid * w.per;
+  w.group0 = make_int2(0, 0);
+  w.sum = w.rank0 = 0;
+  w.scale0 = 0.0f;
+  if (w.ad0 < p.n) {
+    w.group0 = pool_group(p, w.ad0);
+    w.rank0 = pool_rank(p, w.ad0);
+    w.scale0 = p.scales[w.ad0];
+    w.sum = (w.group0.y - w.group0.x + tn - 1) / tn;
+    for (int i = 1; i < w.per && w.ad0 + i < p.n; ++i) {
+      const int2 g = pool_group(p, w.ad0 + i);
+      w.sum += (g.y - g.x + tn - 1) / tn;
+    }
+  }
+  int inc = w.sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  w.before = inc - w.sum;
+  w.tiles = 0;
+#pragma unroll
+  for (int i = 0; i < kPoolThreads / 32; ++i) {
+    if (i < warp) w.before += warp_sum[i];
+    w.tiles += warp_sum[i];
+  }
+  return w;
+}
+
+// *out = the tile (an empty one past the last); the caller synchronises.
+__device__ __forceinline__ void pool_find(const PoolArgs &p, const PoolWalk &w, int tn, int tile, PoolTile *out) {
+  if (tile >= w.tiles && threadIdx.x == 0) {
+    out->ad = out->lo = out->cnt = out->rank = 0;
+    out->scale = 0.0f;
+  }
+  if (tile >= w.before && tile < w.before + w.sum) {
+    int2 g = w.group0;
+    int ad = w.ad0, t = tile - w.before, nt;
+    while (t >= (nt = (g.y - g.x + tn - 1) / tn)) {
+      t -= nt;
+      g = pool_group(p, ++ad);
+    }
+    out->ad = ad;
+    out->lo = g.x + t * tn;
+    out->cnt = min(tn, g.y - out->lo);
+    out->rank = ad > w.ad0 ? pool_rank(p, ad) : w.rank0;
+    out->scale = ad > w.ad0 ? p.scales[ad] : w.scale0;
+  }
+}
+
+// The loads of a tile's token rows, four rows a lane of warp 0: whole runs of 32 and the rest (masks over lanes).
+struct PoolRowLoads {
+  uint32_t tiles, gathers;
+  __device__ __forceinline__ uint32_t bytes() const { return __popc(tiles) * 4096u + __popc(gathers) * 512u; }
+};
+__device__ __forceinline__ PoolRowLoads pool_row_loads(const PoolArgs &p, const PoolTile &t, int tn, int lane, int4 *row4) {
+  const int4 rows = t.cnt > 0 ? pool_rows(p, t.lo + 4 * min(lane, tn / 4 - 1), t.lo + t.cnt - 1) : make_int4(0, 0, 0, 0);
+  const bool mine = 4 * lane < t.cnt, run = pool_run32(rows, lane, 4 * lane, t.cnt, true);
+  PoolRowLoads l;
+  l.tiles = __ballot_sync(0xffffffffu, run && (lane & 7) == 0 && mine);
+  l.gathers = __ballot_sync(0xffffffffu, !run && mine);
+  if (lane < 16) row4[lane] = rows;
+  __syncwarp();
+  return l;
+}
+// One thread: columns [x, x + 64) of the tile's rows, moved down by `down` rows, to dst.
+__device__ __forceinline__ void pool_load_rows(const PoolRowLoads &l, const int4 *row4, uint8_t *dst, const CUtensorMap *gather,
+                                               const CUtensorMap *tile, uint64_t *bar, int x, int down) {
+  for (uint32_t m = l.tiles; m; m &= m - 1) {
+    const int i = __ffs(m) - 1;
+    ptx::tma_load_2d(dst + i * 512, tile, bar, x, row4[i].x + down);
+  }
+  for (uint32_t m = l.gathers; m; m &= m - 1) {
+    const int i = __ffs(m) - 1;
+    const int4 y = row4[i];
+    ptx::tma_gather4(dst + i * 512, gather, bar, x, make_int4(y.x + down, y.y + down, y.z + down, y.w + down));
+  }
+}
+
+// Descriptor words (128-byte swizzle, groups of eight rows 1024 bytes apart): the high one is the same for all operands,
+// the low one is the address and the distance of 64-element blocks, which MN-major operands use (8192 bytes); 16
+// elements on, a K-major operand is 32 bytes away and an MN-major one 2048.
+constexpr uint32_t kPoolDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__host__ __device__ constexpr uint32_t pool_desc_lbo(bool mn) { return mn ? ((8192u >> 4) - (16u >> 4)) << 16 : 0u; }
+__host__ __device__ constexpr uint32_t pool_desc_16(bool mn) { return mn ? 128u : 2u; }
+
+// ---------------------------------------------------------------------------
+// down: g CTAs of a cluster take a tile of 64 tokens (32 above rank 128) and sum a part of the long dimension each,
+// with the accumulator's rows as ranks and its columns as tokens.  The steps of 64 go round four accumulators, which
+// keeps each one's chain of float32 additions short (the tensor cores' additions cut off: one chain over 1400 elements
+// was 3e-6 off, all to one side).  Each CTA leaves its float32 partial sums in shared memory; each then adds up a share
+// of the tokens over the g CTAs, in CTA order, through distributed shared memory, and writes the planes: no partial
+// planes in HBM, no further launch, and the same bits every time.  g, a divisor of the cluster, follows on the device
+// from the number of tiles.
+//   warp 0  loads; warp 1  products; warps 2..9  accumulators -> shared memory; all  the sums
+// W_MN false: W is [n][r][len], K-major (T: A); true: [n][len][r], MN-major (U: B).
+// ---------------------------------------------------------------------------
+constexpr uint32_t kPoolDownTmem = 256;
+// Shared memory: two CTAs an SM, or all of it for one.
+constexpr uint32_t kPoolHalfBytes = 107 * 1024, kPoolFullBytes = 218 * 1024;
+
+struct PoolDownLayout {
+  int tn;        // tokens a tile
+  int rpad;      // floats a token of the partial sums
+  uint32_t stage, stages, exch_at, bytes;
+};
+// roomy: the call is too small to give every SM a CTA, so that a deeper ring is worth more than a second one.
+__host__ __device__ constexpr PoolDownLayout pool_down_layout(int r, bool roomy) {
+  PoolDownLayout l{};
   l.tn = r <= 128 ? 64 : 32;
   l.rpad = r <= 64 ? 64 : r <= 128 ? 128 : 256;
-  l.stage = l.tn * 128u + l.rpad * 128u;  // token rows and W1's
-  if (l.stage < 16384u) l.stage = 16384u;  // a block of W2
-  l.plane = l.tn * 128u;
-  const uint32_t budget = r <= 64 && !roomy ? 107u * 1024u : kPoolTermMostBytes, p_bytes = (r + 63) / 64 * planes * l.plane;
-  const uint32_t exch = l.tn * l.rpad * 4u > 8 * kPoolWarpBuf * 4u ? l.tn * l.rpad * 4u : 8 * kPoolWarpBuf * 4u;
-  const uint32_t fit = (budget - p_bytes - exch) / l.stage;
+  l.stage = l.tn * 128u + l.rpad * 128u;  // token rows, then W's
+  const uint32_t exch = l.tn * l.rpad * 4u;
+  const uint32_t fit = ((r <= 128 && !roomy ? kPoolHalfBytes : kPoolFullBytes) - exch) / l.stage;
   l.stages = fit < kPoolMostStages ? fit : kPoolMostStages;
-  l.planes_at = l.stages * l.stage;
-  l.exch_at = l.planes_at + p_bytes;
+  l.exch_at = l.stages * l.stage;
   l.bytes = l.exch_at + exch;
   return l;
 }
-static_assert(pool_term_layout(64, 3, false).stages >= 3 && pool_term_layout(128, 3, false).stages >= 3 &&
-                  pool_term_layout(256, 3, false).stages >= 3,
+static_assert(pool_down_layout(64, false).stages >= 3 && pool_down_layout(128, false).stages >= 3 && pool_down_layout(256, false).stages >= 3,
               "a ring of three stages at least");
-static_assert(pool_smem_bytes(pool_term_layout(64, 3, false).bytes) + 2048 <= 114 * 1024 &&
-                  pool_smem_bytes(pool_term_layout(256, 3, false).bytes) <= 225 * 1024,
-              "shared memory");
 
-struct PoolTermArgs {
+struct PoolDownArgs {
   PoolArgs p;
-  int64_t len;         // columns of V
-  int64_t cols, ldo;   // of Out
-  void *out;           // nullable: P alone
-  __nv_bfloat16 *P;    // nullable [3, M, r]
-  int planes;          // used for Out
-  PoolTermLayout l;
+  int64_t len;       // columns of V
+  __nv_bfloat16 *P;  // [3, M, r]
+  PoolDownLayout l;
+};
+
+template <bool W_MN>
+__global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                                    const __grid_constant__ CUtensorMap tmV,
+                                                                    const __grid_constant__ CUtensorMap tmVt, const PoolDownArgs a) {
+  extern __shared__ uint8_t pool_raw[];
+  __shared__ int4 row4[16];
+  __shared__ int warp_sum[kPoolThreads / 32];
+  __shared__ PoolTile tile_s;
+  constexpr uint32_t kWLbo = pool_desc_lbo(W_MN), kW16 = pool_desc_16(W_MN);
+  const PoolArgs &p = a.p;
+  const PoolDownLayout &l = a.l;
+  const PoolSmem sm = pool_smem(pool_raw, l.bytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tn = l.tn;
+  const uint32_t stages = l.stages, v_bytes = tn * 128u;
+  uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
+  float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
+  if (tid < 3) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmV : &tmVt);
+  const uint32_t tmem = pool_setup(sm, kPoolDownTmem, kPoolBars);
+  const PoolWalk walk = pool_walk(p, tn, warp_sum);
+  // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
+  const int cluster = static_cast<int>(ptx::cluster_nctarank()), crank = static_cast<int>(ptx::cluster_ctarank());
+  int g = cluster;
+  while (g > 1 && (static_cast<int64_t>(walk.tiles) * g > gridDim.x || cluster % g)) --g;
+  const int q = crank % g, peers = crank - q;  // the g CTAs from rank `peers` of the cluster
+  const int k_steps = static_cast<int>((a.len + 63) / 64), k_per = (k_steps + g - 1) / g;
+  const int nrb = (p.r + 127) / 128, acc_cols = tn * nrb;  // one of the four accumulators
+  RingPos pos;
+  uint32_t sum_phase = 0, issued = 0;
+  bool ok = true;
+  // all CTAs of a cluster walk as long as the first of its tiles exists
+  for (int lead = (blockIdx.x - crank) / g; lead < walk.tiles; lead += gridDim.x / g) {
+    pool_find(p, walk, tn, lead + crank / g, &tile_s);
+    __syncthreads();
+    const int ad = tile_s.ad, lo = tile_s.lo, cnt = tile_s.cnt, rank = tile_s.rank;
+    const int kb = rank > 0 ? min(q * k_per, k_steps) : 0, ke = rank > 0 ? min(k_steps, kb + k_per) : 0;
+    const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, W_MN ? 1 : 0, 0);
+    if (warp == 0) {
+      const PoolRowLoads rows = pool_row_loads(p, tile_s, tn, lane, row4);
+      if (ok && ptx::elect_one()) {
+        // W's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
+        const int w_loads = W_MN ? (p.r + 63) / 64 : nrb;
+        const uint32_t bytes = w_loads * (W_MN ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u) + rows.bytes();
+        for (int ks = kb; ks < ke; ++ks) {
+          if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
+          uint8_t *st = sm.buf + pos.s * l.stage;
+          uint64_t *bar = &full[pos.s];
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+          for (int i = 0; i < w_loads; ++i)
+            ptx::tma_load_3d(st + v_bytes + i * (W_MN ? 8192 : 16384), &tmW, bar, W_MN ? i * 64 : ks * 64, W_MN ? ks * 64 : i * 128,
+                             ad);
+          pool_load_rows(rows, row4, st, &tmV, &tmVt, bar, ks * 64, 0);
+          ++issued;
+          pos.next(stages);
+        }
+        if (!ok) pool_fail(sm, p.status);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (ok && ptx::elect_one()) {
+        const uint32_t v_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
+        for (int ks = kb; ks < ke; ++ks) {
+          if (!ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t v = v_lo + pos.s * (l.stage >> 4), w = v + (v_bytes >> 4) + kWLbo, d = tmem + ((ks - kb) & 3) * acc_cols;
+          const uint32_t more = ks - kb >= 4 ? 1u : 0u;
+#pragma unroll
+          for (int k16 = 0; k16 < 4; ++k16)
+            ptx::mma_bf16_lohi(d, w + k16 * kW16, kPoolDescHi, v + k16 * 2, kPoolDescHi, idesc, k16 ? 1u : more);
+          if (nrb > 1) {  // ranks 128 and up
+#pragma unroll
+            for (int k16 = 0; k16 < 4; ++k16)
+              ptx::mma_bf16_lohi(d + tn, w + 1024 + k16 * kW16, kPoolDescHi, v + k16 * 2, kPoolDescHi, idesc, k16 ? 1u : more);
+          }
+          ptx::mma_commit(&empty[pos.s]);
+          pos.next(stages);
+        }
+        if (ok && ke > kb) ptx::mma_commit(sum_full);
+        if (!ok) pool_fail(sm, p.status);
+      }
+      __syncwarp();
+    } else {
+      const int quad = warp & 3, set = (warp - 2) >> 2;
+      if (ke > kb && ok) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(sum_full, sum_phase, sm.abort_flag));
+        sum_phase ^= 1;
+        if (!ok && lane == 0) pool_fail(sm, p.status);
+      }
+      ptx::tc_fence_after();
+      const int nacc = ok ? min(4, ke - kb) : 0, c_end = min(cnt, (set + 1) * (tn / 2));
+      for (int rb = 0; rb < nrb; ++rb) {
+        if (rb * 128 + quad * 32 >= p.r) break;
+        for (int c0 = set * (tn / 2); c0 < c_end; c0 += 16) {
+          const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + rb * tn + c0;
+          float x[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            if (i >= nacc) break;
+            uint32_t v[16], w[16];
+            ptx::tmem_ld16(from + i * acc_cols, v);
+            if (i + 1 < nacc) ptx::tmem_ld16(from + (i + 1) * acc_cols, w);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]) + (i + 1 < nacc ? __uint_as_float(w[j]) : 0.0f);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c0 + j < c_end) exch[(c0 + j) * l.rpad + rb * 128 + quad * 32 + lane] = x[j];
+        }
+      }
+      ptx::tc_fence_before();
+    }
+
+    pool_cluster_sync();
+    // this CTA's share of the tokens, four ranks a thread
+    {
+      const int pt = (cnt + g - 1) / g, c_lo = min(cnt, q * pt), c_hi = min(cnt, c_lo + pt), n4 = p.r / 4;
+      const uint32_t exch_addr = ptx::smem_addr(exch);
+      for (int e = tid; e < (c_hi - c_lo) * n4; e += kPoolThreads) {
+        const int c = c_lo + e / n4, j = e % n4 * 4;
+        const int t = pool_token(p, lo + c);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (j < rank) {
+          const uint32_t src = exch_addr + (c * l.rpad + j) * 4;
+          float4 u[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < g) u[r] = ptx::ld_cluster_f32x4(ptx::mapa_shared(src, peers + r));
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < g) { x.x += u[r].x; x.y += u[r].y; x.z += u[r].z; x.w += u[r].w; }
+        }
+        if (t < 0) continue;
+        __nv_bfloat16 *out = a.P + static_cast<int64_t>(t) * p.r + j;
+#pragma unroll
+        for (int pl = 0; pl < kPoolPlanes; ++pl) {
+          const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+          x.x -= bf16lo_to_f32(h.x);
+          x.y -= bf16hi_to_f32(h.x);
+          x.z -= bf16lo_to_f32(h.y);
+          x.w -= bf16hi_to_f32(h.y);
+          *reinterpret_cast<uint2 *>(out + pl * p.M * p.r) = h;
+        }
+      }
+    }
+    pool_cluster_sync();  // the partial sums, and the tile, are done with
+  }
+  if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the thread that loads
+  pool_teardown(tmem, kPoolDownTmem);
+}
+
+// ---------------------------------------------------------------------------
+// up: one unit is a tile of 64 tokens (32 where the planes are many) and every runs-th block of 128 features.  P's rows
+// come once, W's blocks stream through the ring, rows of the accumulator are features.  Two sets of four epilogue warps
+// take turns with the blocks, each with two of four accumulators: while one is added to Out, the next is multiplied.
+// The lanes hold features; where Out's rows are 16-byte aligned, 16 tokens at a time pass through shared memory, so that
+// four lanes (bf16; eight for float32) then share a token's 32 features in 16-byte pieces (element by element the
+// epilogue took 47 instructions an element and warp, and bound the kernel on issue).  The pieces are loaded an item
+// ahead, and the lines of the next block are prefetched to L2 (203 -> 172 us for 4096 tokens on 22016 float32 columns).
+// Tiles of up to four tokens go straight from the accumulator to Out, and other outputs, odd strides or columns of a
+// wider tensor, element by element.
+//   warp 0  loads; warp 1  products; warps 2..9  Out += s accumulator
+// W_MN false: W is [n][cols][r], K-major (Y: B); true: [n][r][cols], MN-major (dX: A).
+// ---------------------------------------------------------------------------
+constexpr uint32_t kPoolUpTmem = 256;
+// Shared memory of a warp's 16 tokens x 32 features: a pitch of 36 floats keeps 16-byte pieces aligned and both
+// directions without bank conflicts.
+constexpr int kPoolPitch = 36, kPoolWarpBuf = 16 * kPoolPitch;
+constexpr uint32_t kPoolUpStage = 16384;  // 128 features x 64 ranks
+
+struct PoolUpLayout {
+  int tn;          // tokens a tile
+  uint32_t plane;  // bytes of one 64-rank chunk of one plane
+  uint32_t stages, planes_at, buf_at, bytes;
+};
+__host__ __device__ constexpr PoolUpLayout pool_up_layout(int r, int planes) {
+  PoolUpLayout l{};
+  const int chunks = (r + 63) / 64 * planes;
+  l.tn = chunks <= 6 ? 64 : 32;
+  l.plane = l.tn * 128u;
+  const uint32_t rest = chunks * l.plane + 8 * kPoolWarpBuf * 4u;
+  l.stages = (kPoolHalfBytes - rest) / kPoolUpStage;
+  l.planes_at = l.stages * kPoolUpStage;
+  l.buf_at = l.planes_at + chunks * l.plane;
+  l.bytes = l.planes_at + rest;
+  return l;
+}
+static_assert(pool_up_layout(64, 3).stages >= 3 && pool_up_layout(128, 3).stages >= 2 && pool_up_layout(256, 3).stages >= 2 &&
+                  pool_up_layout(64, 2).stages <= kPoolMostStages,
+              "a ring of two stages at least");
+static_assert(pool_smem_bytes(kPoolHalfBytes) + 2048 <= 114 * 1024 && pool_smem_bytes(kPoolFullBytes) <= 225 * 1024, "shared memory");
+
+struct PoolUpArgs {
+  PoolArgs p;
+  int64_t cols, ldo;  // of Out
+  void *out;
+  int planes;
+  PoolUpLayout l;
 };
 
 __device__ __forceinline__ float pool_load(const float *p) { return __ldcg(p); }
@@ -340,107 +622,42 @@ struct PoolPiece<__nv_bfloat16> {
   __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = y; }
 };
 
-// The tile at hand.
-struct PoolTile {
-  int ad, lo, cnt, rank;
-  float scale;
-};
-
 template <bool W_MN, typename O, bool VEC>
-__global__ void __launch_bounds__(kPoolTermThreads, 2)
-    pool_term_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmW2,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVt, const PoolTermArgs a) {
+__global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                                  const __grid_constant__ CUtensorMap tmP,
+                                                                  const __grid_constant__ CUtensorMap tmPt, const PoolUpArgs a) {
   extern __shared__ uint8_t pool_raw[];
   __shared__ int64_t row_at[64];  // of the tile's tokens in Out, in elements; -1: not a token
   __shared__ int4 row4[16];
-  __shared__ int warp_sum[kPoolTermThreads / 32];
+  __shared__ int warp_sum[kPoolThreads / 32];
   __shared__ PoolTile tile_s;
-  // descriptor words (128-byte swizzle, groups of eight rows 1024 bytes apart): the high one is the same for all operands,
-  // the low one is the address and the distance of 64-element blocks, which MN-major operands use (8192 bytes); 16
-  // elements on, a K-major operand is 32 bytes away and an MN-major one 2048
-  constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-  constexpr uint32_t kWLbo = W_MN ? ((8192u >> 4) - (16u >> 4)) << 16 : 0u, kW16 = W_MN ? 128u : 2u;
+  constexpr uint32_t kWLbo = pool_desc_lbo(W_MN), kW16 = pool_desc_16(W_MN);
   const PoolArgs &p = a.p;
-  const PoolTermLayout &l = a.l;
+  const PoolUpLayout &l = a.l;
   const PoolSmem sm = pool_smem(pool_raw, l.bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tn = l.tn;
-  const uint32_t stages = l.stages, v_bytes = tn * 128u;
-  uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
-  uint64_t *acc_full = sum_full + 1, *acc_empty = acc_full + 4;
-  float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
-  uint8_t *planes = sm.buf + l.planes_at;
-  if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &tmW1 : tid == 1 ? &tmW2 : tid == 2 ? &tmV : &tmVt);
-  const uint32_t tmem = pool_setup(sm, kPoolTermTmem, 2 * kPoolMostStages + 5);
-
-  // this thread's adapters, ad0 .. ad0 + per: what is known of the first stays in registers
-  const int per = (p.n + kPoolTermThreads - 1) / kPoolTermThreads, ad0 = tid * per;
-  int2 group0 = make_int2(0, 0);
-  int sum = 0, rank0 = 0;
-  float scale0 = 0.0f;
-  if (ad0 < p.n) {
-    group0 = pool_group(p, ad0);
-    rank0 = pool_rank(p, ad0);
-    scale0 = p.scales[ad0];
-    sum = (group0.y - group0.x + tn - 1) / tn;
-    for (int i = 1; i < per && ad0 + i < p.n; ++i) {
-      const int2 grp = pool_group(p, ad0 + i);
-      sum += (grp.y - grp.x + tn - 1) / tn;
-    }
-  }
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
-  int before = inc - sum, tiles = 0;
-#pragma unroll
-  for (int w = 0; w < kPoolTermThreads / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    tiles += warp_sum[w];
-  }
-
-  // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
-  const int cluster = static_cast<int>(ptx::cluster_nctarank()), crank = static_cast<int>(ptx::cluster_ctarank());
-  int g = cluster;
-  while (g > 1 && (static_cast<int64_t>(tiles) * g > gridDim.x || cluster % g)) --g;
-  const int q = crank % g, peers = crank - q;  // the g CTAs from rank `peers` of the cluster
-  const int k_steps = static_cast<int>((a.len + 63) / 64), k_per = (k_steps + g - 1) / g;
-  const int nblk = a.out ? static_cast<int>((a.cols + 127) / 128) : 0;
-  const int nrb = (p.r + 127) / 128, acc_cols = tn * nrb;  // one of the four accumulators of the sums
+  const uint32_t stages = l.stages;
+  uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *p_full = sm.bars + 2 * kPoolMostStages;
+  uint64_t *acc_full = p_full + 1, *acc_empty = acc_full + 4;
+  if (tid < 3) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmP : &tmPt);
+  const uint32_t tmem = pool_setup(sm, kPoolUpTmem, 2 * kPoolMostStages + 5);
+  const PoolWalk walk = pool_walk(p, tn, warp_sum);
+  // runs of blocks a tile: as many as give every CTA a unit
+  const int nblk = static_cast<int>((a.cols + 127) / 128);
+  const int g = min(max(static_cast<int>(gridDim.x) / max(walk.tiles, 1), 1), nblk);
+  const int64_t units = static_cast<int64_t>(walk.tiles) * g;
   RingPos pos;
-  uint32_t sum_phase = 0, issued = 0, blocks = 0;  // blocks: accumulators of features used so far
+  uint32_t p_phase = 0, issued = 0, blocks = 0;  // blocks: accumulators used so far
   bool ok = true;
-  // all CTAs of a cluster walk as long as the first of its tiles exists
-  for (int lead = (blockIdx.x - crank) / g; lead < tiles; lead += gridDim.x / g) {
-    const int tile = lead + crank / g;
-    if (tile >= tiles && tid == 0) {
-      tile_s.ad = tile_s.lo = tile_s.cnt = tile_s.rank = 0;
-      tile_s.scale = 0.0f;
-    }
-    if (tile >= before && tile < before + sum) {  // among this thread's
-      int2 grp = group0;
-      int ad = ad0, t = tile - before, nt;
-      while (t >= (nt = (grp.y - grp.x + tn - 1) / tn)) {
-        t -= nt;
-        grp = pool_group(p, ++ad);
-      }
-      tile_s.ad = ad;
-      tile_s.lo = grp.x + t * tn;
-      tile_s.cnt = min(tn, grp.y - tile_s.lo);
-      tile_s.rank = ad > ad0 ? pool_rank(p, ad) : rank0;
-      tile_s.scale = ad > ad0 ? p.scales[ad] : scale0;
-    }
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int tile = static_cast<int>(u / g), q = static_cast<int>(u - static_cast<int64_t>(tile) * g);
+    pool_find(p, walk, tn, tile, &tile_s);
     __syncthreads();
     const int ad = tile_s.ad, lo = tile_s.lo, cnt = tile_s.cnt, rank = tile_s.rank;
-    const int kb = rank > 0 ? min(q * k_per, k_steps) : 0, ke = rank > 0 ? min(k_steps, kb + k_per) : 0;
-    const int nch = rank > 0 ? (rank + 63) / 64 : 0;
-    const int mine = rank > 0 && nblk > q ? (nblk - q + g - 1) / g : 0;  // blocks q, q + g, ...
+    const int nch = (rank + 63) / 64;
+    const int mine = rank > 0 ? (nblk - q + g - 1) / g : 0;  // blocks q, q + g, ...
     const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, W_MN ? 1 : 0, 0);
     const int quad = warp & 3, set = (warp - 2) >> 2;
-
     // epilogue: a warp's items are (block, group of tokens), the blocks being those whose accumulator is its set's
     constexpr int kGroup = PoolPiece<O>::kTokens, kElems = PoolPiece<O>::kElems, kLanes = 32 / kElems, kRows = 32 / kLanes;
     constexpr int kPieces = kGroup / kRows;
@@ -470,195 +687,53 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
       }
     };
 
-    // warp 0's thread: stages [i0, i1) of W2's blocks, 64 ranks of a block each
-    auto load_w2 = [&](int i0, int i1) {
-      int b = i0 / max(nch, 1), ch = i0 - b * nch;
-      for (int i = i0; i < i1; ++i) {
-        if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
-        const int f = (q + b * g) * 128, x = ch * 64;
-        uint8_t *st = sm.buf + pos.s * l.stage;
-        ptx::mbar_arrive_expect_tx(&full[pos.s], 16384u);
-        if (W_MN) {
-          ptx::tma_load_3d(st, &tmW2, &full[pos.s], f, x, ad);
-          ptx::tma_load_3d(st + 8192, &tmW2, &full[pos.s], f + 64, x, ad);
-        } else {
-          ptx::tma_load_3d(st, &tmW2, &full[pos.s], x, f, ad);
-        }
-        if (++ch == nch) { ch = 0; ++b; }
-        ++issued;
-        pos.next(stages);
-      }
-    };
-
-    // ------------------------------------------------------------ 1. the sums over the long dimension
     if (warp == 0) {
-      const int4 rows = cnt > 0 ? pool_rows(p, lo + 4 * min(lane, tn / 4 - 1), lo + cnt - 1) : make_int4(0, 0, 0, 0);
-      const bool mine4 = 4 * lane < cnt;
-      const bool run = pool_run32(rows, lane, 4 * lane, cnt, true);
-      const uint32_t tile_loads = __ballot_sync(0xffffffffu, run && (lane & 7) == 0 && mine4);
-      const uint32_t gathers = __ballot_sync(0xffffffffu, !run && mine4);
-      if (lane < 16) row4[lane] = rows;
-      __syncwarp();
-      if (ok && ptx::elect_one()) {
-        // W1's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
-        const int w_loads = W_MN ? (p.r + 63) / 64 : nrb;
-        const uint32_t w_box = W_MN ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u;
-        const uint32_t bytes = w_loads * w_box + __popc(tile_loads) * 4096u + __popc(gathers) * 512u;
-        for (int ks = kb; ks < ke; ++ks) {
+      const PoolRowLoads rows = pool_row_loads(p, tile_s, tn, lane, row4);
+      if (ok && mine > 0 && ptx::elect_one()) {
+        // the first blocks of W, then P's rows, then the other blocks
+        int b = 0, ch = 0;
+        for (int i = 0; i < mine * nch; ++i) {
+          if (i == min(static_cast<int>(stages), mine * nch) - 1) {
+            ptx::mbar_arrive_expect_tx(p_full, nch * a.planes * rows.bytes());
+            for (int c = 0; c < nch * a.planes; ++c)
+              pool_load_rows(rows, row4, sm.buf + l.planes_at + c * l.plane, &tmP, &tmPt, p_full, c / a.planes * 64,
+                             c % a.planes * static_cast<int>(p.M));
+          }
           if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
-          uint8_t *st = sm.buf + pos.s * l.stage;
-          uint64_t *bar = &full[pos.s];
-          ptx::mbar_arrive_expect_tx(bar, bytes);
-          for (int i = 0; i < w_loads; ++i)
-            ptx::tma_load_3d(st + v_bytes + i * (W_MN ? 8192 : 16384), &tmW1, bar, W_MN ? i * 64 : ks * 64, W_MN ? ks * 64 : i * 128,
-                             ad);
-          for (uint32_t m = tile_loads; m; m &= m - 1) {
-            const int i = __ffs(m) - 1;
-            ptx::tma_load_2d(st + i * 512, &tmVt, bar, ks * 64, row4[i].x);
+          const int f = (q + b * g) * 128, x = ch * 64;
+          uint8_t *st = sm.buf + pos.s * kPoolUpStage;
+          ptx::mbar_arrive_expect_tx(&full[pos.s], kPoolUpStage);
+          if (W_MN) {
+            ptx::tma_load_3d(st, &tmW, &full[pos.s], f, x, ad);
+            ptx::tma_load_3d(st + 8192, &tmW, &full[pos.s], f + 64, x, ad);
+          } else {
+            ptx::tma_load_3d(st, &tmW, &full[pos.s], x, f, ad);
           }
-          for (uint32_t m = gathers; m; m &= m - 1) {
-            const int i = __ffs(m) - 1;
-            ptx::tma_gather4(st + i * 512, &tmV, bar, ks * 64, row4[i]);
-          }
+          if (++ch == nch) { ch = 0; ++b; }
           ++issued;
           pos.next(stages);
         }
-        // the first of W2's blocks follow through the ring while the sums are joined
-        if (ok) load_w2(0, min(mine * nch, static_cast<int>(stages)));
         if (!ok) pool_fail(sm, p.status);
       }
       __syncwarp();
     } else if (warp == 1) {
-      if (ok && ptx::elect_one()) {
-        const uint32_t v_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
-        for (int ks = kb; ks < ke; ++ks) {
-          if (!ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag)) { ok = false; break; }
-          ptx::tc_fence_after();
-          const uint32_t v = v_lo + pos.s * (l.stage >> 4), w = v + (v_bytes >> 4) + kWLbo, d = tmem + ((ks - kb) & 3) * acc_cols;
-          const uint32_t more = ks - kb >= 4 ? 1u : 0u;
-#pragma unroll
-          for (int k16 = 0; k16 < 4; ++k16)
-            ptx::mma_bf16_lohi(d, w + k16 * kW16, kDescHi, v + k16 * 2, kDescHi, idesc, k16 ? 1u : more);
-          if (nrb > 1) {  // ranks 128 and up
-#pragma unroll
-            for (int k16 = 0; k16 < 4; ++k16)
-              ptx::mma_bf16_lohi(d + tn, w + 1024 + k16 * kW16, kDescHi, v + k16 * 2, kDescHi, idesc, k16 ? 1u : more);
-          }
-          ptx::mma_commit(&empty[pos.s]);
-          pos.next(stages);
-        }
-        if (ok && ke > kb) ptx::mma_commit(sum_full);
-        if (!ok) pool_fail(sm, p.status);
-      }
-      __syncwarp();
-    } else {
-      if (tid - 64 < tn) {
-        const int t = tid - 64 < cnt ? pool_token(p, lo + tid - 64) : -1;
-        row_at[tid - 64] = t < 0 ? -1 : t * a.ldo;
-      }
-      ptx::named_bar_sync(1, kPoolTermThreads - 64);
-      if (pieces && b_first < mine) {  // the first ones', while the sums are formed
-        load_y(y0, b_first, 0);
-        prefetch_block(b_first);
-      }
-      if (ke > kb && ok) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(sum_full, sum_phase, sm.abort_flag));
-        sum_phase ^= 1;
+      if (mine > 0 && ok) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(p_full, p_phase, sm.abort_flag));
         if (!ok && lane == 0) pool_fail(sm, p.status);
       }
-      ptx::tc_fence_after();
-      const int nacc = ok ? min(4, ke - kb) : 0, c_end = min(cnt, (set + 1) * (tn / 2));
-      for (int rb = 0; rb < nrb; ++rb) {
-        if (rb * 128 + quad * 32 >= p.r) break;
-        for (int c0 = set * (tn / 2); c0 < c_end; c0 += 16) {
-          const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + rb * tn + c0;
-          float x[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            if (i >= nacc) break;
-            uint32_t v[16], w[16];
-            ptx::tmem_ld16(from + i * acc_cols, v);
-            if (i + 1 < nacc) ptx::tmem_ld16(from + (i + 1) * acc_cols, w);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]) + (i + 1 < nacc ? __uint_as_float(w[j]) : 0.0f);
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c0 + j < c_end) exch[(c0 + j) * l.rpad + rb * 128 + quad * 32 + lane] = x[j];
-        }
-      }
-      ptx::tc_fence_before();
-    }
-
-    // ------------------------------------------------------------ 2. the sums over the cluster
-    pool_cluster_sync();
-    {
-      const int pt = (cnt + g - 1) / g, c_lo = min(cnt, q * pt), c_hi = min(cnt, c_lo + pt);
-      const int n4 = (p.r + 15) / 16 * 4;  // groups of 4 ranks; products take 16 at a time
-      const uint32_t exch_addr = ptx::smem_addr(exch), planes_addr = ptx::smem_addr(planes);
-      for (int e = tid; e < (c_hi - c_lo) * n4; e += kPoolTermThreads) {
-        const int c = c_lo + e / n4, j = e % n4 * 4;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (j < rank) {
-          const uint32_t src = exch_addr + (c * l.rpad + j) * 4;
-#pragma unroll
-          for (int r0 = 0; r0 < 8; r0 += 4) {
-            if (r0 >= g) break;
-            float4 u[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (r0 + r < g) u[r] = ptx::ld_cluster_f32x4(ptx::mapa_shared(src, peers + r0 + r));
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (r0 + r < g) { x.x += u[r].x; x.y += u[r].y; x.z += u[r].z; x.w += u[r].w; }
-          }
-        }
-        const int t = a.P ? pool_token(p, lo + c) : -1;
-        const uint32_t dst = planes_addr + (j >> 6) * a.planes * l.plane + c * 128 + ((((j >> 3) & 7) ^ (c & 7)) << 4) + (j & 4) * 2;
-#pragma unroll
-        for (int pl = 0; pl < kPoolPlanes; ++pl) {
-          const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-          x.x -= bf16lo_to_f32(h.x);
-          x.y -= bf16hi_to_f32(h.x);
-          x.z -= bf16lo_to_f32(h.y);
-          x.w -= bf16hi_to_f32(h.y);
-          if (t >= 0 && j < p.r) *reinterpret_cast<uint2 *>(a.P + (static_cast<int64_t>(pl) * p.M + t) * p.r + j) = h;
-          if (a.out && pl < a.planes) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-              if (r < g) ptx::st_cluster_u32x2(ptx::mapa_shared(dst + pl * l.plane, peers + r), h);
-          }
-        }
-      }
-    }
-    ptx::fence_proxy_async_cluster();  // the planes are read by the tensor cores
-    pool_cluster_sync();
-
-    // ------------------------------------------------------------ 3. the features
-    if (warp == 0) {
-      if (ok && ptx::elect_one()) {
-        load_w2(min(mine * nch, static_cast<int>(stages)), mine * nch);
-        if (!ok) pool_fail(sm, p.status);
-      }
-      __syncwarp();
-    } else if (warp == 1) {
-      ptx::fence_proxy_async_cluster();
       const uint32_t p_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
       // one thread issues a chunk of a block's products
       auto issue = [&](uint32_t acc, int ch) {
         ptx::tc_fence_after();
         const int left = min(64, rank - ch * 64);  // a multiple of 8; products go 16 ranks at a time
-        const uint32_t w = p_lo + pos.s * (l.stage >> 4) + kWLbo, pc = p_lo + ((l.planes_at + ch * a.planes * l.plane) >> 4);
+        const uint32_t w = p_lo + pos.s * (kPoolUpStage >> 4) + kWLbo, pc = p_lo + ((l.planes_at + ch * a.planes * l.plane) >> 4);
 #pragma unroll
         for (int k16 = 0; k16 < 4; ++k16) {
           if (k16 * 16 >= left) break;
 #pragma unroll
           for (int pl = 0; pl < kPoolPlanes; ++pl)
             if (pl < a.planes)
-              ptx::mma_bf16_lohi(tmem + acc * 64, w + k16 * kW16, kDescHi, pc + pl * (l.plane >> 4) + k16 * 2, kDescHi, idesc,
+              ptx::mma_bf16_lohi(tmem + acc * 64, w + k16 * kW16, kPoolDescHi, pc + pl * (l.plane >> 4) + k16 * 2, kPoolDescHi, idesc,
                                  (ch || k16 || pl) ? 1u : 0u);
         }
         ptx::mma_commit(&empty[pos.s]);
@@ -691,7 +766,7 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
             if (!ok) break;
             if (ch == nch - 1) {
-              uint8_t *st = sm.buf + pos.s * l.stage;
+              uint8_t *st = sm.buf + pos.s * kPoolUpStage;
               const int at_rank = rank & 63;
 #pragma unroll
               for (int i = lane; i < 128; i += 32) {
@@ -711,6 +786,15 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
       }
       __syncwarp();
     } else {
+      if (tid - 64 < tn) {
+        const int t = tid - 64 < cnt ? pool_token(p, lo + tid - 64) : -1;
+        row_at[tid - 64] = t < 0 ? -1 : t * a.ldo;
+      }
+      ptx::named_bar_sync(1, kPoolThreads - 64);
+      if (pieces && b_first < mine) {  // the first ones', while the products are formed
+        load_y(y0, b_first, 0);
+        prefetch_block(b_first);
+      }
       const float s = tile_s.scale;
       uint32_t acc = 0, d = 0;
       auto wait = [&](int b) {
@@ -755,7 +839,7 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
           }
         }
       } else if (VEC) {
-        float *buf = exch + (warp - 2) * kPoolWarpBuf;
+        float *buf = reinterpret_cast<float *>(sm.buf + l.buf_at) + (warp - 2) * kPoolWarpBuf;
         auto add_store = [&](PoolPiece<O>(&y)[kPieces], int b, int g0) {
           if (g0 == 0 && !wait(b)) return;
           const int64_t f = static_cast<int64_t>(q + b * g) * 128 + quad * 32 + part * kElems;
@@ -824,11 +908,15 @@ __global__ void __launch_bounds__(kPoolTermThreads, 2)
       }
       if (!ok && lane == 0) pool_fail(sm, p.status);
     }
+    if (mine > 0) p_phase ^= 1;
     blocks += mine;
-    __syncthreads();  // the tile's tokens, planes and buffers are done with
+    __syncthreads();  // the tile's tokens and planes are done with
   }
-  if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the thread that loads
-  pool_teardown(tmem, kPoolTermTmem);
+  if (issued && *sm.abort_flag) {  // the thread that loads
+    ring_drain(full, pos, stages, issued);
+    ptx::mbar_wait(p_full, p_phase ^ 1, nullptr);
+  }
+  pool_teardown(tmem, kPoolUpTmem);
 }
 
 // ---------------------------------------------------------------------------

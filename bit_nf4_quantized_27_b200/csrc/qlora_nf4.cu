@@ -937,7 +937,7 @@ qlora_status check_pool_call(const qlora_adapter_pool *pool, const int32_t *orde
 }
 
 size_t pool_ws_bytes(int64_t M, int32_t r, int for_backward) {
-  return QLORA_STATUS_BYTES + (for_backward ? 2 * align256(static_cast<size_t>(kPoolPlanes) * M * r * 2) : 0);
+  return QLORA_STATUS_BYTES + (for_backward ? 2 : 1) * align256(static_cast<size_t>(kPoolPlanes) * M * r * 2);
 }
 
 PoolArgs pool_args(const qlora_adapter_pool *p, const int32_t *order, const int32_t *offsets, int64_t M, int64_t N,
@@ -1066,49 +1066,65 @@ qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int
   return QLORA_OK;
 }
 
-// P = V W1_a for every grouped token, then, with Out, Out[t] += s_a P[t] W2_a.  Forward (W_MN false): V = X, W1 = A,
-// W2 = B, Out = Y; backward: V = dY, W1 = B, W2 = A, Out = dX.  P: nullable [3, M, r] in HBM.
-template <bool W_MN, typename O>
-qlora_status launch_pool_term_t(const PoolArgs &p, const qlora_adapter_pool *pool, const void *V, int64_t ldv, __nv_bfloat16 *P,
-                                void *Out, int64_t ldo, int dev, int sms, cudaStream_t st) {
-  PoolTermArgs a;
+// P = V W_a for every grouped token.  T: V = X, W = A; U: V = dY, W = B (MN-major).
+template <bool W_MN>
+qlora_status launch_pool_down(const PoolArgs &p, const void *V, int64_t ldv, const void *W, __nv_bfloat16 *P, int dev, int sms,
+                              cudaStream_t st) {
+  const int64_t adapters = std::min<int64_t>(p.n, p.M);
+  PoolDownArgs a;
   a.p = p;
   a.len = W_MN ? p.N : p.K;
+  a.P = P;
+  a.l = pool_down_layout(p.r, (p.M / 64 + adapters) * 8 <= sms);
+  CUtensorMap tmW, tmV, tmVt;
+  if (!(W_MN ? tmap_pool(&tmW, W, p.r, a.len, p.n, 64) : tmap_pool(&tmW, W, a.len, p.r, p.n, std::min(p.r, 128))) ||
+      !tmap_tokens(&tmV, &tmVt, V, a.len, p.M, ldv))
+    return QLORA_ERR_CUDA;
+  static PoolKernelState states[64];
+  auto kernel = pool_down_kernel<W_MN>;
+  const qlora_status s = pool_attributes(kernel, kPoolFullBytes, states[dev]);
+  if (s != QLORA_OK) return s;
+  // CTAs a tile: as many as let the tiles run at once, taken that three of four adapters that may have tokens have a short
+  // tile.  The kernel splits a cluster over several tiles, or walks, where there are more.
+  const int64_t tiles = (p.M + a.l.tn - 1) / a.l.tn + adapters * 3 / 4;
+  int cs = 8, fit = 0;
+  for (;; cs = cs > 2 ? cs - 2 : 1) {
+    if ((fit = pool_fit(kernel, kPoolThreads, a.l.bytes, cs, states[dev], dev)) == 0) return QLORA_ERR_CUDA;
+    if (cs == 1 || fit >= tiles) break;
+  }
+  return launch_pool(kernel, std::min<int64_t>(p.M / a.l.tn + adapters, fit), cs, kPoolThreads, a.l.bytes, st, tmW, tmV, tmVt, a);
+}
+
+// Out[t] += s_a P[t] W_a for every grouped token.  Y: W = B; dX: W = A (MN-major).
+template <bool W_MN, typename O>
+qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo, int dev,
+                              int sms, cudaStream_t st) {
+  PoolUpArgs a;
+  a.p = p;
   a.cols = W_MN ? p.K : p.N;
   a.ldo = ldo;
   a.out = Out;
-  a.P = P;
   a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
-  const int64_t adapters = std::min<int64_t>(p.n, p.M), most = p.M / 64 + adapters;  // tiles at most
-  a.l = pool_term_layout(p.r, a.planes, most * 8 <= sms);
-  CUtensorMap tmW1, tmW2, tmV, tmVt;
-  if (!(W_MN ? tmap_pool(&tmW1, pool->B, p.r, p.N, p.n, 64) : tmap_pool(&tmW1, pool->A, p.K, p.r, p.n, std::min(p.r, 128))) ||
-      !(W_MN ? tmap_pool(&tmW2, pool->A, p.K, p.r, p.n, 64) : tmap_pool(&tmW2, pool->B, p.r, p.N, p.n, 128)) ||
-      !tmap_tokens(&tmV, &tmVt, V, a.len, p.M, ldv))
+  a.l = pool_up_layout(p.r, a.planes);
+  CUtensorMap tmW, tmP, tmPt;
+  if (!(W_MN ? tmap_pool(&tmW, W, a.cols, p.r, p.n, 64) : tmap_pool(&tmW, W, p.r, a.cols, p.n, 128)) ||
+      !tmap_tokens(&tmP, &tmPt, P, p.r, kPoolPlanes * p.M, p.r))
     return QLORA_ERR_CUDA;
+  const int64_t units = (p.M / a.l.tn + std::min<int64_t>(p.n, p.M)) * ((a.cols + 127) / 128);
   auto launch = [&](auto kernel, PoolKernelState &ks) -> qlora_status {
-    const qlora_status s = pool_attributes(kernel, kPoolTermMostBytes, ks);
+    const qlora_status s = pool_attributes(kernel, kPoolHalfBytes, ks);
     if (s != QLORA_OK) return s;
-    // CTAs a tile: as many as let the tiles run at once, taken that three of four adapters that may have tokens have a
-    // short tile.  The kernel splits a cluster over several tiles, or walks, where there are more.
-    const int64_t tiles = (p.M + a.l.tn - 1) / a.l.tn + adapters * 3 / 4;
-    int cs = 8, fit = 0;
-    for (;; cs = cs > 2 ? cs - 2 : 1) {
-      if ((fit = pool_fit(kernel, kPoolTermThreads, a.l.bytes, cs, ks, dev)) == 0) return QLORA_ERR_CUDA;
-      if (cs == 1 || fit >= tiles) break;
-    }
-    return launch_pool(kernel, std::min<int64_t>(p.M / a.l.tn + adapters, fit), cs, kPoolTermThreads, a.l.bytes, st, tmW1, tmW2, tmV,
-                       tmVt, a);
+    return launch_pool(kernel, std::min<int64_t>(units, 2 * sms), 1, kPoolThreads, a.l.bytes, st, tmW, tmP, tmPt, a);
   };
   static PoolKernelState states[2][64];
   const bool vec = aligned(Out, 16) && ldo * sizeof(O) % 16 == 0;
-  return vec ? launch(pool_term_kernel<W_MN, O, true>, states[0][dev]) : launch(pool_term_kernel<W_MN, O, false>, states[1][dev]);
+  return vec ? launch(pool_up_kernel<W_MN, O, true>, states[0][dev]) : launch(pool_up_kernel<W_MN, O, false>, states[1][dev]);
 }
 template <bool W_MN>
-qlora_status launch_pool_term(const PoolArgs &p, const qlora_adapter_pool *pool, const void *V, int64_t ldv, __nv_bfloat16 *P,
-                              void *Out, int64_t ldo, qlora_dtype dt, int dev, int sms, cudaStream_t st) {
-  return dt == QLORA_F32 ? launch_pool_term_t<W_MN, float>(p, pool, V, ldv, P, Out, ldo, dev, sms, st)
-                         : launch_pool_term_t<W_MN, __nv_bfloat16>(p, pool, V, ldv, P, Out, ldo, dev, sms, st);
+qlora_status launch_pool_up(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo, qlora_dtype dt,
+                            int dev, int sms, cudaStream_t st) {
+  return dt == QLORA_F32 ? launch_pool_up_t<W_MN, float>(p, P, W, Out, ldo, dev, sms, st)
+                         : launch_pool_up_t<W_MN, __nv_bfloat16>(p, P, W, Out, ldo, dev, sms, st);
 }
 
 template <typename O>
@@ -1222,7 +1238,9 @@ qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, cons
     const qlora_status s = base_fwd(W, X, M, Y, y_dtype, ws, dev, sms, st);
     if (s != QLORA_OK) return s;
   }
-  return launch_pool_term<false>(a, pool, X, ldx, static_cast<__nv_bfloat16 *>(T_save), Y, ldy, y_dtype, dev, sms, st);
+  __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
+  const qlora_status s = launch_pool_down<false>(a, X, ldx, pool->A, T, dev, sms, st);
+  return s != QLORA_OK ? s : launch_pool_up<false>(a, T, pool->B, Y, ldy, y_dtype, dev, sms, st);
 }
 
 qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
@@ -1234,12 +1252,11 @@ qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, cons
   const __nv_bfloat16 *T = static_cast<const __nv_bfloat16 *>(T_saved);
   qlora_status s;
   if (M > 0) {
-    if ((dX || dA) &&
-        (s = launch_pool_term<true>(a, pool, dY, lddy, dA ? U : nullptr, dX, lddx, dx_dtype, dev, sms, st)) != QLORA_OK)
-      return s;
+    if ((dX || dA) && (s = launch_pool_down<true>(a, dY, lddy, pool->B, U, dev, sms, st)) != QLORA_OK) return s;
+    if (dX && (s = launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, dev, sms, st)) != QLORA_OK) return s;
     if (dA && !T) {
       __nv_bfloat16 *Tw = U + align256(static_cast<size_t>(kPoolPlanes) * M * a.r * 2) / 2;
-      if ((s = launch_pool_term<false>(a, pool, X, ldx, Tw, nullptr, 0, QLORA_F32, dev, sms, st)) != QLORA_OK) return s;
+      if ((s = launch_pool_down<false>(a, X, ldx, pool->A, Tw, dev, sms, st)) != QLORA_OK) return s;
       T = Tw;
     }
   }

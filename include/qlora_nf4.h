@@ -335,8 +335,8 @@ QLORA_API qlora_status qlora_adapter_groups(const int32_t *adapter_of_token, int
                                             int32_t *offsets, void *ws, qlora_stream_t stream);
 
 /* Least workspace of qlora_adapters_fwd (for_backward = 0) and qlora_adapters_bwd
- * (1), and of qlora_linear_fwd_pool and qlora_linear_bwd_pool: QLORA_STATUS_BYTES,
- * and for the backward two bf16 [3, M, r] buffers, each rounded to 256 bytes; 0 for
+ * (1), and of qlora_linear_fwd_pool and qlora_linear_bwd_pool: QLORA_STATUS_BYTES
+ * plus one, or two, bf16 [3, M, r] buffers, each rounded to 256 bytes; 0 for
  * invalid sizes.  Only the status word has to start zeroed. */
 QLORA_API size_t qlora_workspace_bytes_adapters(int64_t M, int64_t N, int64_t K, int32_t r, int for_backward);
 
