@@ -62,6 +62,17 @@ __device__ __forceinline__ double block_sum(double x, double *red) {
   return s;  // thread 0
 }
 
+// Eight consecutive gradients as float32: wide loads where the address allows them.
+__device__ __forceinline__ void load_grads8(const float *g, float (&x)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4 *>(g)), b = __ldcs(reinterpret_cast<const float4 *>(g) + 1);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load_grads8(const __nv_bfloat16 *g, float (&x)[8]) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(g));
+  x[0] = bf16lo_to_f32(a.x); x[1] = bf16hi_to_f32(a.x); x[2] = bf16lo_to_f32(a.y); x[3] = bf16hi_to_f32(a.y);
+  x[4] = bf16lo_to_f32(a.z); x[5] = bf16hi_to_f32(a.z); x[6] = bf16lo_to_f32(a.w); x[7] = bf16hi_to_f32(a.w);
+}
+
 template <typename G>
 __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const TensorTable tab, float max_norm,
                                                                 float *__restrict__ out, uint32_t *counter,
@@ -69,13 +80,25 @@ __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const TensorTabl
   __shared__ double red[kOptThreads / 32];
   __shared__ bool last;
   double s = 0.0;
-  for (int64_t c = blockIdx.x; c < tab.n_chunks; c += gridDim.x) {
+  // a CTA's chunks are neighbours, mostly of one tensor: its entry stays in L1
+  const int64_t per = (tab.n_chunks + gridDim.x - 1) / gridDim.x, c0 = blockIdx.x * per, c1 = min(tab.n_chunks, c0 + per);
+  for (int64_t c = c0; c < c1; ++c) {
     const int2 tc = tab.chunks[c];
     const G *g = static_cast<const G *>(tab.tensors[tc.x].grad);
-    const int64_t n = tab.tensors[tc.x].n, e0 = static_cast<int64_t>(tc.y) * kOptChunk;
-    for (int64_t e = e0 + threadIdx.x; e < n && e < e0 + kOptChunk; e += kOptThreads) {
-      const double x = static_cast<double>(static_cast<float>(g[e]));
-      s += x * x;
+    const int64_t n = tab.tensors[tc.x].n, e = static_cast<int64_t>(tc.y) * kOptChunk + threadIdx.x * 8;
+    if ((reinterpret_cast<uintptr_t>(g) & 15) == 0 && e + 8 <= n) {
+      float x[8];
+      load_grads8(g + e, x);
+      double t = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), t);
+      s += t;
+    } else {
+      for (int i = 0; i < 8; ++i)
+        if (e + i < n) {
+          const double x = static_cast<double>(static_cast<float>(g[e + i]));
+          s = fma(x, x, s);
+        }
     }
   }
   s = block_sum(s, red);
@@ -89,6 +112,7 @@ __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const TensorTabl
   __threadfence();
   double t = 0.0;
   for (unsigned i = threadIdx.x; i < gridDim.x; i += kOptThreads) t += __ldcg(partial + i);
+  __syncthreads();  // red is read by thread 0 until here
   t = block_sum(t, red);
   if (threadIdx.x == 0) {
     const double norm = sqrt(t);
@@ -144,75 +168,165 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
+// Eight elements of one lane.  WIDE: whole and at addresses for wide accesses; else element by element, those below n.
+template <bool WIDE>
+__device__ __forceinline__ void load_f32x8(const float *p, int valid, float (&x)[8]) {
+  if (WIDE) {
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < valid ? p[i] : 0.0f;
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_f32x8(float *p, int valid, const float (&x)[8]) {
+  if (WIDE) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = x[i];
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ uint2 load_codes8(const uint8_t *p, int valid) {
+  if (WIDE) return __ldcs(reinterpret_cast<const uint2 *>(p));
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < valid) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_codes8(uint8_t *p, int valid, const uint32_t (&w)[2]) {
+  if (WIDE) {
+    __stcs(reinterpret_cast<uint2 *>(p), make_uint2(w[0], w[1]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+template <typename G, bool EIGHT, bool WIDE>
+__device__ __forceinline__ void adamw_block(const qlora_tensor &t, const AdamWMulti &a, int place, int64_t blk, int lane, float clip,
+                                            float decay, float step_size) {
+  const int64_t e0 = blk * QLORA_STATE_BLOCK + 8 * lane;
+  const int valid = WIDE ? 8 : static_cast<int>(max(int64_t(0), min(int64_t(8), t.n - e0)));
+  float p[8], g[8], m[8], v[8];
+  load_f32x8<WIDE>(t.param + e0, valid, p);
+  const G *grad = static_cast<const G *>(t.grad) + e0;
+  if (WIDE) {
+    load_grads8(grad, g);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = i < valid ? static_cast<float>(grad[i]) : 0.0f;
+  }
+  uint2 cm, cv;
+  float sm = 0.0f, sv = 0.0f;
+  if (EIGHT) {
+    cm = load_codes8<WIDE>(static_cast<const uint8_t *>(t.exp_avg) + e0, valid);
+    cv = load_codes8<WIDE>(static_cast<const uint8_t *>(t.exp_avg_sq) + e0, valid);
+    sm = t.exp_avg_scale[blk];
+    sv = t.exp_avg_sq_scale[blk];
+  } else {
+    load_f32x8<WIDE>(static_cast<const float *>(t.exp_avg) + e0, valid, m);
+    load_f32x8<WIDE>(static_cast<const float *>(t.exp_avg_sq) + e0, valid, v);
+  }
+  if (EIGHT) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = scale_code_value2((i < 2 ? cm.x : cm.y) >> (16 * (i & 1)), QLORA_SCALE_E4M3);
+      const float2 y = scale_code_value2((i < 2 ? cv.x : cv.y) >> (16 * (i & 1)), QLORA_SCALE_E5M2);
+      m[2 * i] = __fmul_rn(x.x, sm);
+      m[2 * i + 1] = __fmul_rn(x.y, sm);
+      v[2 * i] = __fmul_rn(y.x, sv);
+      v[2 * i + 1] = __fmul_rn(y.y, sv);
+    }
+  }
+  const float omb1 = 1.0f - a.beta1, omb2 = 1.0f - a.beta2;
+  float mm = 0.0f, vm = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float gi = __fmul_rn(g[i], clip);
+    m[i] = __fadd_rn(__fmul_rn(a.beta1, m[i]), __fmul_rn(omb1, gi));
+    v[i] = __fadd_rn(__fmul_rn(a.beta2, v[i]), __fmul_rn(omb2, __fmul_rn(gi, gi)));
+    const float denom = __fadd_rn(__fdiv_rn(__fsqrt_rn(v[i]), a.sqrt_bc2), a.eps);
+    p[i] = __fsub_rn(__fmul_rn(p[i], decay), __fdiv_rn(__fmul_rn(step_size, m[i]), denom));
+    if (EIGHT) {
+      const float am = fabsf(m[i]);
+      mm = (am > mm || am != am) ? am : mm;
+      vm = (v[i] > vm || v[i] != v[i]) ? v[i] : vm;
+    }
+  }
+  store_f32x8<WIDE>(t.param + e0, valid, p);
+  if (t.param_bf16) {
+    __nv_bfloat16 *p16 = static_cast<__nv_bfloat16 *>(t.param_bf16) + e0;
+    if (WIDE) {
+      __stcs(reinterpret_cast<uint4 *>(p16), make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
+                                                        pack_bf16x2(p[6], p[7])));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < valid) p16[i] = __float2bfloat16_rn(p[i]);
+    }
+  }
+  if (!EIGHT) {
+    store_f32x8<WIDE>(static_cast<float *>(t.exp_avg) + e0, valid, m);
+    store_f32x8<WIDE>(static_cast<float *>(t.exp_avg_sq) + e0, valid, v);
+    return;
+  }
+  mm = warp_max(mm);
+  vm = warp_max(vm);
+  // a maximum below 2^-100 is a block of zeros: its reciprocal would overflow
+  const float im = mm < 0x1p-100f ? 0.0f : __fdiv_rn(448.0f, mm), iv = vm < 0x1p-100f ? 0.0f : __fdiv_rn(57344.0f, vm);
+  if (lane == 0) {
+    t.exp_avg_scale[blk] = mm < 0x1p-100f ? 0.0f : __fdiv_rn(mm, 448.0f);
+    t.exp_avg_sq_scale[blk] = vm < 0x1p-100f ? 0.0f : __fdiv_rn(vm, 57344.0f);
+  }
+  const uint32_t stream = a.seed * 0xB7E15163u + static_cast<uint32_t>(place) * 0x3504F333u;
+  uint32_t wm[2] = {0u, 0u}, wv[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    float qm[2], qv[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t h = state_hash(static_cast<uint32_t>(e0) + i + k, stream);
+      const float x = round_float8<20>(__fmul_rn(fabsf(m[i + k]), im), h & 0xFFFFFu, 0x1p-6f, 448.0f);
+      qm[k] = copysignf(x, m[i + k]);
+      qv[k] = round_float8<21>(__fmul_rn(v[i + k], iv), h >> 11, 0x1p-14f, 57344.0f);
+      if (v[i + k] > 0.0f && iv > 0.0f) qv[k] = fmaxf(qv[k], 0x1p-16f);
+    }
+    wm[i >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(qm[0], qm[1]), __NV_SATFINITE, __NV_E4M3)) << (8 * (i & 3));
+    wv[i >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(qv[0], qv[1]), __NV_SATFINITE, __NV_E5M2)) << (8 * (i & 3));
+  }
+  store_codes8<WIDE>(static_cast<uint8_t *>(t.exp_avg) + e0, valid, wm);
+  store_codes8<WIDE>(static_cast<uint8_t *>(t.exp_avg_sq) + e0, valid, wv);
+}
+
 template <typename G, bool EIGHT>
 __global__ void __launch_bounds__(kOptThreads) adamw_multi_kernel(const TensorTable tab, const AdamWMulti a) {
   const float clip = a.clip ? a.clip[1] : 1.0f;
   if (clip != clip) return;  // the norm was not finite: the step changes nothing
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float omb1 = 1.0f - a.beta1, omb2 = 1.0f - a.beta2;
   for (int64_t c = blockIdx.x; c < tab.n_chunks; c += gridDim.x) {
     const int2 tc = tab.chunks[c];
     const qlora_tensor t = tab.tensors[tc.x];
+    const int64_t blk = static_cast<int64_t>(tc.y) * (kOptThreads / 32) + warp, e0 = blk * QLORA_STATE_BLOCK;
+    if (e0 >= t.n) continue;
     const double lr_scale = static_cast<double>(t.lr_scale);
     const float decay = static_cast<float>(1.0 - a.lr * lr_scale * a.weight_decay);
     const float step_size = static_cast<float>(a.step_size * lr_scale);
-    const int64_t blk = static_cast<int64_t>(tc.y) * (kOptThreads / 32) + warp;
-    const int64_t e0 = blk * QLORA_STATE_BLOCK;
-    if (e0 >= t.n) continue;
-    float m[8], v[8];
-    float sm = 0.0f, sv = 0.0f;
-    if (EIGHT) { sm = t.exp_avg_scale[blk]; sv = t.exp_avg_sq_scale[blk]; }
-    float mm = 0.0f, vm = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t e = e0 + 8 * lane + i;
-      m[i] = v[i] = 0.0f;
-      if (e >= t.n) continue;
-      float p = t.param[e];
-      const float g = __fmul_rn(static_cast<float>(static_cast<const G *>(t.grad)[e]), clip);
-      if (EIGHT) {
-        m[i] = __fmul_rn(scale_code_value(static_cast<const uint8_t *>(t.exp_avg)[e], QLORA_SCALE_E4M3), sm);
-        v[i] = __fmul_rn(scale_code_value(static_cast<const uint8_t *>(t.exp_avg_sq)[e], QLORA_SCALE_E5M2), sv);
-      } else {
-        m[i] = static_cast<const float *>(t.exp_avg)[e];
-        v[i] = static_cast<const float *>(t.exp_avg_sq)[e];
-      }
-      m[i] = __fadd_rn(__fmul_rn(a.beta1, m[i]), __fmul_rn(omb1, g));
-      v[i] = __fadd_rn(__fmul_rn(a.beta2, v[i]), __fmul_rn(omb2, __fmul_rn(g, g)));
-      const float denom = __fadd_rn(__fdiv_rn(__fsqrt_rn(v[i]), a.sqrt_bc2), a.eps);
-      p = __fsub_rn(__fmul_rn(p, decay), __fdiv_rn(__fmul_rn(step_size, m[i]), denom));
-      t.param[e] = p;
-      if (t.param_bf16) static_cast<__nv_bfloat16 *>(t.param_bf16)[e] = __float2bfloat16_rn(p);
-      if (!EIGHT) {
-        static_cast<float *>(t.exp_avg)[e] = m[i];
-        static_cast<float *>(t.exp_avg_sq)[e] = v[i];
-      }
-      const float am = fabsf(m[i]);
-      mm = (am > mm || am != am) ? am : mm;
-      vm = (v[i] > vm || v[i] != v[i]) ? v[i] : vm;
-    }
-    if (EIGHT) {
-      mm = warp_max(mm);
-      vm = warp_max(vm);
-      // a maximum below 2^-100 is a block of zeros: its reciprocal would overflow
-      const float im = mm < 0x1p-100f ? 0.0f : __fdiv_rn(448.0f, mm), iv = vm < 0x1p-100f ? 0.0f : __fdiv_rn(57344.0f, vm);
-      if (lane == 0) {
-        t.exp_avg_scale[blk] = mm < 0x1p-100f ? 0.0f : __fdiv_rn(mm, 448.0f);
-        t.exp_avg_sq_scale[blk] = vm < 0x1p-100f ? 0.0f : __fdiv_rn(vm, 57344.0f);
-      }
-      const uint32_t stream = a.seed * 0xB7E15163u + static_cast<uint32_t>(tc.x) * 0x3504F333u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t e = e0 + 8 * lane + i;
-        if (e >= t.n) continue;
-        const uint32_t h = state_hash(static_cast<uint32_t>(e), stream);
-        const float qm = round_float8<20>(__fmul_rn(fabsf(m[i]), im), h & 0xFFFFFu, 0x1p-6f, 448.0f);
-        float qv = round_float8<21>(__fmul_rn(v[i], iv), h >> 11, 0x1p-14f, 57344.0f);
-        if (v[i] > 0.0f && iv > 0.0f) qv = fmaxf(qv, 0x1p-16f);
-        static_cast<uint8_t *>(t.exp_avg)[e] = f32_to_e4m3(copysignf(qm, m[i]));
-        static_cast<uint8_t *>(t.exp_avg_sq)[e] = scale_code_encode(qv, QLORA_SCALE_E5M2);
-      }
-    }
+    // wide accesses where all addresses allow them (16 bytes; codes 8) and the block is whole
+    const uintptr_t wide = reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.param_bf16) |
+                           reinterpret_cast<uintptr_t>(t.grad) |
+                           (reinterpret_cast<uintptr_t>(t.exp_avg) | reinterpret_cast<uintptr_t>(t.exp_avg_sq)) * (EIGHT ? 2 : 1);
+    if ((wide & 15) == 0 && e0 + QLORA_STATE_BLOCK <= t.n)
+      adamw_block<G, EIGHT, true>(t, a, tc.x, blk, lane, clip, decay, step_size);
+    else
+      adamw_block<G, EIGHT, false>(t, a, tc.x, blk, lane, clip, decay, step_size);
   }
 }
 
