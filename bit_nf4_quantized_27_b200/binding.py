@@ -142,12 +142,12 @@ def _check(code: int, where: str):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle without building a Stream object, which costs more than some of the kernels
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _dtype_code(dt):
@@ -403,9 +403,11 @@ def linear_bwd_dropout(q: NF4Weight, A, B, alpha: float, X, dY, keep: torch.Tens
 # ---------------------------------------------------------------------------
 def _here(*tensors):
     """The operands of a call lie on the current device, where its kernels run."""
-    dev = torch.cuda.current_device()
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and t.get_device() != dev:  # -1 for a tensor on the CPU
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
 
 
@@ -428,6 +430,8 @@ class AdapterPool:
         self._c = PoolC(self.n, self.r, A.data_ptr(), B.data_ptr(), None if ranks is None else ranks.data_ptr(),
                         scales.data_ptr())
 
+        self._ref = ctypes.byref(self._c)
+
     def c_struct(self) -> PoolC:
         return self._c
 
@@ -440,16 +444,17 @@ def adapter_groups(adapter_of_token: torch.Tensor, n: int, out=None, ws: torch.T
     """(order [M], offsets [n + 1]) int32: the tokens grouped by adapter (-1: none, last)."""
     idx = adapter_of_token
     assert idx.dtype == torch.int32 and idx.is_contiguous() and idx.dim() == 1
+    M = idx.numel()
     if out is None:
-        buf = torch.empty(idx.numel() + n + 1, dtype=torch.int32, device=idx.device)
-        out = buf[:idx.numel()], buf[idx.numel():]
-    order, offsets = out
-    assert order.dtype == offsets.dtype == torch.int32 and order.is_contiguous() and offsets.is_contiguous()
-    assert order.numel() == idx.numel() and offsets.numel() == n + 1
+        order, offsets = idx.new_empty(M), idx.new_empty(n + 1)
+    else:
+        order, offsets = out
+        assert order.dtype == offsets.dtype == torch.int32 and order.is_contiguous() and offsets.is_contiguous()
+        assert order.numel() == M and offsets.numel() == n + 1
     _here(idx, order, offsets, ws)
     if ws is None:
         ws = new_workspace(STATUS_BYTES, idx.device)
-    _check(lib().qlora_adapter_groups(_ptr(idx), idx.numel(), n, _ptr(order), _ptr(offsets), _ptr(ws), _stream(stream)),
+    _check(lib().qlora_adapter_groups(_ptr(idx), M, n, _ptr(order), _ptr(offsets), _ptr(ws), _stream(stream)),
            "qlora_adapter_groups")
     return order, offsets
 
@@ -463,8 +468,9 @@ def _group_ptrs(groups, pool: AdapterPool, m: int):
 
 def _row_stride(t: torch.Tensor) -> int:
     """Row stride of a [rows, cols] tensor whose rows are contiguous."""
-    assert t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    (rows, cols), (row, col) = t.shape, t.stride()
+    assert cols == 1 or col == 1
+    return row if rows > 1 else max(row, cols)
 
 
 def adapters_fwd(pool: AdapterPool, groups, X: torch.Tensor, Y: torch.Tensor, save_t: bool = False, t_out=None,
@@ -480,7 +486,7 @@ def adapters_fwd(pool: AdapterPool, groups, X: torch.Tensor, Y: torch.Tensor, sa
     _here(X, Y, T, ws, pool.A, *groups)
     if ws is None:
         ws = new_workspace(workspace_bytes_adapters(M, pool.rows, pool.cols, pool.r, False), X.device)
-    _check(lib().qlora_adapters_fwd(ctypes.byref(pool.c_struct()), order, offsets, _ptr(X), _row_stride(X), M, pool.rows,
+    _check(lib().qlora_adapters_fwd(pool._ref, order, offsets, _ptr(X), _row_stride(X), M, pool.rows,
                                     pool.cols, _ptr(Y), _row_stride(Y), _dtype_code(Y.dtype), _ptr(T), _ptr(ws),
                                     ws.numel(), _stream(stream)), "qlora_adapters_fwd")
     return T
@@ -510,7 +516,7 @@ def adapters_bwd(pool: AdapterPool, groups, X: torch.Tensor, dY: torch.Tensor, T
     _here(X, dY, T, dX, dA, dB, ws, pool.A, *groups)
     if ws is None:
         ws = new_workspace(workspace_bytes_adapters(M, pool.rows, pool.cols, pool.r, True), X.device)
-    _check(lib().qlora_adapters_bwd(ctypes.byref(pool.c_struct()), order, offsets, _ptr(X), _row_stride(X), _ptr(dY),
+    _check(lib().qlora_adapters_bwd(pool._ref, order, offsets, _ptr(X), _row_stride(X), _ptr(dY),
                                     _row_stride(dY), M, pool.rows, pool.cols, _ptr(T), _ptr(dX),
                                     0 if dX is None else _row_stride(dX), QLORA_F32 if dX is None else _dtype_code(dX.dtype),
                                     _ptr(dA), _ptr(dB), QLORA_F32 if dA is None else _dtype_code(dA.dtype), _ptr(ws),
@@ -531,7 +537,7 @@ def linear_fwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, y_dtype=torch.bf
     if ws is None:
         ws = new_workspace(workspace_bytes_adapters(M, q.rows, q.cols, pool.r, False), X.device)
     t = q.c_struct()
-    _check(lib().qlora_linear_fwd_pool(ctypes.byref(t), ctypes.byref(pool.c_struct()), order, offsets, _ptr(X), M, _ptr(Y),
+    _check(lib().qlora_linear_fwd_pool(ctypes.byref(t), pool._ref, order, offsets, _ptr(X), M, _ptr(Y),
                                        _dtype_code(Y.dtype), _ptr(T), _ptr(ws), ws.numel(), _stream(stream)),
            "qlora_linear_fwd_pool")
     return Y, T
@@ -551,7 +557,7 @@ def linear_bwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, dY, T=None, dx_d
     if ws is None:
         ws = new_workspace(workspace_bytes_adapters(M, q.rows, q.cols, pool.r, True), X.device)
     t = q.c_struct()
-    _check(lib().qlora_linear_bwd_pool(ctypes.byref(t), ctypes.byref(pool.c_struct()), order, offsets, _ptr(X), _ptr(dY), M,
+    _check(lib().qlora_linear_bwd_pool(ctypes.byref(t), pool._ref, order, offsets, _ptr(X), _ptr(dY), M,
                                        _ptr(T), _ptr(dX), _dtype_code(dX.dtype), _ptr(dA), _ptr(dB), _dtype_code(dA.dtype),
                                        _ptr(ws), ws.numel(), _stream(stream)), "qlora_linear_bwd_pool")
     return dX, dA, dB
@@ -628,6 +634,7 @@ class TensorList:
                                             ctypes.byref(self._c), _stream(stream)), "qlora_tensor_list_init")
         self._keep = columns
         self.state_bits = bits
+        self._ref = ctypes.byref(self._c)
 
     def c_struct(self) -> TensorListC:
         return self._c
@@ -646,7 +653,7 @@ def grad_norm(tensors: TensorList, max_norm: float, out: torch.Tensor | None = N
     _here(tensors.table, out, ws)
     if ws is None:
         ws = new_workspace(workspace_bytes_grad_norm(), tensors.table.device)
-    _check(lib().qlora_grad_norm(ctypes.byref(tensors.c_struct()), float(max_norm), _ptr(out), _ptr(ws), ws.numel(),
+    _check(lib().qlora_grad_norm(tensors._ref, float(max_norm), _ptr(out), _ptr(ws), ws.numel(),
                                  _stream(stream)), "qlora_grad_norm")
     return out
 
@@ -659,5 +666,5 @@ def adamw_multi(tensors: TensorList, step: int, lr: float, beta1: float = 0.9, b
     assert clip is None or (clip.dtype == torch.float32 and clip.is_contiguous() and clip.numel() == 2)
     _here(tensors.table, clip)
     hp = AdamWC(lr, beta1, beta2, eps, weight_decay)
-    _check(lib().qlora_adamw_multi(ctypes.byref(tensors.c_struct()), ctypes.byref(hp), step, _ptr(clip), seed & 0xffffffff,
+    _check(lib().qlora_adamw_multi(tensors._ref, ctypes.byref(hp), step, _ptr(clip), seed & 0xffffffff,
                                    _stream(stream)), "qlora_adamw_multi")

@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const TensorTabl
   __shared__ double red[kOptThreads / 32];
   __shared__ bool last;
   double s = 0.0;
-  // a CTA's chunks are neighbours, mostly of one tensor: its entry stays in L1
+  // A CTA's chunks are neighbours, mostly of one tensor: its entry stays in L1.  Eight CTAs an SM keep the loads going (two or
+  // four chunks ahead in fewer CTAs were slower: 16.7 and 24.9 against 15.8 us for 27M bf16 gradients).
   const int64_t per = (tab.n_chunks + gridDim.x - 1) / gridDim.x, c0 = blockIdx.x * per, c1 = min(tab.n_chunks, c0 + per);
   for (int64_t c = c0; c < c1; ++c) {
     const int2 tc = tab.chunks[c];
@@ -124,8 +125,8 @@ __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const TensorTabl
 }
 
 // ---------------------------------------------------------------------------
-// AdamW.  The arithmetic is adamw_one's, float32 operation by operation.  8-bit
-// states: a warp holds one block of 256 elements, eight consecutive ones per
+// AdamW.  The arithmetic is adamw_one's, float32 operation by operation (with 8-bit
+// states but for the update's root and quotient).  8-bit states: a warp holds one block of 256 elements, eight consecutive ones per
 // lane; the block's new maxima come from warp shuffles, the codes from adding
 // random bits below the last mantissa bit kept and cutting them off.  The result is
 // unbiased, which round-to-nearest is not where it matters: a step changes the
@@ -133,10 +134,11 @@ __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const TensorTabl
 // variance would never move.
 // ---------------------------------------------------------------------------
 struct AdamWMulti {
-  float beta1, beta2, eps, sqrt_bc2;
+  float beta1, beta2, eps, sqrt_bc2, inv_sqrt_bc2;
   double lr, weight_decay, step_size;  // step_size = lr / bc1
   const float *clip;                   // nullable [2]
   uint32_t seed;
+  int per;  // chunks a CTA
 };
 
 // 32 bits for an element: multiplications by the first fraction bits of the golden
@@ -148,24 +150,40 @@ __device__ __forceinline__ uint32_t state_hash(uint32_t element, uint32_t stream
   return x ^ (x >> 16);
 }
 
-// x >= 0 to a float8 value (as float32) at or next to it, up with the probability
-// of rnd's kDrop bits.  Below the format's least normal value kLeast the step is
-// that of the first binade: adding kLeast puts x there.
+// x >= 0 to the code of a float8 value at or next to it, up with the probability of rnd's kDrop bits: added below the last
+// mantissa bit kept, they carry into it, and the shift cuts the rest off.  Below the format's least normal value kLeast
+// the step is that of the first binade: adding kLeast puts x there, kBinade codes up.  kBias: the float32 code of the
+// format's exponent 0, shifted alike.
 template <int kDrop>
-__device__ __forceinline__ float round_float8(float x, uint32_t rnd, float least, float most) {
+__device__ __forceinline__ uint32_t round_float8(float x, uint32_t rnd, float least, uint32_t bias, uint32_t binade, uint32_t most) {
   const bool small = x < least;
-  const float z = small ? __fadd_rn(x, least) : x;
-  const float y = __uint_as_float((__float_as_uint(z) + rnd) & ~((1u << kDrop) - 1u));
-  return fminf(small ? __fsub_rn(y, least) : y, most);
+  const float z = __fadd_rn(x, small ? least : 0.0f);
+  return min((__float_as_uint(z) + rnd - (bias << kDrop) - (small ? binade << kDrop : 0u)) >> kDrop, most);
 }
+__device__ __forceinline__ uint32_t round_e4m3(float x, uint32_t rnd) { return round_float8<20>(x, rnd, 0x1p-6f, 120u << 3, 8u, 126u); }
+__device__ __forceinline__ uint32_t round_e5m2(float x, uint32_t rnd) { return round_float8<21>(x, rnd, 0x1p-14f, 112u << 2, 4u, 123u); }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float y = __shfl_xor_sync(0xffffffffu, x, o);
-    x = (y > x || y != y) ? y : x;  // a NaN stays
-  }
-  return x;
+// The larger one; a NaN stays.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+// The warp's largest magnitude; a NaN stays.
+__device__ __forceinline__ float warp_max_abs(float x) {
+  float r;
+  asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Eight elements of one lane.  WIDE: whole and at addresses for wide accesses; else element by element, those below n.
@@ -235,30 +253,38 @@ __device__ __forceinline__ void adamw_block(const qlora_tensor &t, const AdamWMu
     load_f32x8<WIDE>(static_cast<const float *>(t.exp_avg) + e0, valid, m);
     load_f32x8<WIDE>(static_cast<const float *>(t.exp_avg_sq) + e0, valid, v);
   }
-  if (EIGHT) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = scale_code_value2((i < 2 ? cm.x : cm.y) >> (16 * (i & 1)), QLORA_SCALE_E4M3);
-      const float2 y = scale_code_value2((i < 2 ? cv.x : cv.y) >> (16 * (i & 1)), QLORA_SCALE_E5M2);
-      m[2 * i] = __fmul_rn(x.x, sm);
-      m[2 * i + 1] = __fmul_rn(x.y, sm);
-      v[2 * i] = __fmul_rn(y.x, sv);
-      v[2 * i + 1] = __fmul_rn(y.y, sv);
-    }
-  }
   const float omb1 = 1.0f - a.beta1, omb2 = 1.0f - a.beta2;
   float mm = 0.0f, vm = 0.0f;
+  if (EIGHT) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float gi = __fmul_rn(g[i], clip);
-    m[i] = __fadd_rn(__fmul_rn(a.beta1, m[i]), __fmul_rn(omb1, gi));
-    v[i] = __fadd_rn(__fmul_rn(a.beta2, v[i]), __fmul_rn(omb2, __fmul_rn(gi, gi)));
-    const float denom = __fadd_rn(__fdiv_rn(__fsqrt_rn(v[i]), a.sqrt_bc2), a.eps);
-    p[i] = __fsub_rn(__fmul_rn(p[i], decay), __fdiv_rn(__fmul_rn(step_size, m[i]), denom));
-    if (EIGHT) {
-      const float am = fabsf(m[i]);
-      mm = (am > mm || am != am) ? am : mm;
-      vm = (v[i] > vm || v[i] != v[i]) ? v[i] : vm;
+    for (int i = 0; i < 8; i += 2) {
+      const float2 x = scale_code_value2((i < 4 ? cm.x : cm.y) >> (8 * (i & 2)), QLORA_SCALE_E4M3);
+      const float2 y = scale_code_value2((i < 4 ? cv.x : cv.y) >> (8 * (i & 2)), QLORA_SCALE_E5M2);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float gi = __fmul_rn(g[i + k], clip);
+        m[i + k] = __fadd_rn(__fmul_rn(a.beta1, __fmul_rn(k ? x.y : x.x, sm)), __fmul_rn(omb1, gi));
+        v[i + k] = __fadd_rn(__fmul_rn(a.beta2, __fmul_rn(k ? y.y : y.x, sv)), __fmul_rn(omb2, __fmul_rn(gi, gi)));
+      }
+      // The states were read to 2^-4 and 2^-3, so the update needs no last bit: approximate root and reciprocal (a few
+      // 2^-23 of the update) in place of IEEE ones, which made this path issue-bound (112
+      // instructions a parameter, 243 us for 54M).  The states' own chain stays in single roundings.
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float denom = fmaf(sqrt_approx(v[i + k]), a.inv_sqrt_bc2, a.eps);
+        p[i + k] = fmaf(p[i + k], decay, -__fmul_rn(__fmul_rn(step_size, m[i + k]), rcp_approx(denom)));
+      }
+      mm = max_nan(mm, max_nan(fabsf(m[i]), fabsf(m[i + 1])));
+      vm = max_nan(vm, max_nan(v[i], v[i + 1]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float gi = __fmul_rn(g[i], clip);
+      m[i] = __fadd_rn(__fmul_rn(a.beta1, m[i]), __fmul_rn(omb1, gi));
+      v[i] = __fadd_rn(__fmul_rn(a.beta2, v[i]), __fmul_rn(omb2, __fmul_rn(gi, gi)));
+      const float denom = __fadd_rn(__fdiv_rn(__fsqrt_rn(v[i]), a.sqrt_bc2), a.eps);
+      p[i] = __fsub_rn(__fmul_rn(p[i], decay), __fdiv_rn(__fmul_rn(step_size, m[i]), denom));
     }
   }
   store_f32x8<WIDE>(t.param + e0, valid, p);
@@ -278,55 +304,69 @@ __device__ __forceinline__ void adamw_block(const qlora_tensor &t, const AdamWMu
     store_f32x8<WIDE>(static_cast<float *>(t.exp_avg_sq) + e0, valid, v);
     return;
   }
-  mm = warp_max(mm);
-  vm = warp_max(vm);
-  // a maximum below 2^-100 is a block of zeros: its reciprocal would overflow
-  const float im = mm < 0x1p-100f ? 0.0f : __fdiv_rn(448.0f, mm), iv = vm < 0x1p-100f ? 0.0f : __fdiv_rn(57344.0f, vm);
-  if (lane == 0) {
-    t.exp_avg_scale[blk] = mm < 0x1p-100f ? 0.0f : __fdiv_rn(mm, 448.0f);
-    t.exp_avg_sq_scale[blk] = vm < 0x1p-100f ? 0.0f : __fdiv_rn(vm, 57344.0f);
-  }
+  mm = warp_max_abs(mm);
+  vm = warp_max_abs(vm);
+  // Reciprocals for the codes (lanes 0 and 1) and scales (lanes 2 and 3) in one division.  A maximum below 2^-100 is a block
+  // of zeros: its reciprocal would overflow.
+  const bool of_v = lane & 1, scale = lane & 2;
+  const float top = of_v ? vm : mm, most = of_v ? 57344.0f : 448.0f;
+  const float quot = top < 0x1p-100f ? 0.0f : __fdiv_rn(scale ? top : most, scale ? most : top);
+  if (lane == 2) t.exp_avg_scale[blk] = quot;
+  if (lane == 3) t.exp_avg_sq_scale[blk] = quot;
+  const float im = __shfl_sync(0xffffffffu, quot, 0), iv = __shfl_sync(0xffffffffu, quot, 1);
   const uint32_t stream = a.seed * 0xB7E15163u + static_cast<uint32_t>(place) * 0x3504F333u;
   uint32_t wm[2] = {0u, 0u}, wv[2] = {0u, 0u};
+  const uint32_t least_v = iv > 0.0f ? 1u : 0u;  // a variance that is not zero keeps a code above zero
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    float qm[2], qv[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const uint32_t h = state_hash(static_cast<uint32_t>(e0) + i + k, stream);
-      const float x = round_float8<20>(__fmul_rn(fabsf(m[i + k]), im), h & 0xFFFFFu, 0x1p-6f, 448.0f);
-      qm[k] = copysignf(x, m[i + k]);
-      qv[k] = round_float8<21>(__fmul_rn(v[i + k], iv), h >> 11, 0x1p-14f, 57344.0f);
-      if (v[i + k] > 0.0f && iv > 0.0f) qv[k] = fmaxf(qv[k], 0x1p-16f);
+      const uint32_t qm = round_e4m3(__fmul_rn(fabsf(m[i + k]), im), h & 0xFFFFFu);
+      const uint32_t qv = round_e5m2(__fmul_rn(v[i + k], iv), h >> 11);
+      wm[i >> 2] |= (qm | (__float_as_uint(m[i + k]) >> 24 & 0x80u)) << (8 * ((i + k) & 3));
+      wv[i >> 2] |= (v[i + k] > 0.0f ? max(qv, least_v) : qv) << (8 * ((i + k) & 3));
     }
-    wm[i >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(qm[0], qm[1]), __NV_SATFINITE, __NV_E4M3)) << (8 * (i & 3));
-    wv[i >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(qv[0], qv[1]), __NV_SATFINITE, __NV_E5M2)) << (8 * (i & 3));
   }
   store_codes8<WIDE>(static_cast<uint8_t *>(t.exp_avg) + e0, valid, wm);
   store_codes8<WIDE>(static_cast<uint8_t *>(t.exp_avg_sq) + e0, valid, wv);
 }
 
 template <typename G, bool EIGHT>
-__global__ void __launch_bounds__(kOptThreads) adamw_multi_kernel(const TensorTable tab, const AdamWMulti a) {
+__global__ void __launch_bounds__(kOptThreads, EIGHT ? 4 : 3) adamw_multi_kernel(const TensorTable tab, const AdamWMulti a) {
   const float clip = a.clip ? a.clip[1] : 1.0f;
   if (clip != clip) return;  // the norm was not finite: the step changes nothing
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t c = blockIdx.x; c < tab.n_chunks; c += gridDim.x) {
-    const int2 tc = tab.chunks[c];
-    const qlora_tensor t = tab.tensors[tc.x];
+  // a CTA's chunks are neighbours, mostly of one tensor, whose entry is read once; the next chunk's place is read ahead
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.per, c1 = min(tab.n_chunks, c0 + a.per);
+  int2 next = tab.chunks[c0];
+  int at = -1;
+  __shared__ qlora_tensor t;  // not in registers: they are what bounds the warps on an SM
+  float decay = 0.0f, step_size = 0.0f;
+  bool wide = false;
+  for (int64_t c = c0; c < c1; ++c) {
+    const int2 tc = next;
+    if (c + 1 < c1) next = tab.chunks[c + 1];
+    if (tc.x != at) {
+      at = tc.x;
+      __syncthreads();  // the last entry is done with
+      if (threadIdx.x == 0) t = tab.tensors[at];
+      __syncthreads();
+      const double lr_scale = static_cast<double>(t.lr_scale);
+      decay = static_cast<float>(1.0 - a.lr * lr_scale * a.weight_decay);
+      step_size = static_cast<float>(a.step_size * lr_scale);
+      // wide accesses where all addresses allow them (16 bytes; codes 8), and the block is whole
+      const uintptr_t any = reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.param_bf16) |
+                            reinterpret_cast<uintptr_t>(t.grad) |
+                            (reinterpret_cast<uintptr_t>(t.exp_avg) | reinterpret_cast<uintptr_t>(t.exp_avg_sq)) * (EIGHT ? 2 : 1);
+      wide = (any & 15) == 0;
+    }
     const int64_t blk = static_cast<int64_t>(tc.y) * (kOptThreads / 32) + warp, e0 = blk * QLORA_STATE_BLOCK;
     if (e0 >= t.n) continue;
-    const double lr_scale = static_cast<double>(t.lr_scale);
-    const float decay = static_cast<float>(1.0 - a.lr * lr_scale * a.weight_decay);
-    const float step_size = static_cast<float>(a.step_size * lr_scale);
-    // wide accesses where all addresses allow them (16 bytes; codes 8) and the block is whole
-    const uintptr_t wide = reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.param_bf16) |
-                           reinterpret_cast<uintptr_t>(t.grad) |
-                           (reinterpret_cast<uintptr_t>(t.exp_avg) | reinterpret_cast<uintptr_t>(t.exp_avg_sq)) * (EIGHT ? 2 : 1);
-    if ((wide & 15) == 0 && e0 + QLORA_STATE_BLOCK <= t.n)
-      adamw_block<G, EIGHT, true>(t, a, tc.x, blk, lane, clip, decay, step_size);
+    if (wide && e0 + QLORA_STATE_BLOCK <= t.n)
+      adamw_block<G, EIGHT, true>(t, a, at, blk, lane, clip, decay, step_size);
     else
-      adamw_block<G, EIGHT, false>(t, a, tc.x, blk, lane, clip, decay, step_size);
+      adamw_block<G, EIGHT, false>(t, a, at, blk, lane, clip, decay, step_size);
   }
 }
 

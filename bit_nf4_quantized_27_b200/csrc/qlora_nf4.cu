@@ -1499,14 +1499,17 @@ qlora_status qlora_adamw_multi(const qlora_tensor_list *list, const qlora_adamw_
   const double bc2 = 1.0 - std::pow(static_cast<double>(hp->beta2), static_cast<double>(step));
   a.beta1 = hp->beta1;
   a.beta2 = hp->beta2;
-  a.eps = hp->eps;
+  a.eps = list->state_bits == 8 ? std::max(hp->eps, 1.17549435e-38f) : hp->eps;  // below it the approximate reciprocal sees 0
   a.sqrt_bc2 = static_cast<float>(std::sqrt(bc2));
+  a.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
   a.lr = hp->lr;
   a.weight_decay = hp->weight_decay;
   a.step_size = hp->lr / bc1;
   a.clip = norm_and_clip;
   a.seed = seed;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(list->n_chunks, static_cast<int64_t>(sms) * 8));
+  // four chunks a CTA where that still makes several CTAs for each place on the GPU
+  a.per = list->n_chunks >= static_cast<int64_t>(sms) * 64 ? 4 : 1;
+  const unsigned grid = static_cast<unsigned>((list->n_chunks + a.per - 1) / a.per);
   const TensorTable t = table_of(list);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = list->grad_dtype == QLORA_F32;
