@@ -10,13 +10,18 @@
 namespace qlora {
 
 // ---------------------------------------------------------------------------
-// Tokens grouped by adapter: a stable counting sort in one CTA.  Warp w owns the
-// w-th contiguous piece of the tokens and counts its keys in its own row of
-// shared counters; a running sum over (key, warp) turns the counts into first
-// places; each warp then walks its piece again, 32 tokens at a time, and places
-// them with the rank among equal keys that match gives.  Key n: no adapter.
+// Tokens grouped by adapter: a stable counting sort by the CTAs of one cluster (one CTA for
+// few tokens).  Warp w of CTA b owns the (b, w)-th contiguous piece of the tokens and counts
+// its keys in its own row of shared counters, 32 tokens at a time: match gives the lanes of
+// equal keys, and their first adds for all (runs of one request would serialise atomics).  Each
+// CTA then needs, of each key, the counts of the CTAs before it and of all, read
+// through distributed shared memory, and a running sum over the keys; that turns the counters
+// into first places, and a second walk places the tokens with the rank among equal keys.
+// Key n: no adapter.  Latency bound: 22 us with one CTA for 65536 tokens of 512 adapters.
 // ---------------------------------------------------------------------------
-constexpr int kGroupThreads = 1024;
+constexpr int kGroupThreads = 1024, kGroupWarps = kGroupThreads / 32;
+constexpr int kGroupCluster = 8;
+constexpr int64_t kGroupOneCta = 4096;  // tokens up to which one CTA is faster
 
 __device__ __forceinline__ int group_key(const int32_t *idx, int64_t t, int n, uint32_t *status) {
   const int a = idx[t];
@@ -28,50 +33,84 @@ __device__ __forceinline__ int group_key(const int32_t *idx, int64_t t, int n, u
 __global__ void __launch_bounds__(kGroupThreads) adapter_groups_kernel(const int32_t *__restrict__ idx, int64_t M, int n,
                                                                        int32_t *__restrict__ order,
                                                                        int32_t *__restrict__ offsets, uint32_t *status) {
-  extern __shared__ int32_t group_counts[];  // [warps][n + 1]
-  __shared__ int32_t scan[kGroupThreads];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, keys = n + 1;
-  int32_t *mine = group_counts + warp * keys;
-  for (int i = threadIdx.x; i < warps * keys; i += blockDim.x) group_counts[i] = 0;
+  extern __shared__ int32_t group_counts[];  // [warps][n + 1], then [n + 1] of the CTA
+  __shared__ int32_t warp_sum[kGroupWarps];
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, keys = n + 1;
+  const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
+  int32_t *mine = group_counts + warp * keys, *cta = group_counts + kGroupWarps * keys;
+  for (int i = tid; i < kGroupWarps * keys; i += kGroupThreads) group_counts[i] = 0;
   __syncthreads();
-  const int64_t per = ((M + warps - 1) / warps + 31) / 32 * 32;
-  const int64_t t0 = warp * per, t1 = min(M, t0 + per);
-  for (int64_t t = t0 + lane; t < t1; t += 32) atomicAdd(&mine[group_key(idx, t, n, status)], 1);
-  __syncthreads();
-  // first place of each key, then of each (key, warp)
-  const int per_thread = (keys + blockDim.x - 1) / blockDim.x, k0 = threadIdx.x * per_thread;
-  int32_t sum = 0;
-  for (int k = k0; k < min(keys, k0 + per_thread); ++k)
-    for (int w = 0; w < warps; ++w) sum += group_counts[w * keys + k];
-  scan[threadIdx.x] = sum;
-  __syncthreads();
-  for (int o = 1; o < static_cast<int>(blockDim.x); o <<= 1) {
-    const int32_t x = threadIdx.x >= o ? scan[threadIdx.x - o] : 0;
-    __syncthreads();
-    scan[threadIdx.x] += x;
-    __syncthreads();
+  const int64_t pieces = static_cast<int64_t>(ctas) * kGroupWarps;
+  const int64_t per = ((M + pieces - 1) / pieces + 31) / 32 * 32;
+  const int64_t t0 = (static_cast<int64_t>(rank) * kGroupWarps + warp) * per, t1 = min(M, t0 + per);
+  for (int64_t b = t0; b < t1; b += 32) {
+    const int64_t t = b + lane;
+    const int key = t < t1 ? group_key(idx, t, n, status) : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, key);
+    if (key >= 0 && (same & ((1u << lane) - 1u)) == 0) mine[key] += __popc(same);
+    __syncwarp();
   }
-  int32_t at = scan[threadIdx.x] - sum;
-  for (int k = k0; k < min(keys, k0 + per_thread); ++k) {
-    offsets[k] = at;  // key n: the number of tokens with an adapter
-    for (int w = 0; w < warps; ++w) {
+  __syncthreads();
+  // a thread's key (at most one key more than threads: QLORA_MAX_ADAPTERS + 1, so the last thread may have two)
+  for (int k = tid; k < keys; k += kGroupThreads) {
+    int32_t s = 0;
+#pragma unroll
+    for (int w = 0; w < kGroupWarps; ++w) s += group_counts[w * keys + k];
+    cta[k] = s;
+  }
+  if (ctas > 1) ptx::cluster_sync(); else __syncthreads();
+  // of key k: the count of all CTAs, and of those before this one
+  auto totals = [&](int k, int32_t &before) {
+    int32_t all = 0;
+    before = 0;
+    const uint32_t at = ptx::smem_addr(cta + k);
+    for (int c = 0; c < ctas; ++c) {
+      const int32_t x = ctas > 1 ? static_cast<int32_t>(ptx::ld_cluster_u32(ptx::mapa_shared(at, c))) : cta[k];
+      all += x;
+      if (c < rank) before += x;
+    }
+    return all;
+  };
+  int32_t before = 0, extra_before = 0;
+  const int32_t all = tid < keys ? totals(tid, before) : 0;
+  const bool two = tid == kGroupThreads - 1 && keys > kGroupThreads;  // the last key
+  if (two) totals(kGroupThreads, extra_before);
+  int32_t inc = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int32_t first = inc - all;
+  for (int w = 0; w < warp; ++w) first += warp_sum[w];
+  auto place = [&](int k, int32_t at, int32_t ahead) {
+    if (rank == 0) offsets[k] = at;  // key n: the number of tokens with an adapter
+    at += ahead;
+#pragma unroll
+    for (int w = 0; w < kGroupWarps; ++w) {
       const int32_t c = group_counts[w * keys + k];
       group_counts[w * keys + k] = at;
       at += c;
     }
-  }
+  };
+  if (tid < keys) place(tid, first, before);
+  if (two) place(kGroupThreads, first + all, extra_before);
   __syncthreads();
   for (int64_t b = t0; b < t1; b += 32) {
     const int64_t t = b + lane;
-    const bool in = t < t1;
-    const int key = in ? group_key(idx, t, n, nullptr) : -1;
+    const int key = t < t1 ? group_key(idx, t, n, nullptr) : -1;
     const uint32_t same = __match_any_sync(0xffffffffu, key);
-    const int before = __popc(same & ((1u << lane) - 1u));
-    if (in) order[mine[key] + before] = static_cast<int32_t>(t);
+    const int ahead = __popc(same & ((1u << lane) - 1u));
+    if (key >= 0) order[mine[key] + ahead] = static_cast<int32_t>(t);
     __syncwarp();
-    if (in && before == 0) mine[key] += __popc(same);
+    if (key >= 0 && ahead == 0) mine[key] += __popc(same);
     __syncwarp();
   }
+  if (ctas > 1) ptx::cluster_sync();  // the counts are read by the others
 }
 
 // ---------------------------------------------------------------------------

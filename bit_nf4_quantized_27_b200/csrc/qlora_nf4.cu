@@ -1291,11 +1291,28 @@ qlora_status qlora_adapter_groups(const int32_t *adapter_of_token, int64_t M, in
   if ((s = check_device(&dev, &sms)) != QLORA_OK) return s;
   static std::once_flag flags[64];
   static qlora_status results[64];
-  const int smem = (kGroupThreads / 32) * (QLORA_MAX_ADAPTERS + 1) * 4;
+  const int smem = (kGroupWarps + 1) * (QLORA_MAX_ADAPTERS + 1) * 4;
   if ((s = set_smem(adapter_groups_kernel, smem, dev, flags, results)) != QLORA_OK) return s;
-  adapter_groups_kernel<<<1, kGroupThreads, (kGroupThreads / 32) * (n + 1) * 4, reinterpret_cast<cudaStream_t>(stream)>>>(
-      adapter_of_token, M, n, order, offsets, status_ptr(ws));
-  return launch_status();
+  cudaLaunchConfig_t cfg = {};
+  const int ctas = M > kGroupOneCta ? kGroupCluster : 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kGroupThreads);
+  cfg.dynamicSmemBytes = (kGroupWarps + 1) * (n + 1) * 4;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, adapter_groups_kernel, adapter_of_token, M, n, order, offsets, status_ptr(ws)) != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return QLORA_OK;
 }
 
 qlora_status qlora_adapters_fwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets,
