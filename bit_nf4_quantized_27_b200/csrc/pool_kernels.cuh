@@ -959,23 +959,272 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------------------
-// grad: one unit is 128 features x 64 ranks of one adapter's dA or dB, summed over its tokens;
-// the CTAs of a cluster each take a part of the tokens and add up as in down.  Both
-// operands come as token rows (MN-major).  An adapter without tokens gets zeros.
-//   warp 0  loads; warp 1  products; warps 2..5  accumulator -> shared memory; all  the sum
+// grad: one unit is 128 features x 64 ranks of one adapter's dA or dB, summed over its tokens.  Both operands come as
+// token rows (MN-major), 64 tokens a step.  The first plane's products go round three accumulators and the other
+// planes' into a fourth, which keeps each one's chain of additions short.  While one unit is stored the next one's
+// tokens are loaded.  Units are taken longest adapter first, back and forth over the CTAs, so that long and short ones
+// meet: a CTA has one or two, and their lengths differ.  An adapter without tokens gets zeros.
+//   warp 0  loads; warp 1  products; warps 2..9  accumulators -> dA or dB
 // ---------------------------------------------------------------------------
-constexpr int kPoolGradThreads = 192;
-constexpr uint32_t kPoolGradTmem = 64;
-constexpr uint32_t kPoolGradBytes = 98 * 1024;  // two CTAs share an SM
+constexpr uint32_t kPoolGradTmem = 256;
 
 struct PoolGradArgs {
   PoolArgs p;
   void *dA, *dB;  // [n, r, K], [n, N, r]
   int planes;
+  uint32_t stages, bytes;
+};
+// Shared memory: the ring, then of each adapter the places of its tokens and the adapters by length.
+__host__ __device__ constexpr uint32_t pool_grad_stage(int planes) { return 16384u + planes * 8192u; }
+__host__ __device__ constexpr uint32_t pool_grad_lists(int n) { return (static_cast<uint32_t>(n) * 12u + 15u) & ~15u; }
+__host__ __device__ constexpr uint32_t pool_grad_stages(int planes, int n) {
+  return (kPoolHalfBytes - pool_grad_lists(n)) / pool_grad_stage(planes);
+}
+__host__ __device__ constexpr uint32_t pool_grad_bytes(int planes, int n) {
+  return pool_grad_stages(planes, n) * pool_grad_stage(planes) + pool_grad_lists(n);  // barriers follow: 16-byte aligned
+}
+static_assert(pool_grad_bytes(3, 1) % 16 == 0 && pool_grad_bytes(2, 7) % 16 == 0, "the barriers' alignment");
+static_assert(pool_grad_stages(3, QLORA_MAX_ADAPTERS) >= 2 && pool_grad_stages(2, 1) <= kPoolMostStages, "a ring of two stages at least");
+
+struct PoolGradUnit {
+  int ad, lo, cnt, live, fb, rb;
+  bool is_a;
 };
 
 template <typename O>
-__global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __grid_constant__ CUtensorMap tmX,
+__global__ void __launch_bounds__(kPoolThreads, 2)
+    pool_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
+                     const __grid_constant__ CUtensorMap tmDY, const __grid_constant__ CUtensorMap tmT,
+                     const __grid_constant__ CUtensorMap tmXt, const __grid_constant__ CUtensorMap tmUt,
+                     const __grid_constant__ CUtensorMap tmDYt, const __grid_constant__ CUtensorMap tmTt, const PoolGradArgs a) {
+  extern __shared__ uint8_t pool_raw[];
+  __shared__ int4 row4[16];
+  const PoolSmem sm = pool_smem(pool_raw, a.bytes);
+  const PoolArgs &p = a.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t stage_bytes = pool_grad_stage(a.planes), stages = a.stages;
+  uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *acc_full = sm.bars + 2 * kPoolMostStages;
+  uint64_t *acc_empty0 = acc_full + 1, *acc_empty1 = acc_full + 2;  // from the two sets of four warps
+  int2 *group = reinterpret_cast<int2 *>(sm.buf + stages * stage_bytes);
+  int *by_length = reinterpret_cast<int *>(group + p.n);
+  const uint32_t tmem = pool_setup(sm, kPoolGradTmem, 2 * kPoolMostStages + 1);
+  for (int i = tid; i < p.n; i += kPoolThreads) group[i] = pool_group(p, i);
+  __syncthreads();
+  for (int i = tid; i < p.n; i += kPoolThreads) {
+    // its place among the adapters, the longest first (more of them than threads: in their own order)
+    int place = i;
+    if (p.n <= kPoolThreads) {
+      const int mine = group[i].y - group[i].x;
+      place = 0;
+      for (int k = 0; k < p.n; ++k) {
+        const int len = group[k].y - group[k].x;
+        place += len > mine || (len == mine && k < i);
+      }
+    }
+    by_length[place] = i;
+  }
+  __syncthreads();
+  const int nrb = (p.r + 63) / 64;
+  const int in_a = static_cast<int>((p.K + 127) / 128) * nrb, per_adapter = in_a + static_cast<int>((p.N + 127) / 128) * nrb;
+  const int64_t units = static_cast<int64_t>(p.n) * per_adapter;
+  const int G = gridDim.x;
+  // the unit of this CTA in a round; false if the round has none for it
+  auto unit_of = [&](int64_t round, PoolGradUnit &u) {
+    const int64_t i = round * G + (round & 1 ? G - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+    if (i >= units) return false;
+    const int at = static_cast<int>(i / per_adapter);
+    int w = static_cast<int>(i - static_cast<int64_t>(at) * per_adapter);
+    u.ad = by_length[at];
+    u.is_a = w < in_a;
+    if (!u.is_a) w -= in_a;
+    u.fb = w / nrb;
+    u.rb = w - u.fb * nrb;
+    u.lo = group[u.ad].x;
+    u.cnt = group[u.ad].y - u.lo;
+    u.live = pool_rank(p, u.ad) - u.rb * 64;
+    return true;
+  };
+  RingPos pos;
+  uint32_t issued = 0, acc_phase = 0;
+  bool ok = true;
+  const int64_t rounds = (units + G - 1) / G;
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    for (int64_t round = 0; round < rounds && ok; ++round) {
+      PoolGradUnit u;
+      if (!unit_of(round, u) || u.live <= 0 || u.cnt == 0) continue;
+      const CUtensorMap *tmV = u.is_a ? &tmX : &tmDY, *tmP = u.is_a ? &tmU : &tmT;
+      const CUtensorMap *tmVt = u.is_a ? &tmXt : &tmDYt, *tmPt = u.is_a ? &tmUt : &tmTt;
+      const int g = lane & 15, last = u.lo + u.cnt - 1;
+      int4 rows = pool_rows(p, u.lo + 4 * g, last);
+      for (int t0 = 0; t0 < u.cnt && ok; t0 += 64) {
+        const int left = u.cnt - t0, groups = (min(64, left) + 15) / 16 * 4;  // whole steps of 16 tokens
+        // a run of 32 that is not whole is gathered: rows of other adapters' tokens must not meet the padding
+        const bool run = pool_run32(rows, lane, 4 * g, left, false);
+        PoolRowLoads loads;
+        loads.tiles = __ballot_sync(0xffffffffu, run && (lane & 7) == 0) & 0xffffu;
+        loads.gathers = __ballot_sync(0xffffffffu, !run && g < groups) & 0xffffu;
+        if (lane < 16) row4[lane] = rows;
+        if (t0 + 64 < u.cnt) rows = pool_rows(p, u.lo + t0 + 64 + 4 * g, last);
+        __syncwarp();
+        if (ptx::elect_one()) {
+          ok = ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag);
+          if (ok) {
+            uint8_t *d = sm.buf + pos.s * stage_bytes;
+            ptx::mbar_arrive_expect_tx(&full[pos.s], loads.bytes() * (2 + a.planes));
+            pool_load_rows(loads, row4, d, tmV, tmVt, &full[pos.s], u.fb * 128, 0);
+            pool_load_rows(loads, row4, d + 8192, tmV, tmVt, &full[pos.s], u.fb * 128 + 64, 0);
+            for (int pl = 0; pl < a.planes; ++pl)
+              pool_load_rows(loads, row4, d + 16384 + pl * 8192, tmP, tmPt, &full[pos.s], u.rb * 64, pl * static_cast<int>(p.M));
+            ++issued;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        pos.next(stages);
+      }
+    }
+    if (!ok && lane == 0) pool_fail(sm, p.status);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    const uint32_t idesc = ptx::idesc_bf16(128, 64, 1, 1);
+    constexpr uint32_t kLbo = pool_desc_lbo(true), k16s = pool_desc_16(true);
+    const uint32_t base = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024)) + kLbo;
+    const bool one = ptx::elect_one();
+    for (int64_t round = 0; round < rounds && ok; ++round) {
+      PoolGradUnit u;
+      if (!unit_of(round, u) || u.live <= 0 || u.cnt == 0) continue;
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_empty0, acc_phase ^ 1, sm.abort_flag) &&
+                                       ptx::mbar_wait(acc_empty1, acc_phase ^ 1, sm.abort_flag));
+      acc_phase ^= 1;
+      uint32_t turn = 0, used = 0;
+      for (int t0 = 0; t0 < u.cnt && ok; t0 += 64) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
+        if (!ok) break;
+        const int valid = min(64, u.cnt - t0);
+        if (valid & 15) {
+          // the last 16 tokens are not all there: zero rows of P meet repeated rows of V
+          uint8_t *d = sm.buf + pos.s * stage_bytes + 16384;
+          const int pad = 16 - (valid & 15);
+          for (int i = lane; i < pad * 8 * a.planes; i += 32) {
+            const int pl = i / (pad * 8), e = i - pl * pad * 8;
+            *reinterpret_cast<uint4 *>(d + pl * 8192 + (valid + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ptx::tc_fence_after();
+        if (one) {
+          const uint32_t v = base + pos.s * (stage_bytes >> 4), b = v + (16384 >> 4), d = tmem + turn * 64;
+          const uint32_t more = used & (1u << turn) ? 1u : 0u, rest = used ? 1u : 0u;
+#pragma unroll
+          for (int k16 = 0; k16 < 4; ++k16) {
+            if (k16 * 16 >= valid) break;
+            ptx::mma_bf16_lohi(d, v + k16 * k16s, kPoolDescHi, b + k16 * k16s, kPoolDescHi, idesc, k16 ? 1u : more);
+#pragma unroll
+            for (int pl = 1; pl < kPoolPlanes; ++pl)
+              if (pl < a.planes)
+                ptx::mma_bf16_lohi(tmem + 192, v + k16 * k16s, kPoolDescHi, b + pl * (8192 >> 4) + k16 * k16s, kPoolDescHi, idesc,
+                                   (k16 || pl > 1) ? 1u : rest);
+          }
+          ptx::mma_commit(&empty[pos.s]);
+          if (t0 + 64 >= u.cnt) ptx::mma_commit(acc_full);
+        }
+        __syncwarp();
+        used |= 1u << turn;
+        turn = turn == 2 ? 0 : turn + 1;
+        pos.next(stages);
+      }
+    }
+    if (!ok && lane == 0) pool_fail(sm, p.status);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ the gradients
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 32;
+    for (int64_t round = 0; round < rounds && ok; ++round) {
+      PoolGradUnit u;
+      if (!unit_of(round, u)) continue;
+      const bool sums = u.live > 0 && u.cnt > 0;
+      const int steps = (u.cnt + 63) / 64, j0 = u.rb * 64 + half * 32;  // ranks j0 .. j0 + 32
+      const float s = p.scales[u.ad];
+      const int64_t cols = u.is_a ? p.K : p.N, f = static_cast<int64_t>(u.fb) * 128 + quad * 32 + lane;
+      if (sums) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_full, acc_phase, sm.abort_flag));
+        acc_phase ^= 1;
+        if (!ok) break;
+        ptx::tc_fence_after();
+      }
+      for (int c = 0; c < 32; c += 16) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+        if (sums) {
+          uint32_t v[16], w[16];
+          ptx::tmem_ld16(from + c, v);
+          ptx::tmem_ld16(from + 192 + c, w);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
+          float rest[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) rest[i] = __uint_as_float(w[i]);
+          if (steps > 1) {
+            ptx::tmem_ld16(from + 64 + c, v);
+            if (steps > 2) ptx::tmem_ld16(from + 128 + c, w);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(v[i]) + (steps > 2 ? __uint_as_float(w[i]) : 0.0f);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = s * (x[i] + rest[i]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (half * 32 + c + i >= u.live) x[i] = 0.0f;
+        }
+        if (f >= cols) continue;
+        if (u.is_a) {
+          O *out = static_cast<O *>(a.dA) + (static_cast<int64_t>(u.ad) * p.r + j0 + c) * p.K + f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (j0 + c + i < p.r) pool_store(out + i * p.K, x[i]);
+        } else {
+          O *out = static_cast<O *>(a.dB) + (static_cast<int64_t>(u.ad) * p.N + f) * p.r + j0 + c;
+#pragma unroll
+          for (int i = 0; i < 16; i += 8) {
+            if (j0 + c + i >= p.r) break;  // r is a multiple of 8
+            if (sizeof(O) == 4) {
+              reinterpret_cast<float4 *>(out + i)[0] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+              reinterpret_cast<float4 *>(out + i)[1] = make_float4(x[i + 4], x[i + 5], x[i + 6], x[i + 7]);
+            } else {
+              *reinterpret_cast<uint4 *>(out + i) = make_uint4(pack_bf16x2(x[i], x[i + 1]), pack_bf16x2(x[i + 2], x[i + 3]),
+                                                               pack_bf16x2(x[i + 4], x[i + 5]), pack_bf16x2(x[i + 6], x[i + 7]));
+            }
+          }
+        }
+      }
+      if (sums) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(half ? acc_empty1 : acc_empty0);
+      }
+    }
+    if (!ok && lane == 0) pool_fail(sm, p.status);
+  }
+  if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the thread that loads
+  pool_teardown(tmem, kPoolGradTmem);
+}
+
+// ---------------------------------------------------------------------------
+// grad, split: the same for calls with so few units that CTAs would be idle.  The CTAs of a cluster each take a part of
+// a unit's tokens and add up as in down.
+//   warp 0  loads; warp 1  products; warps 2..5  accumulator -> shared memory; all  the sum
+// ---------------------------------------------------------------------------
+constexpr int kPoolGradSplitThreads = 192;
+constexpr uint32_t kPoolGradSplitTmem = 64;
+constexpr uint32_t kPoolGradSplitBytes = 98 * 1024;  // two CTAs share an SM
+
+template <typename O>
+__global__ void __launch_bounds__(kPoolGradSplitThreads) pool_grad_split_kernel(const __grid_constant__ CUtensorMap tmX,
                                                                      const __grid_constant__ CUtensorMap tmU,
                                                                      const __grid_constant__ CUtensorMap tmDY,
                                                                      const __grid_constant__ CUtensorMap tmT,
@@ -985,12 +1234,12 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
                                                                      const __grid_constant__ CUtensorMap tmTt,
                                                                      const PoolGradArgs a) {
   extern __shared__ uint8_t pool_raw[];
-  const PoolSmem sm = pool_smem(pool_raw, kPoolGradBytes);
+  const PoolSmem sm = pool_smem(pool_raw, kPoolGradSplitBytes);
   const PoolArgs &p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t stage_bytes = 16384u + a.planes * 8192u, stages = min(kPoolGradBytes / stage_bytes, kPoolMostStages);
+  const uint32_t stage_bytes = 16384u + a.planes * 8192u, stages = min(kPoolGradSplitBytes / stage_bytes, kPoolMostStages);
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *acc_full = sm.bars + 2 * kPoolMostStages;
-  const uint32_t tmem = pool_setup(sm, kPoolGradTmem, kPoolBars);
+  const uint32_t tmem = pool_setup(sm, kPoolGradSplitTmem, kPoolBars);
   const int nrb = (p.r + 63) / 64;
   const int in_a = static_cast<int>((p.K + 127) / 128) * nrb, per_adapter = in_a + static_cast<int>((p.N + 127) / 128) * nrb;
   const int64_t units = static_cast<int64_t>(p.n) * per_adapter;
@@ -1104,7 +1353,7 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
     const uint32_t exch_addr = ptx::smem_addr(exch);
     const int rows = is_a ? 64 : 128, width = is_a ? 64 : 32, pitch = is_a ? 128 : 66;  // pairs a row
     const int per = (rows + cs - 1) / cs, r_lo = min(rows, q * per), r_hi = min(rows, r_lo + per);
-    for (int e = threadIdx.x; e < (r_hi - r_lo) * width; e += kPoolGradThreads) {
+    for (int e = threadIdx.x; e < (r_hi - r_lo) * width; e += kPoolGradSplitThreads) {
       const int row = r_lo + e / width, x = 2 * (e % width);
       const int j = rb * 64 + (is_a ? row : x);
       const int64_t f = static_cast<int64_t>(fb) * 128 + (is_a ? x : row);
@@ -1132,7 +1381,7 @@ __global__ void __launch_bounds__(kPoolGradThreads) pool_grad_kernel(const __gri
     }
   }
   if (warp == 0 && lane == 0 && *sm.abort_flag) ring_drain(full, pos, stages, issued);
-  pool_teardown(tmem, kPoolGradTmem);
+  pool_teardown(tmem, kPoolGradSplitTmem);
 }
 
 }  // namespace qlora

@@ -1141,18 +1141,28 @@ qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const 
   a.dA = dA;
   a.dB = dB;
   a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
-  // split the tokens while the tiles of dA and dB leave CTAs idle (two to an SM) and a part has whole steps of 64
   const int64_t units = static_cast<int64_t>(p.n) * ((p.r + 63) / 64) * ((p.K + 127) / 128 + (p.N + 127) / 128);
+  if (2 * units >= sms || p.M < 256) {
+    a.stages = pool_grad_stages(a.planes, p.n);
+    a.bytes = pool_grad_bytes(a.planes, p.n);
+    static PoolKernelState states[64];
+    auto kernel = pool_grad_kernel<O>;
+    const qlora_status s = pool_attributes(kernel, kPoolHalfBytes, states[dev]);
+    if (s != QLORA_OK) return s;
+    return launch_pool(kernel, std::min<int64_t>(units, 2 * sms), 1, kPoolThreads, a.bytes, st, tmX, tmU, tmDY, tmT, tmXt, tmUt,
+                       tmDYt, tmTt, a);
+  }
+  // few units and tokens enough: split the tokens while CTAs (two to an SM) are idle and a part has whole steps of 64
   int cs = 8;
   while (cs > 1 && (units * cs > 4 * sms || cs * 64 > p.M)) cs /= 2;
   static PoolKernelState states[64];
-  auto kernel = pool_grad_kernel<O>;
-  const qlora_status s = pool_attributes(kernel, kPoolGradBytes, states[dev]);
+  auto kernel = pool_grad_split_kernel<O>;
+  const qlora_status s = pool_attributes(kernel, kPoolGradSplitBytes, states[dev]);
   if (s != QLORA_OK) return s;
-  const int fit = pool_fit(kernel, kPoolGradThreads, kPoolGradBytes, cs, states[dev], dev);
+  const int fit = pool_fit(kernel, kPoolGradSplitThreads, kPoolGradSplitBytes, cs, states[dev], dev);
   if (fit == 0) return QLORA_ERR_CUDA;
-  return launch_pool(kernel, std::min<int64_t>(units, fit), cs, kPoolGradThreads, kPoolGradBytes, st, tmX, tmU, tmDY, tmT, tmXt,
-                     tmUt, tmDYt, tmTt, a);
+  return launch_pool(kernel, std::min<int64_t>(units, fit), cs, kPoolGradSplitThreads, kPoolGradSplitBytes, st, tmX, tmU, tmDY, tmT,
+                     tmXt, tmUt, tmDYt, tmTt, a);
 }
 
 // The base products alone: Y = X W'^T, and dX = dY W'.
