@@ -178,19 +178,26 @@ __device__ __forceinline__ int4 pool_rows(const PoolArgs &p, int i, int last) {
   return y;
 }
 
-// Loads of token rows into a stage: 32 consecutive rows of memory come with one tiled load (box 64 x 32), other rows
-// four to a gather.  A gather costs the loading thread as much as a tiled load eight times its size (reading 67 MB by
-// gathers alone took 46 us), and requests of a packed batch are runs of rows.
-//
-// Whether the eight lanes from lane & ~7, with four rows each, hold 32 consecutive rows.  valid: rows of the tile; those
-// past it may be any rows where `loose` (at least half of the 32 must be wanted).
-__device__ __forceinline__ bool pool_run32(const int4 &y, int lane, int first, int valid, bool loose) {
-  const int base = __shfl_sync(0xffffffffu, y.x, lane & ~7) + 4 * (lane & 7), left = valid - first;
+// Loads of token rows into a stage: 32 or 16 consecutive rows of memory come with one tiled load (boxes 64 x 32 and
+// 64 x 16), other rows four to a gather.  A gather costs the loading thread about 40 cycles and a tiled load 20, whatever
+// its rows, so gathers alone bound a tile's step at several times its time (reading 67 MB by them took 46 us), and
+// requests of a packed batch are runs of rows.
+struct PoolMaps {
+  CUtensorMap row, row16, row32;
+};
+
+// Whether the kRows / 4 lanes that share this one's run hold kRows consecutive rows, four a lane.  first: of this lane's
+// rows in the tile; valid: rows of the tile; those past it may be any rows where `loose` (half of the run must be
+// wanted).
+template <int kRows>
+__device__ __forceinline__ bool pool_run(const int4 &y, int lane, int first, int valid, bool loose) {
+  constexpr int kLanes = kRows / 4;
+  const int lead = lane & ~(kLanes - 1), base = __shfl_sync(0xffffffffu, y.x, lead) + 4 * (lane - lead), left = valid - first;
   const bool seq = (y.x == base || left < 1) && (y.y == base + 1 || left < 2) && (y.z == base + 2 || left < 3) &&
                    (y.w == base + 3 || left < 4);
   const uint32_t all = __ballot_sync(0xffffffffu, seq);
-  const int wanted = valid - (first - 4 * (lane & 7));
-  return ((all >> (lane & ~7)) & 0xffu) == 0xffu && wanted >= (loose ? 16 : 32);
+  const int wanted = valid - (first - 4 * (lane - lead));
+  return ((all >> lead) & ((1u << kLanes) - 1u)) == (1u << kLanes) - 1u && wanted >= (loose ? kRows / 2 : kRows);
 }
 
 // Position in a ring of stages, with the phase of its barriers.
@@ -344,33 +351,48 @@ __device__ __forceinline__ void pool_find(const PoolArgs &p, const PoolWalk &w, 
   }
 }
 
-// The loads of a tile's token rows, four rows a lane of warp 0: whole runs of 32 and the rest (masks over lanes).
+// How up to 64 token rows, four a lane of the first 16 (the others the same again), are loaded: masks over lanes.
 struct PoolRowLoads {
-  uint32_t tiles, gathers;
-  __device__ __forceinline__ uint32_t bytes() const { return __popc(tiles) * 4096u + __popc(gathers) * 512u; }
+  uint32_t runs32, runs16, gathers;
+  __device__ __forceinline__ uint32_t bytes() const {
+    return __popc(runs32) * 4096u + __popc(runs16) * 2048u + __popc(gathers) * 512u;
+  }
 };
-__device__ __forceinline__ PoolRowLoads pool_row_loads(const PoolArgs &p, const PoolTile &t, int tn, int lane, int4 *row4) {
-  const int4 rows = t.cnt > 0 ? pool_rows(p, t.lo + 4 * min(lane, tn / 4 - 1), t.lo + t.cnt - 1) : make_int4(0, 0, 0, 0);
-  const bool mine = 4 * lane < t.cnt, run = pool_run32(rows, lane, 4 * lane, t.cnt, true);
+// valid: rows that exist; wanted: lanes with rows to load; loose: as pool_run.  The whole warp; writes row4.
+__device__ __forceinline__ PoolRowLoads pool_row_loads(const int4 &rows, int lane, int valid, int wanted, bool loose, int4 *row4) {
+  const int i = lane & 15;
+  const bool run32 = pool_run<32>(rows, lane, 4 * i, valid, loose);
+  bool run16 = pool_run<16>(rows, lane, 4 * i, valid, loose);  // outside any condition: the whole warp takes part
+  run16 = run16 && !run32;
   PoolRowLoads l;
-  l.tiles = __ballot_sync(0xffffffffu, run && (lane & 7) == 0 && mine);
-  l.gathers = __ballot_sync(0xffffffffu, !run && mine);
+  l.runs32 = __ballot_sync(0xffffffffu, run32 && (i & 7) == 0 && i < wanted) & 0xffffu;
+  l.runs16 = __ballot_sync(0xffffffffu, run16 && (i & 3) == 0 && i < wanted) & 0xffffu;
+  l.gathers = __ballot_sync(0xffffffffu, !run32 && !run16 && i < wanted) & 0xffffu;
   if (lane < 16) row4[lane] = rows;
   __syncwarp();
   return l;
 }
-// One thread: columns [x, x + 64) of the tile's rows, moved down by `down` rows, to dst.
-__device__ __forceinline__ void pool_load_rows(const PoolRowLoads &l, const int4 *row4, uint8_t *dst, const CUtensorMap *gather,
-                                               const CUtensorMap *tile, uint64_t *bar, int x, int down) {
-  for (uint32_t m = l.tiles; m; m &= m - 1) {
+// One thread: columns [x, x + 64) of the rows, moved down by `down` rows, to dst.
+__device__ __forceinline__ void pool_load_rows(const PoolRowLoads &l, const int4 *row4, uint8_t *dst, const PoolMaps *maps,
+                                               uint64_t *bar, int x, int down) {
+  for (uint32_t m = l.runs32; m; m &= m - 1) {
     const int i = __ffs(m) - 1;
-    ptx::tma_load_2d(dst + i * 512, tile, bar, x, row4[i].x + down);
+    ptx::tma_load_2d(dst + i * 512, &maps->row32, bar, x, row4[i].x + down);
+  }
+  for (uint32_t m = l.runs16; m; m &= m - 1) {
+    const int i = __ffs(m) - 1;
+    ptx::tma_load_2d(dst + i * 512, &maps->row16, bar, x, row4[i].x + down);
   }
   for (uint32_t m = l.gathers; m; m &= m - 1) {
     const int i = __ffs(m) - 1;
     const int4 y = row4[i];
-    ptx::tma_gather4(dst + i * 512, gather, bar, x, make_int4(y.x + down, y.y + down, y.z + down, y.w + down));
+    ptx::tma_gather4(dst + i * 512, &maps->row, bar, x, make_int4(y.x + down, y.y + down, y.z + down, y.w + down));
   }
+}
+// The same of a tile of up to 64 tokens.
+__device__ __forceinline__ PoolRowLoads pool_tile_loads(const PoolArgs &p, const PoolTile &t, int lane, int4 *row4) {
+  const int4 rows = t.cnt > 0 ? pool_rows(p, t.lo + 4 * (lane & 15), t.lo + t.cnt - 1) : make_int4(0, 0, 0, 0);
+  return pool_row_loads(rows, lane, t.cnt, (t.cnt + 3) / 4, true, row4);
 }
 
 // Descriptor words (128-byte swizzle, groups of eight rows 1024 bytes apart): the high one is the same for all operands,
@@ -425,8 +447,7 @@ struct PoolDownArgs {
 
 template <bool W_MN>
 __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid_constant__ CUtensorMap tmW,
-                                                                    const __grid_constant__ CUtensorMap tmV,
-                                                                    const __grid_constant__ CUtensorMap tmVt, const PoolDownArgs a) {
+                                                                    const __grid_constant__ PoolMaps tmV, const PoolDownArgs a) {
   extern __shared__ uint8_t pool_raw[];
   __shared__ int4 row4[16];
   __shared__ int warp_sum[kPoolThreads / 32];
@@ -439,7 +460,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
   const uint32_t stages = l.stages, v_bytes = tn * 128u;
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
   float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
-  if (tid < 3) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmV : &tmVt);
+  if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmV.row : tid == 2 ? &tmV.row16 : &tmV.row32);
   const uint32_t tmem = pool_setup(sm, kPoolDownTmem, kPoolBars);
   const PoolWalk walk = pool_walk(p, tn, warp_sum);
   // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
@@ -460,7 +481,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
     const int kb = rank > 0 ? min(q * k_per, k_steps) : 0, ke = rank > 0 ? min(k_steps, kb + k_per) : 0;
     const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, W_MN ? 1 : 0, 0);
     if (warp == 0) {
-      const PoolRowLoads rows = pool_row_loads(p, tile_s, tn, lane, row4);
+      const PoolRowLoads rows = pool_tile_loads(p, tile_s, lane, row4);
       if (ok && ptx::elect_one()) {
         // W's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
         const int w_loads = W_MN ? (p.r + 63) / 64 : nrb;
@@ -473,7 +494,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
           for (int i = 0; i < w_loads; ++i)
             ptx::tma_load_3d(st + v_bytes + i * (W_MN ? 8192 : 16384), &tmW, bar, W_MN ? i * 64 : ks * 64, W_MN ? ks * 64 : i * 128,
                              ad);
-          pool_load_rows(rows, row4, st, &tmV, &tmVt, bar, ks * 64, 0);
+          pool_load_rows(rows, row4, st, &tmV, bar, ks * 64, 0);
           ++issued;
           pos.next(stages);
         }
@@ -663,8 +684,7 @@ struct PoolPiece<__nv_bfloat16> {
 
 template <bool W_MN, typename O, bool VEC>
 __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_constant__ CUtensorMap tmW,
-                                                                  const __grid_constant__ CUtensorMap tmP,
-                                                                  const __grid_constant__ CUtensorMap tmPt, const PoolUpArgs a) {
+                                                                  const __grid_constant__ PoolMaps tmP, const PoolUpArgs a) {
   extern __shared__ uint8_t pool_raw[];
   __shared__ int64_t row_at[64];  // of the tile's tokens in Out, in elements; -1: not a token
   __shared__ int4 row4[16];
@@ -678,7 +698,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
   const uint32_t stages = l.stages;
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *p_full = sm.bars + 2 * kPoolMostStages;
   uint64_t *acc_full = p_full + 1, *acc_empty = acc_full + 4;
-  if (tid < 3) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmP : &tmPt);
+  if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmP.row : tid == 2 ? &tmP.row16 : &tmP.row32);
   const uint32_t tmem = pool_setup(sm, kPoolUpTmem, 2 * kPoolMostStages + 5);
   const PoolWalk walk = pool_walk(p, tn, warp_sum);
   // runs of blocks a tile: as many as give every CTA a unit
@@ -727,7 +747,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
     };
 
     if (warp == 0) {
-      const PoolRowLoads rows = pool_row_loads(p, tile_s, tn, lane, row4);
+      const PoolRowLoads rows = pool_tile_loads(p, tile_s, lane, row4);
       if (ok && mine > 0 && ptx::elect_one()) {
         // the first blocks of W, then P's rows, then the other blocks
         int b = 0, ch = 0;
@@ -735,7 +755,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
           if (i == min(static_cast<int>(stages), mine * nch) - 1) {
             ptx::mbar_arrive_expect_tx(p_full, nch * a.planes * rows.bytes());
             for (int c = 0; c < nch * a.planes; ++c)
-              pool_load_rows(rows, row4, sm.buf + l.planes_at + c * l.plane, &tmP, &tmPt, p_full, c / a.planes * 64,
+              pool_load_rows(rows, row4, sm.buf + l.planes_at + c * l.plane, &tmP, p_full, c / a.planes * 64,
                              c % a.planes * static_cast<int>(p.M));
           }
           if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
@@ -993,10 +1013,8 @@ struct PoolGradUnit {
 
 template <typename O>
 __global__ void __launch_bounds__(kPoolThreads, 2)
-    pool_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
-                     const __grid_constant__ CUtensorMap tmDY, const __grid_constant__ CUtensorMap tmT,
-                     const __grid_constant__ CUtensorMap tmXt, const __grid_constant__ CUtensorMap tmUt,
-                     const __grid_constant__ CUtensorMap tmDYt, const __grid_constant__ CUtensorMap tmTt, const PoolGradArgs a) {
+    pool_grad_kernel(const __grid_constant__ PoolMaps tmX, const __grid_constant__ PoolMaps tmU,
+                     const __grid_constant__ PoolMaps tmDY, const __grid_constant__ PoolMaps tmT, const PoolGradArgs a) {
   extern __shared__ uint8_t pool_raw[];
   __shared__ int4 row4[16];
   const PoolSmem sm = pool_smem(pool_raw, a.bytes);
@@ -1053,18 +1071,13 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
     for (int64_t round = 0; round < rounds && ok; ++round) {
       PoolGradUnit u;
       if (!unit_of(round, u) || u.live <= 0 || u.cnt == 0) continue;
-      const CUtensorMap *tmV = u.is_a ? &tmX : &tmDY, *tmP = u.is_a ? &tmU : &tmT;
-      const CUtensorMap *tmVt = u.is_a ? &tmXt : &tmDYt, *tmPt = u.is_a ? &tmUt : &tmTt;
+      const PoolMaps *tmV = u.is_a ? &tmX : &tmDY, *tmP = u.is_a ? &tmU : &tmT;
       const int g = lane & 15, last = u.lo + u.cnt - 1;
       int4 rows = pool_rows(p, u.lo + 4 * g, last);
       for (int t0 = 0; t0 < u.cnt && ok; t0 += 64) {
         const int left = u.cnt - t0, groups = (min(64, left) + 15) / 16 * 4;  // whole steps of 16 tokens
-        // a run of 32 that is not whole is gathered: rows of other adapters' tokens must not meet the padding
-        const bool run = pool_run32(rows, lane, 4 * g, left, false);
-        PoolRowLoads loads;
-        loads.tiles = __ballot_sync(0xffffffffu, run && (lane & 7) == 0) & 0xffffu;
-        loads.gathers = __ballot_sync(0xffffffffu, !run && g < groups) & 0xffffu;
-        if (lane < 16) row4[lane] = rows;
+        // a run that is not whole is gathered: rows of other adapters' tokens must not meet the padding
+        const PoolRowLoads loads = pool_row_loads(rows, lane, left, groups, false, row4);
         if (t0 + 64 < u.cnt) rows = pool_rows(p, u.lo + t0 + 64 + 4 * g, last);
         __syncwarp();
         if (ptx::elect_one()) {
@@ -1072,10 +1085,10 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
           if (ok) {
             uint8_t *d = sm.buf + pos.s * stage_bytes;
             ptx::mbar_arrive_expect_tx(&full[pos.s], loads.bytes() * (2 + a.planes));
-            pool_load_rows(loads, row4, d, tmV, tmVt, &full[pos.s], u.fb * 128, 0);
-            pool_load_rows(loads, row4, d + 8192, tmV, tmVt, &full[pos.s], u.fb * 128 + 64, 0);
+            pool_load_rows(loads, row4, d, tmV, &full[pos.s], u.fb * 128, 0);
+            pool_load_rows(loads, row4, d + 8192, tmV, &full[pos.s], u.fb * 128 + 64, 0);
             for (int pl = 0; pl < a.planes; ++pl)
-              pool_load_rows(loads, row4, d + 16384 + pl * 8192, tmP, tmPt, &full[pos.s], u.rb * 64, pl * static_cast<int>(p.M));
+              pool_load_rows(loads, row4, d + 16384 + pl * 8192, tmP, &full[pos.s], u.rb * 64, pl * static_cast<int>(p.M));
             ++issued;
           }
         }
@@ -1224,16 +1237,11 @@ constexpr uint32_t kPoolGradSplitTmem = 64;
 constexpr uint32_t kPoolGradSplitBytes = 98 * 1024;  // two CTAs share an SM
 
 template <typename O>
-__global__ void __launch_bounds__(kPoolGradSplitThreads) pool_grad_split_kernel(const __grid_constant__ CUtensorMap tmX,
-                                                                     const __grid_constant__ CUtensorMap tmU,
-                                                                     const __grid_constant__ CUtensorMap tmDY,
-                                                                     const __grid_constant__ CUtensorMap tmT,
-                                                                     const __grid_constant__ CUtensorMap tmXt,
-                                                                     const __grid_constant__ CUtensorMap tmUt,
-                                                                     const __grid_constant__ CUtensorMap tmDYt,
-                                                                     const __grid_constant__ CUtensorMap tmTt,
-                                                                     const PoolGradArgs a) {
+__global__ void __launch_bounds__(kPoolGradSplitThreads)
+    pool_grad_split_kernel(const __grid_constant__ PoolMaps tmX, const __grid_constant__ PoolMaps tmU,
+                           const __grid_constant__ PoolMaps tmDY, const __grid_constant__ PoolMaps tmT, const PoolGradArgs a) {
   extern __shared__ uint8_t pool_raw[];
+  __shared__ int4 row4[16];
   const PoolSmem sm = pool_smem(pool_raw, kPoolGradSplitBytes);
   const PoolArgs &p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1260,34 +1268,26 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads) pool_grad_split_kernel(
     const int steps = live > 0 ? (cnt + 63) / 64 : 0;
     const int s_per = (steps + cs - 1) / cs, sb = min(q * s_per, steps), se = min(steps, sb + s_per);
     if (warp == 0) {
-      const CUtensorMap *tmV = is_a ? &tmX : &tmDY, *tmP = is_a ? &tmU : &tmT;
-      const CUtensorMap *tmVt = is_a ? &tmXt : &tmDYt, *tmPt = is_a ? &tmUt : &tmTt;
+      const PoolMaps *tmV = is_a ? &tmX : &tmDY, *tmP = is_a ? &tmU : &tmT;
       const int g = lane & 15;
-      int4 rows = make_int4(0, 0, 0, 0);
-      if (sb < se) rows = pool_rows(p, grp.x + sb * 64 + 4 * g, grp.y - 1);
       for (int st = sb; st < se && ok; ++st) {
-        const int groups = (min(64, cnt - st * 64) + 15) / 16 * 4;  // whole steps of 16 tokens
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag));
-        if (!ok) break;
-        uint8_t *d = sm.buf + pos.s * stage_bytes;
-        // a group of 32 that is not whole is gathered: rows of other adapters' tokens must not meet the padding
-        const bool run = pool_run32(rows, lane, 4 * g, cnt - st * 64, false), tile_load = run && (lane & 7) == 0;
-        const bool gather = !run && g < groups;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[pos.s], groups * 512u * (2 + a.planes));
-        __syncwarp();
-        uint8_t *dv = d + (lane >> 4) * 8192 + g * 512;
-        const int xv = fb * 128 + (lane >> 4) * 64;
-        if (tile_load) ptx::tma_load_2d(dv, tmVt, &full[pos.s], xv, rows.x);
-        if (gather) ptx::tma_gather4(dv, tmV, &full[pos.s], xv, rows);
-        for (int pl = lane >> 4; pl < a.planes; pl += 2) {
-          const int o = pl * static_cast<int>(p.M);
-          uint8_t *dp = d + 16384 + pl * 8192 + g * 512;
-          if (tile_load) ptx::tma_load_2d(dp, tmPt, &full[pos.s], rb * 64, rows.x + o);
-          if (gather) ptx::tma_gather4(dp, tmP, &full[pos.s], rb * 64, make_int4(rows.x + o, rows.y + o, rows.z + o, rows.w + o));
+        const int left = cnt - st * 64, groups = (min(64, left) + 15) / 16 * 4;  // whole steps of 16 tokens
+        // a run that is not whole is gathered: rows of other adapters' tokens must not meet the padding
+        const PoolRowLoads loads =
+            pool_row_loads(pool_rows(p, grp.x + st * 64 + 4 * g, grp.y - 1), lane, left, groups, false, row4);
+        if (ptx::elect_one()) {
+          ok = ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag);
+          if (ok) {
+            uint8_t *d = sm.buf + pos.s * stage_bytes;
+            ptx::mbar_arrive_expect_tx(&full[pos.s], loads.bytes() * (2 + a.planes));
+            pool_load_rows(loads, row4, d, tmV, &full[pos.s], fb * 128, 0);
+            pool_load_rows(loads, row4, d + 8192, tmV, &full[pos.s], fb * 128 + 64, 0);
+            for (int pl = 0; pl < a.planes; ++pl)
+              pool_load_rows(loads, row4, d + 16384 + pl * 8192, tmP, &full[pos.s], rb * 64, pl * static_cast<int>(p.M));
+            ++issued;
+          }
         }
-        if (st + 1 < se) rows = pool_rows(p, grp.x + (st + 1) * 64 + 4 * g, grp.y - 1);
-        __syncwarp();
-        ++issued;
+        ok = __all_sync(0xffffffffu, ok);
         pos.next(stages);
       }
       if (!ok && lane == 0) pool_fail(sm, p.status);
@@ -1380,7 +1380,7 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads) pool_grad_split_kernel(
       pool_cluster_sync();
     }
   }
-  if (warp == 0 && lane == 0 && *sm.abort_flag) ring_drain(full, pos, stages, issued);
+  if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the thread that loads
   pool_teardown(tmem, kPoolGradSplitTmem);
 }
 

@@ -970,10 +970,11 @@ bool tmap_pool(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Token rows [rows, inner] bf16 with row stride ld: one row a box to gather, and 32 for runs of rows.
-bool tmap_tokens(CUtensorMap *gather, CUtensorMap *tile, const void *ptr, int64_t inner, int64_t rows, int64_t ld) {
-  return make_tmap(gather, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, rows, ld, 64, 1, true) &&
-         make_tmap(tile, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, rows, ld, 64, 32, true);
+// Token rows [rows, inner] bf16 with row stride ld: one row a box to gather, and 16 or 32 for runs of rows.
+bool tmap_tokens(PoolMaps *m, const void *ptr, int64_t inner, int64_t rows, int64_t ld) {
+  const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return make_tmap(&m->row, ptr, dt, 2, inner, rows, ld, 64, 1, true) && make_tmap(&m->row16, ptr, dt, 2, inner, rows, ld, 64, 16, true) &&
+         make_tmap(&m->row32, ptr, dt, 2, inner, rows, ld, 64, 32, true);
 }
 
 // A pool kernel on one device: its attributes are set at the first call, and how many clusters of a size fit the GPU at once
@@ -1076,9 +1077,10 @@ qlora_status launch_pool_down(const PoolArgs &p, const void *V, int64_t ldv, con
   a.len = W_MN ? p.N : p.K;
   a.P = P;
   a.l = pool_down_layout(p.r, (p.M / 64 + adapters) * 8 <= sms);
-  CUtensorMap tmW, tmV, tmVt;
+  CUtensorMap tmW;
+  PoolMaps tmV;
   if (!(W_MN ? tmap_pool(&tmW, W, p.r, a.len, p.n, 64) : tmap_pool(&tmW, W, a.len, p.r, p.n, std::min(p.r, 128))) ||
-      !tmap_tokens(&tmV, &tmVt, V, a.len, p.M, ldv))
+      !tmap_tokens(&tmV, V, a.len, p.M, ldv))
     return QLORA_ERR_CUDA;
   static PoolKernelState states[64];
   auto kernel = pool_down_kernel<W_MN>;
@@ -1092,7 +1094,7 @@ qlora_status launch_pool_down(const PoolArgs &p, const void *V, int64_t ldv, con
     if ((fit = pool_fit(kernel, kPoolThreads, a.l.bytes, cs, states[dev], dev)) == 0) return QLORA_ERR_CUDA;
     if (cs == 1 || fit >= tiles) break;
   }
-  return launch_pool(kernel, std::min<int64_t>(p.M / a.l.tn + adapters, fit), cs, kPoolThreads, a.l.bytes, st, tmW, tmV, tmVt, a);
+  return launch_pool(kernel, std::min<int64_t>(p.M / a.l.tn + adapters, fit), cs, kPoolThreads, a.l.bytes, st, tmW, tmV, a);
 }
 
 // Out[t] += s_a P[t] W_a for every grouped token.  Y: W = B; dX: W = A (MN-major).
@@ -1106,15 +1108,16 @@ qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const v
   a.out = Out;
   a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
   a.l = pool_up_layout(p.r, a.planes);
-  CUtensorMap tmW, tmP, tmPt;
+  CUtensorMap tmW;
+  PoolMaps tmP;
   if (!(W_MN ? tmap_pool(&tmW, W, a.cols, p.r, p.n, 64) : tmap_pool(&tmW, W, p.r, a.cols, p.n, 128)) ||
-      !tmap_tokens(&tmP, &tmPt, P, p.r, kPoolPlanes * p.M, p.r))
+      !tmap_tokens(&tmP, P, p.r, kPoolPlanes * p.M, p.r))
     return QLORA_ERR_CUDA;
   const int64_t units = (p.M / a.l.tn + std::min<int64_t>(p.n, p.M)) * ((a.cols + 127) / 128);
   auto launch = [&](auto kernel, PoolKernelState &ks) -> qlora_status {
     const qlora_status s = pool_attributes(kernel, kPoolHalfBytes, ks);
     if (s != QLORA_OK) return s;
-    return launch_pool(kernel, std::min<int64_t>(units, 2 * sms), 1, kPoolThreads, a.l.bytes, st, tmW, tmP, tmPt, a);
+    return launch_pool(kernel, std::min<int64_t>(units, 2 * sms), 1, kPoolThreads, a.l.bytes, st, tmW, tmP, a);
   };
   static PoolKernelState states[2][64];
   const bool vec = aligned(Out, 16) && ldo * sizeof(O) % 16 == 0;
@@ -1131,10 +1134,9 @@ template <typename O>
 qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const void *X, int64_t ldx,
                                const __nv_bfloat16 *T, const void *dY, int64_t lddy, void *dA, void *dB, int dev,
                                int sms, cudaStream_t st) {
-  CUtensorMap tmX{}, tmU{}, tmDY{}, tmT{}, tmXt{}, tmUt{}, tmDYt{}, tmTt{};
-  if (p.M > 0 &&
-      (!tmap_tokens(&tmX, &tmXt, X, p.K, p.M, ldx) || !tmap_tokens(&tmU, &tmUt, U, p.r, kPoolPlanes * p.M, p.r) ||
-       !tmap_tokens(&tmDY, &tmDYt, dY, p.N, p.M, lddy) || !tmap_tokens(&tmT, &tmTt, T, p.r, kPoolPlanes * p.M, p.r)))
+  PoolMaps tmX{}, tmU{}, tmDY{}, tmT{};
+  if (p.M > 0 && (!tmap_tokens(&tmX, X, p.K, p.M, ldx) || !tmap_tokens(&tmU, U, p.r, kPoolPlanes * p.M, p.r) ||
+                  !tmap_tokens(&tmDY, dY, p.N, p.M, lddy) || !tmap_tokens(&tmT, T, p.r, kPoolPlanes * p.M, p.r)))
     return QLORA_ERR_CUDA;
   PoolGradArgs a;
   a.p = p;
@@ -1149,8 +1151,7 @@ qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const 
     auto kernel = pool_grad_kernel<O>;
     const qlora_status s = pool_attributes(kernel, kPoolHalfBytes, states[dev]);
     if (s != QLORA_OK) return s;
-    return launch_pool(kernel, std::min<int64_t>(units, 2 * sms), 1, kPoolThreads, a.bytes, st, tmX, tmU, tmDY, tmT, tmXt, tmUt,
-                       tmDYt, tmTt, a);
+    return launch_pool(kernel, std::min<int64_t>(units, 2 * sms), 1, kPoolThreads, a.bytes, st, tmX, tmU, tmDY, tmT, a);
   }
   // few units and tokens enough: split the tokens while CTAs (two to an SM) are idle and a part has whole steps of 64
   int cs = 8;
@@ -1161,8 +1162,7 @@ qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const 
   if (s != QLORA_OK) return s;
   const int fit = pool_fit(kernel, kPoolGradSplitThreads, kPoolGradSplitBytes, cs, states[dev], dev);
   if (fit == 0) return QLORA_ERR_CUDA;
-  return launch_pool(kernel, std::min<int64_t>(units, fit), cs, kPoolGradSplitThreads, kPoolGradSplitBytes, st, tmX, tmU, tmDY, tmT,
-                     tmXt, tmUt, tmDYt, tmTt, a);
+  return launch_pool(kernel, std::min<int64_t>(units, fit), cs, kPoolGradSplitThreads, kPoolGradSplitBytes, st, tmX, tmU, tmDY, tmT, a);
 }
 
 // The base products alone: Y = X W'^T, and dX = dY W'.

@@ -67,8 +67,10 @@ def _hold(name, got, ref, mag1, mag2, terms, inner, dt):
     assert not ref.size or float(np.sqrt(np.mean(err ** 2))) <= rel * rms, f"{name}: rms"
 
 
-def _check_all(m, n_out, k, r, n, seed, dt="f32", ranks=None, none=0.2, used=None, junk=False, saved=True):
+def _check_all(m, n_out, k, r, n, seed, dt="f32", ranks=None, none=0.2, used=None, junk=False, saved=True,
+               given=None):
     idx, A, B, scales, X, dY = _setup(m, n_out, k, r, n, seed, ranks, none, used, junk)
+    idx = idx if given is None else given
     Y0, dX0 = I.normal((m, n_out), 1.0, seed + 6, DT[dt]), I.normal((m, k), 1.0, seed + 7, DT[dt])
     pool = _pool(A, B, scales, ranks)
     groups = bd.adapter_groups(idx.cuda(), n)
@@ -132,6 +134,30 @@ def test_forward_and_gradients(m, n_out, k, r, n, seed, dt):
 def test_long_sums():
     """One adapter with all tokens, and the longest contractions of a layer."""
     _check_all(600, 2048, 2752, 64, 1, 30, none=0.0)
+
+
+@pytest.mark.parametrize("n_out,k,r", [(264, 136, 16), (1160, 1096, 72)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[1, 16, 15, 17, 31, 32, 33, 47, 48, 63, 64, 65, 80, 96], [300, 3, 129], [5, 5, 5, 5]])
+def test_runs_of_rows(lengths, dt, n_out, k, r):
+    """Requests one behind the other, adapters in turns, one without: runs of rows of every
+    length, whole and cut by tiles."""
+    n = 5
+    given = torch.cat([torch.full((c,), (3 * i) % n if i % 6 != 4 else -1, dtype=torch.int32) for i, c in enumerate(lengths)])
+    _check_all(given.numel(), n_out, k, r, n, 33, dt, given=given)
+
+
+@pytest.mark.parametrize("m,n,used", [(700, 1024, None), (700, 321, 3), (3, 1024, None), (4, 2, 1)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_many_adapters_and_few_tokens(m, n, used, dt):
+    _check_all(m, 72, 80, 8, n, 35, dt, used=used, none=0.0)
+
+
+def test_more_tiles_than_fit_at_once():
+    """Every kernel takes several rounds; long groups beside short ones."""
+    g = torch.Generator().manual_seed(36)
+    given = torch.where(torch.rand(9000, generator=g) < 0.3, 1, torch.randint(0, 60, (9000,), generator=g)).to(torch.int32)
+    _check_all(9000, 264, 328, 64, 60, 37, "bf16", given=given)
 
 
 @pytest.mark.parametrize("r,ranks", [(64, [8, 64, 24, 0, 56]), (128, [72, 128, 8, 0, 120]), (256, [200, 136, 0, 256, 40]),
