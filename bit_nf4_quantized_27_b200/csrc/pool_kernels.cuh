@@ -411,7 +411,9 @@ __host__ __device__ constexpr uint32_t pool_desc_16(bool mn) { return mn ? 128u 
 // planes in HBM, no further launch, and the same bits every time.  g, a divisor of the cluster, follows on the device
 // from the number of tiles.
 //   warp 0  loads; warp 1  products; warps 2..9  accumulators -> shared memory; all  the sums
-// W_MN false: W is [n][r][len], K-major (T: A); true: [n][len][r], MN-major (U: B).
+// A launch has one or two sums to do (a backward whose T was not kept does U and T, which saves a launch that would wait
+// for the other's last tiles); each has clusters of its own.
+// mn false: W is [n][r][len], K-major (T: A); true: [n][len][r], MN-major (U: B).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kPoolDownTmem = 256;
 // Shared memory: two CTAs an SM, or all of it for one.
@@ -438,21 +440,33 @@ __host__ __device__ constexpr PoolDownLayout pool_down_layout(int r, bool roomy)
 static_assert(pool_down_layout(64, false).stages >= 3 && pool_down_layout(128, false).stages >= 3 && pool_down_layout(256, false).stages >= 3,
               "a ring of three stages at least");
 
-struct PoolDownArgs {
-  PoolArgs p;
+struct PoolDownJob {
+  CUtensorMap W;
+  PoolMaps V;
   int64_t len;       // columns of V
   __nv_bfloat16 *P;  // [3, M, r]
+  int first, clusters;  // its clusters
+  bool mn;
+};
+struct PoolDownArgs {
+  PoolDownJob job[2];
+  PoolArgs p;
   PoolDownLayout l;
 };
 
-template <bool W_MN>
-__global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid_constant__ CUtensorMap tmW,
-                                                                    const __grid_constant__ PoolMaps tmV, const PoolDownArgs a) {
+// kSums: T, U, or both (found at run time, they cost a call with one token 0.9 us of 12.8).
+enum PoolSums { kPoolT, kPoolU, kPoolBoth };
+template <PoolSums kSums>
+__global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid_constant__ PoolDownArgs a) {
   extern __shared__ uint8_t pool_raw[];
   __shared__ int4 row4[16];
   __shared__ int warp_sum[kPoolThreads / 32];
   __shared__ PoolTile tile_s;
-  constexpr uint32_t kWLbo = pool_desc_lbo(W_MN), kW16 = pool_desc_16(W_MN);
+  const int cluster = static_cast<int>(ptx::cluster_nctarank()), crank = static_cast<int>(ptx::cluster_ctarank());
+  const PoolDownJob &job = a.job[kSums == kPoolBoth && blockIdx.x / cluster >= a.job[0].clusters];
+  const int grid = kSums == kPoolBoth ? job.clusters * cluster : gridDim.x;
+  const int bid = kSums == kPoolBoth ? blockIdx.x - job.first * cluster : blockIdx.x;
+  const bool mn = kSums == kPoolBoth ? job.mn : kSums == kPoolU;
   const PoolArgs &p = a.p;
   const PoolDownLayout &l = a.l;
   const PoolSmem sm = pool_smem(pool_raw, l.bytes);
@@ -460,41 +474,39 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
   const uint32_t stages = l.stages, v_bytes = tn * 128u;
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
   float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
-  if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmV.row : tid == 2 ? &tmV.row16 : &tmV.row32);
+  if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &job.W : tid == 1 ? &job.V.row : tid == 2 ? &job.V.row16 : &job.V.row32);
   const uint32_t tmem = pool_setup(sm, kPoolDownTmem, kPoolBars);
   const PoolWalk walk = pool_walk(p, tn, warp_sum);
   // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
-  const int cluster = static_cast<int>(ptx::cluster_nctarank()), crank = static_cast<int>(ptx::cluster_ctarank());
   int g = cluster;
-  while (g > 1 && (static_cast<int64_t>(walk.tiles) * g > gridDim.x || cluster % g)) --g;
+  while (g > 1 && (static_cast<int64_t>(walk.tiles) * g > grid || cluster % g)) --g;
   const int q = crank % g, peers = crank - q;  // the g CTAs from rank `peers` of the cluster
-  const int k_steps = static_cast<int>((a.len + 63) / 64), k_per = (k_steps + g - 1) / g;
+  const int k_steps = static_cast<int>((job.len + 63) / 64), k_per = (k_steps + g - 1) / g;
   const int nrb = (p.r + 127) / 128, acc_cols = tn * nrb;  // one of the four accumulators
   RingPos pos;
   uint32_t sum_phase = 0, issued = 0;
   bool ok = true;
   // all CTAs of a cluster walk as long as the first of its tiles exists
-  for (int lead = (blockIdx.x - crank) / g; lead < walk.tiles; lead += gridDim.x / g) {
+  for (int lead = (bid - crank) / g; lead < walk.tiles; lead += grid / g) {
     pool_find(p, walk, tn, lead + crank / g, &tile_s);
     __syncthreads();
     const int ad = tile_s.ad, lo = tile_s.lo, cnt = tile_s.cnt, rank = tile_s.rank;
     const int kb = rank > 0 ? min(q * k_per, k_steps) : 0, ke = rank > 0 ? min(k_steps, kb + k_per) : 0;
-    const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, W_MN ? 1 : 0, 0);
+    const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, mn ? 1 : 0, 0);
     if (warp == 0) {
       const PoolRowLoads rows = pool_tile_loads(p, tile_s, lane, row4);
       if (ok && ptx::elect_one()) {
         // W's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
-        const int w_loads = W_MN ? (p.r + 63) / 64 : nrb;
-        const uint32_t bytes = w_loads * (W_MN ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u) + rows.bytes();
+        const int w_loads = mn ? (p.r + 63) / 64 : nrb;
+        const uint32_t bytes = w_loads * (mn ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u) + rows.bytes();
         for (int ks = kb; ks < ke; ++ks) {
           if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
           uint8_t *st = sm.buf + pos.s * l.stage;
           uint64_t *bar = &full[pos.s];
           ptx::mbar_arrive_expect_tx(bar, bytes);
           for (int i = 0; i < w_loads; ++i)
-            ptx::tma_load_3d(st + v_bytes + i * (W_MN ? 8192 : 16384), &tmW, bar, W_MN ? i * 64 : ks * 64, W_MN ? ks * 64 : i * 128,
-                             ad);
-          pool_load_rows(rows, row4, st, &tmV, bar, ks * 64, 0);
+            ptx::tma_load_3d(st + v_bytes + i * (mn ? 8192 : 16384), &job.W, bar, mn ? i * 64 : ks * 64, mn ? ks * 64 : i * 128, ad);
+          pool_load_rows(rows, row4, st, &job.V, bar, ks * 64, 0);
           ++issued;
           pos.next(stages);
         }
@@ -503,19 +515,20 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
       __syncwarp();
     } else if (warp == 1) {
       if (ok && ptx::elect_one()) {
+        const uint32_t w_lbo = pool_desc_lbo(mn), w_16 = pool_desc_16(mn);
         const uint32_t v_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
         for (int ks = kb; ks < ke; ++ks) {
           if (!ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag)) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint32_t v = v_lo + pos.s * (l.stage >> 4), w = v + (v_bytes >> 4) + kWLbo, d = tmem + ((ks - kb) & 3) * acc_cols;
+          const uint32_t v = v_lo + pos.s * (l.stage >> 4), w = v + (v_bytes >> 4) + w_lbo, d = tmem + ((ks - kb) & 3) * acc_cols;
           const uint32_t more = ks - kb >= 4 ? 1u : 0u;
 #pragma unroll
           for (int k16 = 0; k16 < 4; ++k16)
-            ptx::mma_bf16_lohi(d, w + k16 * kW16, kPoolDescHi, v + k16 * 2, kPoolDescHi, idesc, k16 ? 1u : more);
+            ptx::mma_bf16_lohi(d, w + k16 * w_16, kPoolDescHi, v + k16 * 2, kPoolDescHi, idesc, k16 ? 1u : more);
           if (nrb > 1) {  // ranks 128 and up
 #pragma unroll
             for (int k16 = 0; k16 < 4; ++k16)
-              ptx::mma_bf16_lohi(d + tn, w + 1024 + k16 * kW16, kPoolDescHi, v + k16 * 2, kPoolDescHi, idesc, k16 ? 1u : more);
+              ptx::mma_bf16_lohi(d + tn, w + 1024 + k16 * w_16, kPoolDescHi, v + k16 * 2, kPoolDescHi, idesc, k16 ? 1u : more);
           }
           ptx::mma_commit(&empty[pos.s]);
           pos.next(stages);
@@ -578,7 +591,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
             if (r < g) { x.x += u[r].x; x.y += u[r].y; x.z += u[r].z; x.w += u[r].w; }
         }
         if (t < 0) continue;
-        __nv_bfloat16 *out = a.P + static_cast<int64_t>(t) * p.r + j;
+        __nv_bfloat16 *out = job.P + static_cast<int64_t>(t) * p.r + j;
 #pragma unroll
         for (int pl = 0; pl < kPoolPlanes; ++pl) {
           const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));

@@ -1068,33 +1068,78 @@ qlora_status launch_pool(void (*kernel)(KArgs...), int64_t clusters, int cs, int
 }
 
 // P = V W_a for every grouped token.  T: V = X, W = A; U: V = dY, W = B (MN-major).
-template <bool W_MN>
-qlora_status launch_pool_down(const PoolArgs &p, const void *V, int64_t ldv, const void *W, __nv_bfloat16 *P, int dev, int sms,
-                              cudaStream_t st) {
+struct PoolDown {
+  const void *V;
+  int64_t ldv;
+  const void *W;
+  __nv_bfloat16 *P;
+  bool mn;
+};
+
+// Clusters of cs CTAs for one or two sums over `tiles` tiles each, steps[i] steps of 64 long: what the longest CTA does.
+int64_t pool_down_steps(int64_t tiles, int64_t steps, int64_t clusters, int cs) {
+  int g = cs;
+  while (g > 1 && (tiles * g > clusters * cs || cs % g)) --g;
+  const int64_t at_once = clusters * cs / g;
+  return (tiles + at_once - 1) / at_once * ((steps + g - 1) / g);
+}
+
+// T, U, or U and T in one launch.
+template <PoolSums kSums>
+qlora_status launch_pool_down(const PoolArgs &p, const PoolDown *jobs, int dev, int sms, cudaStream_t st) {
+  constexpr int n_jobs = kSums == kPoolBoth ? 2 : 1;
+  auto kernel = pool_down_kernel<kSums>;
   const int64_t adapters = std::min<int64_t>(p.n, p.M);
-  PoolDownArgs a;
+  PoolDownArgs a = {};
   a.p = p;
-  a.len = W_MN ? p.N : p.K;
-  a.P = P;
-  a.l = pool_down_layout(p.r, (p.M / 64 + adapters) * 8 <= sms);
-  CUtensorMap tmW;
-  PoolMaps tmV;
-  if (!(W_MN ? tmap_pool(&tmW, W, p.r, a.len, p.n, 64) : tmap_pool(&tmW, W, a.len, p.r, p.n, std::min(p.r, 128))) ||
-      !tmap_tokens(&tmV, V, a.len, p.M, ldv))
-    return QLORA_ERR_CUDA;
+  a.l = pool_down_layout(p.r, (p.M / 64 + adapters) * 8 * n_jobs <= sms);
+  int64_t steps[2] = {0, 0};
+  for (int i = 0; i < n_jobs; ++i) {
+    const PoolDown &d = jobs[i];
+    PoolDownJob &j = a.job[i];
+    j.len = d.mn ? p.N : p.K;
+    j.P = d.P;
+    j.mn = d.mn;
+    steps[i] = (j.len + 63) / 64;
+    if (!(d.mn ? tmap_pool(&j.W, d.W, p.r, j.len, p.n, 64) : tmap_pool(&j.W, d.W, j.len, p.r, p.n, std::min(p.r, 128))) ||
+        !tmap_tokens(&j.V, d.V, j.len, p.M, d.ldv))
+      return QLORA_ERR_CUDA;
+  }
   static PoolKernelState states[64];
-  auto kernel = pool_down_kernel<W_MN>;
   const qlora_status s = pool_attributes(kernel, kPoolFullBytes, states[dev]);
   if (s != QLORA_OK) return s;
   // CTAs a tile: as many as let the tiles run at once, taken that three of four adapters that may have tokens have a short
-  // tile.  The kernel splits a cluster over several tiles, or walks, where there are more.
-  const int64_t tiles = (p.M + a.l.tn - 1) / a.l.tn + adapters * 3 / 4;
-  int cs = 8, fit = 0;
-  for (;; cs = cs > 2 ? cs - 2 : 1) {
-    if ((fit = pool_fit(kernel, kPoolThreads, a.l.bytes, cs, states[dev], dev)) == 0) return QLORA_ERR_CUDA;
-    if (cs == 1 || fit >= tiles) break;
+  // tile.  The kernel splits a cluster over several tiles, or walks, where there are more.  Two sums share the clusters so
+  // that the one that takes longer has the fewest steps.
+  const int64_t tiles = (p.M + a.l.tn - 1) / a.l.tn + adapters * 3 / 4, most = p.M / a.l.tn + adapters;
+  int best_cs = 0, c0 = 0, c1 = 0;
+  int64_t best = 0;
+  for (int cs = 8; cs > 0; cs = cs > 2 ? cs - 2 : cs - 1) {
+    const int fit = pool_fit(kernel, kPoolThreads, a.l.bytes, cs, states[dev], dev);
+    if (fit == 0) return QLORA_ERR_CUDA;
+    if (n_jobs == 1) {
+      best_cs = cs;
+      c0 = static_cast<int>(std::min<int64_t>(most, fit));
+      if (fit >= tiles) break;
+      continue;
+    }
+    for (int g = 0; g <= cs; ++g) {  // the second one's: by length, or g CTAs a tile
+      if (g > 0 && cs % g) continue;
+      const int64_t want = g ? (tiles * g + cs - 1) / cs : fit * steps[1] / (steps[0] + steps[1]);
+      const int64_t x1 = std::max<int64_t>(1, std::min({want, most, static_cast<int64_t>(fit) - 1}));
+      const int64_t x0 = std::max<int64_t>(1, std::min<int64_t>(most, fit - x1));
+      const int64_t t = std::max(pool_down_steps(tiles, steps[0], x0, cs), pool_down_steps(tiles, steps[1], x1, cs));
+      if (best_cs == 0 || t < best) {
+        best = t;
+        best_cs = cs;
+        c0 = static_cast<int>(x0);
+        c1 = static_cast<int>(x1);
+      }
+    }
   }
-  return launch_pool(kernel, std::min<int64_t>(p.M / a.l.tn + adapters, fit), cs, kPoolThreads, a.l.bytes, st, tmW, tmV, a);
+  a.job[0].clusters = a.job[1].first = c0;
+  a.job[1].clusters = c1;
+  return launch_pool(kernel, c0 + c1, best_cs, kPoolThreads, a.l.bytes, st, a);
 }
 
 // Out[t] += s_a P[t] W_a for every grouped token.  Y: W = B; dX: W = A (MN-major).
@@ -1249,7 +1294,8 @@ qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, cons
     if (s != QLORA_OK) return s;
   }
   __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
-  const qlora_status s = launch_pool_down<false>(a, X, ldx, pool->A, T, dev, sms, st);
+  const PoolDown down = {X, ldx, pool->A, T, false};
+  const qlora_status s = launch_pool_down<kPoolT>(a, &down, dev, sms, st);
   return s != QLORA_OK ? s : launch_pool_up<false>(a, T, pool->B, Y, ldy, y_dtype, dev, sms, st);
 }
 
@@ -1261,14 +1307,18 @@ qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, cons
   __nv_bfloat16 *U = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
   const __nv_bfloat16 *T = static_cast<const __nv_bfloat16 *>(T_saved);
   qlora_status s;
-  if (M > 0) {
-    if ((dX || dA) && (s = launch_pool_down<true>(a, dY, lddy, pool->B, U, dev, sms, st)) != QLORA_OK) return s;
-    if (dX && (s = launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, dev, sms, st)) != QLORA_OK) return s;
+  if (M > 0 && (dX || dA)) {
+    PoolDown down[2] = {{dY, lddy, pool->B, U, true}, {}};
     if (dA && !T) {
       __nv_bfloat16 *Tw = U + align256(static_cast<size_t>(kPoolPlanes) * M * a.r * 2) / 2;
-      if ((s = launch_pool_down<false>(a, X, ldx, pool->A, Tw, dev, sms, st)) != QLORA_OK) return s;
+      down[1] = {X, ldx, pool->A, Tw, false};
       T = Tw;
+      s = launch_pool_down<kPoolBoth>(a, down, dev, sms, st);
+    } else {
+      s = launch_pool_down<kPoolU>(a, down, dev, sms, st);
     }
+    if (s != QLORA_OK) return s;
+    if (dX && (s = launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, dev, sms, st)) != QLORA_OK) return s;
   }
   if (!dA) return QLORA_OK;
   return grad_dtype == QLORA_F32 ? launch_pool_grads<float>(a, U, X, ldx, T, dY, lddy, dA, dB, dev, sms, st)
