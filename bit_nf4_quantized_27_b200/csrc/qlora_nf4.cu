@@ -1318,11 +1318,14 @@ qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, cons
       s = launch_pool_down<kPoolU>(a, down, dev, sms, st);
     }
     if (s != QLORA_OK) return s;
-    if (dX && (s = launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, dev, sms, st)) != QLORA_OK) return s;
   }
-  if (!dA) return QLORA_OK;
-  return grad_dtype == QLORA_F32 ? launch_pool_grads<float>(a, U, X, ldx, T, dY, lddy, dA, dB, dev, sms, st)
-                                 : launch_pool_grads<__nv_bfloat16>(a, U, X, ldx, T, dY, lddy, dA, dB, dev, sms, st);
+  // the gradients first: they find X and dY, as far as it holds them, in L2
+  if (dA) {
+    s = grad_dtype == QLORA_F32 ? launch_pool_grads<float>(a, U, X, ldx, T, dY, lddy, dA, dB, dev, sms, st)
+                                : launch_pool_grads<__nv_bfloat16>(a, U, X, ldx, T, dY, lddy, dA, dB, dev, sms, st);
+    if (s != QLORA_OK) return s;
+  }
+  return M > 0 && dX ? launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, dev, sms, st) : QLORA_OK;
 }
 
 qlora_status check_out(const void *p, int64_t ld, int64_t cols, qlora_dtype dt) {
