@@ -178,12 +178,13 @@ __device__ __forceinline__ int4 pool_rows(const PoolArgs &p, int i, int last) {
   return y;
 }
 
-// Loads of token rows into a stage: 32 or 16 consecutive rows of memory come with one tiled load (boxes 64 x 32 and
-// 64 x 16), other rows four to a gather.  A gather costs the loading thread about 40 cycles and a tiled load 20, whatever
-// its rows, so gathers alone bound a tile's step at several times its time (reading 67 MB by them took 46 us), and
-// requests of a packed batch are runs of rows.
+// Loads of token rows into a stage: 64, 32 or 16 consecutive rows of memory come with one tiled load, other rows four to a
+// gather.  Each load costs the loading thread about 130 cycles, whatever its rows, which with gathers alone bounds a step
+// of 64 tokens at many times its time (reading 67 MB by them took 46 us), and with two tiled loads of 32 rows still at
+// twice it (2048 tokens' gradients 40 us, and 3x us with one); requests of a packed batch are runs of rows.  Of the planes,
+// 64 rows of all that are used come with one load.
 struct PoolMaps {
-  CUtensorMap row, row16, row32;
+  CUtensorMap row, row16, row32, row64;
 };
 
 // Whether the kRows / 4 lanes that share this one's run hold kRows consecutive rows, four a lane.  first: of this lane's
@@ -353,20 +354,31 @@ __device__ __forceinline__ void pool_find(const PoolArgs &p, const PoolWalk &w, 
   }
 }
 
-// How up to 64 token rows, four a lane of the first 16 (the others the same again), are loaded: masks over lanes.
+// How up to 64 token rows, four a lane of the first 16 (the others the same again), are loaded: as 64 rows from row64, or
+// (row64 < 0) by masks over lanes.
 struct PoolRowLoads {
+  int row64;
   uint32_t runs32, runs16, gathers;
-  __device__ __forceinline__ uint32_t bytes() const {
-    return __popc(runs32) * 4096u + __popc(runs16) * 2048u + __popc(gathers) * 512u;
+  __device__ __forceinline__ uint32_t bytes() const {  // of 64 columns
+    return row64 >= 0 ? 8192u : __popc(runs32) * 4096u + __popc(runs16) * 2048u + __popc(gathers) * 512u;
   }
 };
 // valid: rows that exist; wanted: lanes with rows to load; loose: as pool_run.  The whole warp; writes row4.
 __device__ __forceinline__ PoolRowLoads pool_row_loads(const int4 &rows, int lane, int valid, int wanted, bool loose, int4 *row4) {
   const int i = lane & 15;
+  PoolRowLoads l = {-1, 0u, 0u, 0u};
+  const int first = __shfl_sync(0xffffffffu, rows.x, 0);
+  if (valid >= (loose ? 33 : 64)) {  // the same for the whole warp, as are the ballots' results
+    const int base = first + 4 * i, left = valid - 4 * i;
+    if (__all_sync(0xffffffffu, (rows.x == base || left < 1) && (rows.y == base + 1 || left < 2) &&
+                                    (rows.z == base + 2 || left < 3) && (rows.w == base + 3 || left < 4))) {
+      l.row64 = first;
+      return l;
+    }
+  }
   const bool run32 = pool_run<32>(rows, lane, 4 * i, valid, loose);
   bool run16 = pool_run<16>(rows, lane, 4 * i, valid, loose);  // outside any condition: the whole warp takes part
   run16 = run16 && !run32;
-  PoolRowLoads l;
   l.runs32 = __ballot_sync(0xffffffffu, run32 && (i & 7) == 0 && i < wanted) & 0xffffu;
   l.runs16 = __ballot_sync(0xffffffffu, run16 && (i & 3) == 0 && i < wanted) & 0xffffu;
   l.gathers = __ballot_sync(0xffffffffu, !run32 && !run16 && i < wanted) & 0xffffu;
@@ -375,8 +387,8 @@ __device__ __forceinline__ PoolRowLoads pool_row_loads(const int4 &rows, int lan
   return l;
 }
 // One thread: columns [x, x + 64) of the rows, moved down by `down` rows, to dst.
-__device__ __forceinline__ void pool_load_rows(const PoolRowLoads &l, const int4 *row4, uint8_t *dst, const PoolMaps *maps,
-                                               uint64_t *bar, int x, int down) {
+__device__ __forceinline__ void pool_load_parts(const PoolRowLoads &l, const int4 *row4, uint8_t *dst, const PoolMaps *maps,
+                                                uint64_t *bar, int x, int down) {
   for (uint32_t m = l.runs32; m; m &= m - 1) {
     const int i = __ffs(m) - 1;
     ptx::tma_load_2d(dst + i * 512, &maps->row32, bar, x, row4[i].x + down);
@@ -390,6 +402,21 @@ __device__ __forceinline__ void pool_load_rows(const PoolRowLoads &l, const int4
     const int4 y = row4[i];
     ptx::tma_gather4(dst + i * 512, &maps->row, bar, x, make_int4(y.x + down, y.y + down, y.z + down, y.w + down));
   }
+}
+__device__ __forceinline__ void pool_load_rows(const PoolRowLoads &l, const int4 *row4, uint8_t *dst, const PoolMaps *maps,
+                                               uint64_t *bar, int x) {
+  if (l.row64 >= 0)
+    ptx::tma_load_2d(dst, &maps->row64, bar, x, l.row64);
+  else
+    pool_load_parts(l, row4, dst, maps, bar, x, 0);
+}
+// The same of the planes [3, M, r], `pitch` bytes from one to the next.
+__device__ __forceinline__ void pool_load_planes(const PoolRowLoads &l, const int4 *row4, uint8_t *dst, const PoolMaps *maps,
+                                                 uint64_t *bar, int x, int planes, int M, uint32_t pitch) {
+  if (l.row64 >= 0)
+    ptx::tma_load_3d(dst, &maps->row64, bar, x, l.row64, 0);  // pitch: 8192
+  else
+    for (int pl = 0; pl < planes; ++pl) pool_load_parts(l, row4, dst + pl * pitch, maps, bar, x, pl * M);
 }
 // The same of a tile of up to 64 tokens.
 __device__ __forceinline__ PoolRowLoads pool_tile_loads(const PoolArgs &p, const PoolTile &t, int lane, int4 *row4) {
@@ -476,7 +503,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
   const uint32_t stages = l.stages, v_bytes = tn * 128u;
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
   float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
-  if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &job.W : tid == 1 ? &job.V.row : tid == 2 ? &job.V.row16 : &job.V.row32);
+  if (tid < 5) ptx::prefetch_tmap(tid == 0 ? &job.W : tid == 1 ? &job.V.row : tid == 2 ? &job.V.row16 : tid == 3 ? &job.V.row32 : &job.V.row64);
   const uint32_t tmem = pool_setup(sm, kPoolDownTmem, kPoolBars);
   const PoolWalk walk = pool_walk(p, tn, warp_sum);
   // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
@@ -508,7 +535,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
           ptx::mbar_arrive_expect_tx(bar, bytes);
           for (int i = 0; i < w_loads; ++i)
             ptx::tma_load_3d(st + v_bytes + i * (mn ? 8192 : 16384), &job.W, bar, mn ? i * 64 : ks * 64, mn ? ks * 64 : i * 128, ad);
-          pool_load_rows(rows, row4, st, &job.V, bar, ks * 64, 0);
+          pool_load_rows(rows, row4, st, &job.V, bar, ks * 64);
           ++issued;
           pos.next(stages);
         }
@@ -713,7 +740,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
   const uint32_t stages = l.stages;
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *p_full = sm.bars + 2 * kPoolMostStages;
   uint64_t *acc_full = p_full + 1, *acc_empty = acc_full + 4;
-  if (tid < 4) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmP.row : tid == 2 ? &tmP.row16 : &tmP.row32);
+  if (tid < 5) ptx::prefetch_tmap(tid == 0 ? &tmW : tid == 1 ? &tmP.row : tid == 2 ? &tmP.row16 : tid == 3 ? &tmP.row32 : &tmP.row64);
   const uint32_t tmem = pool_setup(sm, kPoolUpTmem, 2 * kPoolMostStages + 5);
   const PoolWalk walk = pool_walk(p, tn, warp_sum);
   // runs of blocks a tile: as many as give every CTA a unit
@@ -769,9 +796,9 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
         for (int i = 0; i < mine * nch; ++i) {
           if (i == min(static_cast<int>(stages), mine * nch) - 1) {
             ptx::mbar_arrive_expect_tx(p_full, nch * a.planes * rows.bytes());
-            for (int c = 0; c < nch * a.planes; ++c)
-              pool_load_rows(rows, row4, sm.buf + l.planes_at + c * l.plane, &tmP, p_full, c / a.planes * 64,
-                             c % a.planes * static_cast<int>(p.M));
+            for (int c = 0; c < nch; ++c)
+              pool_load_planes(rows, row4, sm.buf + l.planes_at + c * a.planes * l.plane, &tmP, p_full, c * 64, a.planes,
+                               static_cast<int>(p.M), l.plane);
           }
           if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
           const int f = (q + b * g) * 128, x = ch * 64;
@@ -968,6 +995,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
             }
             if (!ready && !wait(b)) break;
             ready = true;
+            __syncwarp();
             uint32_t v[16];
             ptx::tmem_ld16(d + c0, v);
             ptx::tmem_ld_wait();
@@ -1100,10 +1128,9 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
           if (ok) {
             uint8_t *d = sm.buf + pos.s * stage_bytes;
             ptx::mbar_arrive_expect_tx(&full[pos.s], loads.bytes() * (2 + a.planes));
-            pool_load_rows(loads, row4, d, tmV, &full[pos.s], u.fb * 128, 0);
-            pool_load_rows(loads, row4, d + 8192, tmV, &full[pos.s], u.fb * 128 + 64, 0);
-            for (int pl = 0; pl < a.planes; ++pl)
-              pool_load_rows(loads, row4, d + 16384 + pl * 8192, tmP, &full[pos.s], u.rb * 64, pl * static_cast<int>(p.M));
+            pool_load_rows(loads, row4, d, tmV, &full[pos.s], u.fb * 128);
+            pool_load_rows(loads, row4, d + 8192, tmV, &full[pos.s], u.fb * 128 + 64);
+            pool_load_planes(loads, row4, d + 16384, tmP, &full[pos.s], u.rb * 64, a.planes, static_cast<int>(p.M), 8192);
             ++issued;
           }
         }
@@ -1209,8 +1236,8 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
           for (int i = 0; i < 16; ++i)
             if (half * 32 + c + i >= u.live) x[i] = 0.0f;
         }
-        if (f >= cols) continue;
-        if (u.is_a) {
+        if (f >= cols) {
+        } else if (u.is_a) {
           O *out = static_cast<O *>(a.dA) + (static_cast<int64_t>(u.ad) * p.r + j0 + c) * p.K + f;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -1229,10 +1256,10 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
             }
           }
         }
+        __syncwarp();
       }
       if (sums) {
         ptx::tc_fence_before();
-        __syncwarp();
         if (lane == 0) ptx::mbar_arrive(half ? acc_empty1 : acc_empty0);
       }
     }
@@ -1295,10 +1322,9 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads)
           if (ok) {
             uint8_t *d = sm.buf + pos.s * stage_bytes;
             ptx::mbar_arrive_expect_tx(&full[pos.s], loads.bytes() * (2 + a.planes));
-            pool_load_rows(loads, row4, d, tmV, &full[pos.s], fb * 128, 0);
-            pool_load_rows(loads, row4, d + 8192, tmV, &full[pos.s], fb * 128 + 64, 0);
-            for (int pl = 0; pl < a.planes; ++pl)
-              pool_load_rows(loads, row4, d + 16384 + pl * 8192, tmP, &full[pos.s], rb * 64, pl * static_cast<int>(p.M));
+            pool_load_rows(loads, row4, d, tmV, &full[pos.s], fb * 128);
+            pool_load_rows(loads, row4, d + 8192, tmV, &full[pos.s], fb * 128 + 64);
+            pool_load_planes(loads, row4, d + 16384, tmP, &full[pos.s], rb * 64, a.planes, static_cast<int>(p.M), 8192);
             ++issued;
           }
         }

@@ -958,23 +958,31 @@ PoolArgs pool_args(const qlora_adapter_pool *p, const int32_t *order, const int3
 
 // A pool's matrices [n][rows][inner] bf16, box 64 x box_rows of one of them: what lies past its rows or columns reads
 // as zeros and not as the next one's.
-bool tmap_pool(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, int n, uint32_t box_rows) {
+bool tmap_pool(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, int n, uint32_t box_rows,
+               uint32_t box_n = 1) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner) * 2, static_cast<cuuint64_t>(inner) * rows * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t box[3] = {64, box_rows, box_n};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Token rows [rows, inner] bf16 with row stride ld: one row a box to gather, and 16 or 32 for runs of rows.
-bool tmap_tokens(PoolMaps *m, const void *ptr, int64_t inner, int64_t rows, int64_t ld) {
+// Token rows [M, inner] bf16 with row stride ld: one row a box to gather, and 16, 32 or 64 for runs of rows.
+bool tmap_rows(PoolMaps *m, const void *ptr, int64_t inner, int64_t rows, int64_t ld) {
   const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return make_tmap(&m->row, ptr, dt, 2, inner, rows, ld, 64, 1, true) && make_tmap(&m->row16, ptr, dt, 2, inner, rows, ld, 64, 16, true) &&
          make_tmap(&m->row32, ptr, dt, 2, inner, rows, ld, 64, 32, true);
+}
+bool tmap_tokens(PoolMaps *m, const void *ptr, int64_t inner, int64_t M, int64_t ld) {
+  return tmap_rows(m, ptr, inner, M, ld) && make_tmap(&m->row64, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, M, ld, 64, 64, true);
+}
+// An intermediate's planes [3, M, r], of which `planes` are used: as rows, and 64 rows of each plane in one box.
+bool tmap_planes(PoolMaps *m, const void *ptr, int r, int64_t M, int planes) {
+  return tmap_rows(m, ptr, r, kPoolPlanes * M, r) && tmap_pool(&m->row64, ptr, r, M, kPoolPlanes, 64, planes);
 }
 
 // A pool kernel on one device: its attributes are set at the first call, and how many clusters of a size fit the GPU at once
@@ -1156,7 +1164,7 @@ qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const v
   CUtensorMap tmW;
   PoolMaps tmP;
   if (!(W_MN ? tmap_pool(&tmW, W, a.cols, p.r, p.n, 64) : tmap_pool(&tmW, W, p.r, a.cols, p.n, 128)) ||
-      !tmap_tokens(&tmP, P, p.r, kPoolPlanes * p.M, p.r))
+      !tmap_planes(&tmP, P, p.r, p.M, a.planes))
     return QLORA_ERR_CUDA;
   const int64_t units = (p.M / a.l.tn + std::min<int64_t>(p.n, p.M)) * ((a.cols + 127) / 128);
   auto launch = [&](auto kernel, PoolKernelState &ks) -> qlora_status {
@@ -1179,15 +1187,15 @@ template <typename O>
 qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const void *X, int64_t ldx,
                                const __nv_bfloat16 *T, const void *dY, int64_t lddy, void *dA, void *dB, int dev,
                                int sms, cudaStream_t st) {
-  PoolMaps tmX{}, tmU{}, tmDY{}, tmT{};
-  if (p.M > 0 && (!tmap_tokens(&tmX, X, p.K, p.M, ldx) || !tmap_tokens(&tmU, U, p.r, kPoolPlanes * p.M, p.r) ||
-                  !tmap_tokens(&tmDY, dY, p.N, p.M, lddy) || !tmap_tokens(&tmT, T, p.r, kPoolPlanes * p.M, p.r)))
-    return QLORA_ERR_CUDA;
   PoolGradArgs a;
   a.p = p;
   a.dA = dA;
   a.dB = dB;
   a.planes = sizeof(O) == 4 ? kPoolPlanes : kPoolPlanes - 1;
+  PoolMaps tmX{}, tmU{}, tmDY{}, tmT{};
+  if (p.M > 0 && (!tmap_tokens(&tmX, X, p.K, p.M, ldx) || !tmap_planes(&tmU, U, p.r, p.M, a.planes) ||
+                  !tmap_tokens(&tmDY, dY, p.N, p.M, lddy) || !tmap_planes(&tmT, T, p.r, p.M, a.planes)))
+    return QLORA_ERR_CUDA;
   const int64_t units = static_cast<int64_t>(p.n) * ((p.r + 63) / 64) * ((p.K + 127) / 128 + (p.N + 127) / 128);
   if (2 * units >= sms || p.M < 256) {
     a.stages = pool_grad_stages(a.planes, p.n);
