@@ -160,22 +160,24 @@ __device__ __forceinline__ int2 pool_group(const PoolArgs &p, int a) {
   return make_int2(lo, min(max(p.offsets[a + 1], lo), m));
 }
 
-// Token at place i (below M); -1 if it is out of range.
-__device__ __forceinline__ int pool_token(const PoolArgs &p, int i) {
-  const int t = __ldg(p.order + i);
+// An entry of the order; -1 if it is out of range.
+__device__ __forceinline__ int pool_checked(const PoolArgs &p, int t) {
   if (t >= 0 && t < p.M) return t;
   raise_status(p.status, QLORA_ERR_INVALID_ARGUMENT);
   return -1;
 }
+// Token at place i (below M).
+__device__ __forceinline__ int pool_token(const PoolArgs &p, int i) { return pool_checked(p, __ldg(p.order + i)); }
 
-// The same for a load of four rows, which needs some row in range: row 0 then, whose result is not written.
-__device__ __forceinline__ int4 pool_rows(const PoolArgs &p, int i, int last) {
-  int4 y;
-  y.x = max(pool_token(p, min(i, last)), 0);
-  y.y = max(pool_token(p, min(i + 1, last)), 0);
-  y.z = max(pool_token(p, min(i + 2, last)), 0);
-  y.w = max(pool_token(p, min(i + 3, last)), 0);
-  return y;
+// Four entries for a load of rows, as they are, and checked: the load needs some row in range, row 0 then, whose result is
+// not written.  Apart, so that a step's entries can be on their way during the step before.
+__device__ __forceinline__ int4 pool_entries(const PoolArgs &p, int i, int last) {
+  return make_int4(__ldg(p.order + min(i, last)), __ldg(p.order + min(i + 1, last)), __ldg(p.order + min(i + 2, last)),
+                   __ldg(p.order + min(i + 3, last)));
+}
+__device__ __forceinline__ int4 pool_rows(const PoolArgs &p, const int4 &e) {
+  return make_int4(max(pool_checked(p, e.x), 0), max(pool_checked(p, e.y), 0), max(pool_checked(p, e.z), 0),
+                   max(pool_checked(p, e.w), 0));
 }
 
 // Loads of token rows into a stage: 64, 32 or 16 consecutive rows of memory come with one tiled load, other rows four to a
@@ -420,7 +422,7 @@ __device__ __forceinline__ void pool_load_planes(const PoolRowLoads &l, const in
 }
 // The same of a tile of up to 64 tokens.
 __device__ __forceinline__ PoolRowLoads pool_tile_loads(const PoolArgs &p, const PoolTile &t, int lane, int4 *row4) {
-  const int4 rows = t.cnt > 0 ? pool_rows(p, t.lo + 4 * (lane & 15), t.lo + t.cnt - 1) : make_int4(0, 0, 0, 0);
+  const int4 rows = t.cnt > 0 ? pool_rows(p, pool_entries(p, t.lo + 4 * (lane & 15), t.lo + t.cnt - 1)) : make_int4(0, 0, 0, 0);
   return pool_row_loads(rows, lane, t.cnt, (t.cnt + 3) / 4, true, row4);
 }
 
@@ -1111,31 +1113,33 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
   const int64_t rounds = (units + G - 1) / G;
   if (warp == 0) {
     // ------------------------------------------------------------ loads
+    int planes = a.planes, m = static_cast<int>(p.M); uint32_t sbytes = stage_bytes, nst = stages;
+    asm volatile("" : "+r"(planes), "+r"(m), "+r"(sbytes), "+r"(nst));
     for (int64_t round = 0; round < rounds && ok; ++round) {
       PoolGradUnit u;
       if (!unit_of(round, u) || u.live <= 0 || u.cnt == 0) continue;
       const PoolMaps *tmV = u.is_a ? &tmX : &tmDY, *tmP = u.is_a ? &tmU : &tmT;
       const int g = lane & 15, last = u.lo + u.cnt - 1;
-      int4 rows = pool_rows(p, u.lo + 4 * g, last);
+      int4 entries = pool_entries(p, u.lo + 4 * g, last);
       for (int t0 = 0; t0 < u.cnt && ok; t0 += 64) {
         const int left = u.cnt - t0, groups = (min(64, left) + 15) / 16 * 4;  // whole steps of 16 tokens
         // a run that is not whole is gathered: rows of other adapters' tokens must not meet the padding
-        const PoolRowLoads loads = pool_row_loads(rows, lane, left, groups, false, row4);
-        if (t0 + 64 < u.cnt) rows = pool_rows(p, u.lo + t0 + 64 + 4 * g, last);
+        const PoolRowLoads loads = pool_row_loads(pool_rows(p, entries), lane, left, groups, false, row4);
+        if (t0 + 64 < u.cnt) entries = pool_entries(p, u.lo + t0 + 64 + 4 * g, last);
         __syncwarp();
         if (ptx::elect_one()) {
           ok = ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag);
           if (ok) {
-            uint8_t *d = sm.buf + pos.s * stage_bytes;
-            ptx::mbar_arrive_expect_tx(&full[pos.s], loads.bytes() * (2 + a.planes));
+            uint8_t *d = sm.buf + pos.s * sbytes;
+            ptx::mbar_arrive_expect_tx(&full[pos.s], loads.bytes() * (2 + planes));
             pool_load_rows(loads, row4, d, tmV, &full[pos.s], u.fb * 128);
             pool_load_rows(loads, row4, d + 8192, tmV, &full[pos.s], u.fb * 128 + 64);
-            pool_load_planes(loads, row4, d + 16384, tmP, &full[pos.s], u.rb * 64, a.planes, static_cast<int>(p.M), 8192);
+            pool_load_planes(loads, row4, d + 16384, tmP, &full[pos.s], u.rb * 64, planes, m, 8192);
             ++issued;
           }
         }
         ok = __all_sync(0xffffffffu, ok);
-        pos.next(stages);
+        pos.next(nst);
       }
     }
     if (!ok && lane == 0) pool_fail(sm, p.status);
@@ -1312,11 +1316,13 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads)
     if (warp == 0) {
       const PoolMaps *tmV = is_a ? &tmX : &tmDY, *tmP = is_a ? &tmU : &tmT;
       const int g = lane & 15;
+      int4 entries = make_int4(0, 0, 0, 0);
+      if (sb < se) entries = pool_entries(p, grp.x + sb * 64 + 4 * g, grp.y - 1);
       for (int st = sb; st < se && ok; ++st) {
         const int left = cnt - st * 64, groups = (min(64, left) + 15) / 16 * 4;  // whole steps of 16 tokens
         // a run that is not whole is gathered: rows of other adapters' tokens must not meet the padding
-        const PoolRowLoads loads =
-            pool_row_loads(pool_rows(p, grp.x + st * 64 + 4 * g, grp.y - 1), lane, left, groups, false, row4);
+        const PoolRowLoads loads = pool_row_loads(pool_rows(p, entries), lane, left, groups, false, row4);
+        if (st + 1 < se) entries = pool_entries(p, grp.x + (st + 1) * 64 + 4 * g, grp.y - 1);
         if (ptx::elect_one()) {
           ok = ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag);
           if (ok) {
