@@ -181,10 +181,10 @@ __device__ __forceinline__ int4 pool_rows(const PoolArgs &p, const int4 &e) {
 }
 
 // Loads of token rows into a stage: 64, 32 or 16 consecutive rows of memory come with one tiled load, other rows four to a
-// gather.  Each load costs the loading thread about 130 cycles, whatever its rows, which with gathers alone bounds a step
-// of 64 tokens at many times its time (reading 67 MB by them took 46 us), and with two tiled loads of 32 rows still at
-// twice it (2048 tokens' gradients 40 us, and 3x us with one); requests of a packed batch are runs of rows.  Of the planes,
-// 64 rows of all that are used come with one load.
+// gather, and 64 rows of all planes that are used come with one load too.  Requests of a packed batch are runs of rows, and
+// a load costs the loading thread 100 to 160 cycles, whatever its rows: gathers alone bound a step of 64 tokens at many
+// times its time (reading 67 MB by them took 46 us), and with runs of 32 and planes one by one the backward over 2048
+// tokens took 87 us, with these 78.
 struct PoolMaps {
   CUtensorMap row, row16, row32, row64;
 };
@@ -531,7 +531,8 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
         const int w_loads = mn ? (p.r + 63) / 64 : nrb;
         const uint32_t bytes = w_loads * (mn ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u) + rows.bytes();
         for (int ks = kb; ks < ke; ++ks) {
-          if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
+          // (a wait takes 140 cycles even where it is over: none for the first filling of the ring)
+          if (issued >= stages && !ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
           uint8_t *st = sm.buf + pos.s * l.stage;
           uint64_t *bar = &full[pos.s];
           ptx::mbar_arrive_expect_tx(bar, bytes);
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
               pool_load_planes(rows, row4, sm.buf + l.planes_at + c * a.planes * l.plane, &tmP, p_full, c * 64, a.planes,
                                static_cast<int>(p.M), l.plane);
           }
-          if (!ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
+          if (issued >= stages && !ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
           const int f = (q + b * g) * 128, x = ch * 64;
           uint8_t *st = sm.buf + pos.s * kPoolUpStage;
           ptx::mbar_arrive_expect_tx(&full[pos.s], kPoolUpStage);
@@ -1113,7 +1114,9 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
   const int64_t rounds = (units + G - 1) / G;
   if (warp == 0) {
     // ------------------------------------------------------------ loads
-    int planes = a.planes, m = static_cast<int>(p.M); uint32_t sbytes = stage_bytes, nst = stages;
+    // in registers: read again as parameters at each use, they took part of this thread's time, which bounds a step
+    int planes = a.planes, m = static_cast<int>(p.M);
+    uint32_t sbytes = stage_bytes, nst = stages;
     asm volatile("" : "+r"(planes), "+r"(m), "+r"(sbytes), "+r"(nst));
     for (int64_t round = 0; round < rounds && ok; ++round) {
       PoolGradUnit u;

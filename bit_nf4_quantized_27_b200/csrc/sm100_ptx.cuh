@@ -122,10 +122,6 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t *bar, uint32_t parity, c
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-// The same for the shared memory of the cluster's other CTAs too.
-__device__ __forceinline__ void fence_proxy_async_cluster() {
-  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
-}
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -406,9 +402,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
                : "r"(cluster_addr)
                : "memory");
   return v;
-}
-__device__ __forceinline__ void st_cluster_u32x2(uint32_t cluster_addr, const uint2 &v) {
-  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_nctarank() {
   uint32_t r;
