@@ -306,11 +306,12 @@ __device__ __forceinline__ void adamw_block(const qlora_tensor &t, const AdamWMu
   }
   mm = warp_max_abs(mm);
   vm = warp_max_abs(vm);
-  // Reciprocals for the codes (lanes 0 and 1) and scales (lanes 2 and 3) in one division.  A maximum below 2^-100 is a block
-  // of zeros: its reciprocal would overflow.
+  // Factors for the codes (lanes 0 and 1), the largest code times the maximum's reciprocal, and scales (lanes 2 and 3) in
+  // one division.  A maximum below 2^-100 is a block of zeros: its reciprocal would overflow.
   const bool of_v = lane & 1, scale = lane & 2;
   const float top = of_v ? vm : mm, most = of_v ? 57344.0f : 448.0f;
-  const float quot = top < 0x1p-100f ? 0.0f : __fdiv_rn(scale ? top : most, scale ? most : top);
+  float quot = top < 0x1p-100f ? 0.0f : __fdiv_rn(scale ? top : 1.0f, scale ? most : top);
+  if (!scale) quot = __fmul_rn(most, quot);
   if (lane == 2) t.exp_avg_scale[blk] = quot;
   if (lane == 3) t.exp_avg_sq_scale[blk] = quot;
   const float im = __shfl_sync(0xffffffffu, quot, 0), iv = __shfl_sync(0xffffffffu, quot, 1);

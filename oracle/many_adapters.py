@@ -131,9 +131,9 @@ def adamw8(p, g, m, v, ms, vs, step, tensor, seed, lr, beta1, beta2, eps, weight
         top_m, top_v = f(np.abs(mm[at]).max()), f(vv[at].max())
         if top_m >= 2.0 ** -100:
             nms[b] = top_m / f(448)
-            nm[at] = np.copysign(stochastic_round(np.abs(mm[at]) * (f(448) / top_m), um[at], E4M3), mm[at])
+            nm[at] = np.copysign(stochastic_round(np.abs(mm[at]) * (f(448) * (f(1) / top_m)), um[at], E4M3), mm[at])
         if top_v >= 2.0 ** -100:
             nvs[b] = top_v / f(57344)
-            q = stochastic_round(vv[at] * (f(57344) / top_v), uv[at], E5M2)
+            q = stochastic_round(vv[at] * (f(57344) * (f(1) / top_v)), uv[at], E5M2)
             nv[at] = np.where(vv[at] > 0, np.maximum(q, 2.0 ** -16), q)
     return p.astype(f), nm, nv, nms, nvs
