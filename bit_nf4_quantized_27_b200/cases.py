@@ -15,6 +15,9 @@ CASE is one of:
   quant_4096 / dequant_4096     the same for a 4096x4096 weight
   merge_8192    merged export of an 8192x8192 NF4 weight with an r = 64 adapter
   adamw_65b     AdamW step over the adapters of the 65B-shaped block (flat fp32)
+  pool_packed   forward of 16 r=64 adapters on 4096x4096, 2048 packed tokens of 32 requests
+  pool_train    backward of four r=64 adapters on 11008x4096, 2048 tokens, T not kept
+  adamw_list8   AdamW step with 8-bit states over the r=16 adapters of 32 Llama-7B blocks
 Inputs are drawn on the device from fixed seeds; every run exits 0 on success.
 """
 
@@ -103,6 +106,32 @@ def main(argv=None):
         p16 = torch.empty(n, dtype=torch.bfloat16, device="cuda")
         for i in range(args.reps):
             bd.adamw_step(p, g, m, v, i + 1, 1e-4, weight_decay=0.01, p_bf16=p16)
+        st = 0
+    elif c in ("pool_packed", "pool_train"):
+        s, n, requests = (16, 4096, 32) if c == "pool_packed" else (4, 11008, 4)
+        _, x, _, _, dy = _layer(n, 4096, 2048)
+        ab = [_layer(n, 4096, 1, seed=100 + i)[2:4] for i in range(s)]
+        pool = bd.AdapterPool(torch.stack([a for a, _ in ab]), torch.stack([b for _, b in ab]), torch.ones(s, device="cuda"))
+        per = 2048 // requests
+        groups = bd.adapter_groups((torch.arange(2048, device="cuda") // per % s).to(torch.int32), s)
+        ws = bd.new_workspace(bd.workspace_bytes_adapters(2048, n, 4096, 64, True))
+        y = torch.zeros(2048, n, dtype=torch.bfloat16, device="cuda")
+        dx = torch.zeros(2048, 4096, device="cuda")
+        for _ in range(args.reps):
+            if c == "pool_packed":
+                bd.adapters_fwd(pool, groups, x, y, ws=ws)
+            else:
+                bd.adapters_bwd(pool, groups, x, dy, dX=dx, ws=ws)
+        st = bd.read_status(ws)
+    elif c == "adamw_list8":
+        sizes = [z for n, k in (((4096, 4096),) * 4 + ((11008, 4096),) * 2 + ((4096, 11008),)) * 32 for z in (16 * k, n * 16)]
+        rand = lambda: [torch.randn(z, device="cuda") * 0.01 for z in sizes]  # noqa: E731
+        codes = lambda: [torch.zeros(z, dtype=torch.uint8, device="cuda") for z in sizes]  # noqa: E731
+        scales = lambda: [torch.zeros((z + 255) // 256, device="cuda") for z in sizes]  # noqa: E731
+        tl = bd.TensorList([g.to(torch.bfloat16) for g in rand()], params=rand(), exp_avg=codes(), exp_avg_sq=codes(),
+                           exp_avg_scale=scales(), exp_avg_sq_scale=scales())
+        for i in range(args.reps):
+            bd.adamw_multi(tl, i + 1, 1e-4, weight_decay=0.01, seed=i)
         st = 0
     else:
         raise SystemExit(f"unknown case {c}")

@@ -342,7 +342,7 @@ QLORA_API size_t qlora_workspace_bytes_adapters(int64_t M, int64_t N, int64_t K,
 
 /* Y[t] += s_a (X[t] A_a^T) B_a^T for every token of order[0 .. offsets[n]); the
  * other rows of Y are not touched.  The sum is formed in float32 and rounded once.
- *   order, offsets  as qlora_adapter_groups writes them
+ *   order, offsets  as qlora_adapter_groups writes them: a token at most once
  *   X   bf16 [M, K], row stride ldx (elements, a multiple of 8, >= K), 16-byte aligned
  *   Y   [M, N] of y_dtype, row stride ldy >= N, element aligned; read and written
  *   T_save  nullable bf16 [3, M, r], 16-byte aligned: receives T[t] = X[t] A_a^T for
@@ -363,7 +363,8 @@ QLORA_API qlora_status qlora_adapters_fwd(const qlora_adapter_pool *pool, const 
  *   dA, dB   nullable, both or neither: [n, r, K] and [n, N, r] of grad_dtype,
  *            16-byte aligned, overwritten; zeros for an adapter without tokens and
  *            past an adapter's rank
- *   T_saved  nullable: T_save of the forward; NULL recomputes it
+ *   T_saved  nullable: T_save of the forward; NULL recomputes it (the same sum, whose
+ *            parts may be cut elsewhere along K)
  * dY bf16 [M, N], row stride lddy (a multiple of 8, >= N), 16-byte aligned.  Sums
  * run in a fixed order: the same inputs give the same bits. */
 QLORA_API qlora_status qlora_adapters_bwd(const qlora_adapter_pool *pool, const int32_t *order,
@@ -448,8 +449,10 @@ QLORA_API qlora_status qlora_grad_norm(const qlora_tensor_list *list, float max_
  *   seed  8-bit states are rounded stochastically: the random bits are a hash of
  *       (seed, place in the list, element), so a step is reproducible; give each
  *       step another seed
- * The parameters see the new states before they are rounded to 8 bits.  A variance
- * that is not zero is never rounded to zero. */
+ * The parameters see the new states before they are rounded to 8 bits, and with
+ * those take the update's root and quotient to a few 2^-23 of the update (an eps
+ * below 2^-126 counts as 2^-126).  A variance that is not zero is never rounded to
+ * zero, unless all of its block are below 2^-100: such a block is stored as zeros. */
 QLORA_API qlora_status qlora_adamw_multi(const qlora_tensor_list *list, const qlora_adamw_hparams *hp, int64_t step,
                                          const float *norm_and_clip, uint32_t seed, qlora_stream_t stream);
 
