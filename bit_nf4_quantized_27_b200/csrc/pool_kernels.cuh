@@ -239,12 +239,13 @@ __device__ __forceinline__ PoolSmem pool_smem(uint8_t *raw, uint32_t bytes) {
 }
 __host__ __device__ constexpr uint32_t pool_smem_bytes(uint32_t bytes) { return 1024 + bytes + kPoolTailBytes; }
 
-// Set-up of the kernels: barriers (one arrival each; four, one of each warp of a set, from place `four` on), TMEM, then
+// Set-up of the kernels: barriers (one arrival each; two, of two loading warps, below place `two`; four, one of each warp
+// of a set, from place `four` on), TMEM, then
 // the wait for the kernel ahead.  The next kernel may start only after that wait: one that reads early, or that waits for
 // this kernel alone, then finds everything before this kernel complete too.
-__device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_cols, uint32_t four) {
+__device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_cols, uint32_t four, uint32_t two = 0) {
   if (threadIdx.x == 0) {
-    for (uint32_t i = 0; i < kPoolBars; ++i) ptx::mbar_init(&s.bars[i], i < four ? 1 : 4);
+    for (uint32_t i = 0; i < kPoolBars; ++i) ptx::mbar_init(&s.bars[i], i < two ? 2 : i < four ? 1 : 4);
     *s.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -441,7 +442,8 @@ __host__ __device__ constexpr uint32_t pool_desc_16(bool mn) { return mn ? 128u 
 // of the tokens over the g CTAs, in CTA order, through distributed shared memory, and writes the planes: no partial
 // planes in HBM, no further launch, and the same bits every time.  g, a divisor of the cluster, follows on the device
 // from the number of tiles.
-//   warp 0  loads; warp 1  products; warps 2..9  accumulators -> shared memory; all  the sums
+//   warp 0  loads V; warp 2 W (one thread that loaded both bounded the kernel: 480 cycles a step); warp 1  products;
+//   warps 2..9  accumulators -> shared memory; all  the sums
 // A launch has one or two sums to do (a backward whose T was not kept does U and T, which saves a launch that would wait
 // for the other's last tiles); each has clusters of its own.
 // mn false: W is [n][r][len], K-major (T: A); true: [n][len][r], MN-major (U: B).
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
   float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
   if (tid < 5) ptx::prefetch_tmap(tid == 0 ? &job.W : tid == 1 ? &job.V.row : tid == 2 ? &job.V.row16 : tid == 3 ? &job.V.row32 : &job.V.row64);
-  const uint32_t tmem = pool_setup(sm, kPoolDownTmem, kPoolBars);
+  const uint32_t tmem = pool_setup(sm, kPoolDownTmem, kPoolBars, kPoolMostStages);
   const PoolWalk walk = pool_walk(p, tn, warp_sum);
   // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
   int g = cluster;
@@ -527,18 +529,12 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
     if (warp == 0) {
       const PoolRowLoads rows = pool_tile_loads(p, tile_s, lane, row4);
       if (ok && ptx::elect_one()) {
-        // W's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
-        const int w_loads = mn ? (p.r + 63) / 64 : nrb;
-        const uint32_t bytes = w_loads * (mn ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u) + rows.bytes();
+        const uint32_t bytes = rows.bytes();
         for (int ks = kb; ks < ke; ++ks) {
           // (a wait takes 140 cycles even where it is over: none for the first filling of the ring)
           if (issued >= stages && !ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
-          uint8_t *st = sm.buf + pos.s * l.stage;
-          uint64_t *bar = &full[pos.s];
-          ptx::mbar_arrive_expect_tx(bar, bytes);
-          for (int i = 0; i < w_loads; ++i)
-            ptx::tma_load_3d(st + v_bytes + i * (mn ? 8192 : 16384), &job.W, bar, mn ? i * 64 : ks * 64, mn ? ks * 64 : i * 128, ad);
-          pool_load_rows(rows, row4, st, &job.V, bar, ks * 64);
+          ptx::mbar_arrive_expect_tx(&full[pos.s], bytes);
+          pool_load_rows(rows, row4, sm.buf + pos.s * l.stage, &job.V, &full[pos.s], ks * 64);
           ++issued;
           pos.next(stages);
         }
@@ -571,6 +567,25 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
       __syncwarp();
     } else {
       const int quad = warp & 3, set = (warp - 2) >> 2;
+      if (warp == 2) {
+        if (ok && ptx::elect_one()) {
+          // W's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
+          const int w_loads = mn ? (p.r + 63) / 64 : nrb;
+          const uint32_t bytes = w_loads * (mn ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u);
+          for (int ks = kb; ks < ke; ++ks) {
+            if (issued >= stages && !ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
+            uint8_t *st = sm.buf + pos.s * l.stage + v_bytes;
+            uint64_t *bar = &full[pos.s];
+            ptx::mbar_arrive_expect_tx(bar, bytes);
+            for (int i = 0; i < w_loads; ++i)
+              ptx::tma_load_3d(st + i * (mn ? 8192 : 16384), &job.W, bar, mn ? i * 64 : ks * 64, mn ? ks * 64 : i * 128, ad);
+            ++issued;
+            pos.next(stages);
+          }
+          if (!ok) pool_fail(sm, p.status);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
       if (ke > kb && ok) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(sum_full, sum_phase, sm.abort_flag));
         sum_phase ^= 1;
@@ -637,7 +652,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
     }
     pool_cluster_sync();  // the partial sums, and the tile, are done with
   }
-  if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the thread that loads
+  if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the threads that load
   pool_teardown(tmem, kPoolDownTmem);
 }
 
