@@ -592,11 +592,14 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
         if (!ok && lane == 0) pool_fail(sm, p.status);
       }
       ptx::tc_fence_after();
+      int rpad = l.rpad;
+      asm volatile("" : "+r"(rpad));  // in a register: read again as a parameter, each store took 60 ns
       const int nacc = ok ? min(4, ke - kb) : 0, c_end = min(cnt, (set + 1) * (tn / 2));
       for (int rb = 0; rb < nrb; ++rb) {
         if (rb * 128 + quad * 32 >= p.r) break;
         for (int c0 = set * (tn / 2); c0 < c_end; c0 += 16) {
           const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + rb * tn + c0;
+          float *to = exch + c0 * rpad + rb * 128 + quad * 32 + lane;
           float x[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[j] = 0.0f;
@@ -611,8 +614,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
             for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]) + (i + 1 < nacc ? __uint_as_float(w[j]) : 0.0f);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c0 + j < c_end) exch[(c0 + j) * l.rpad + rb * 128 + quad * 32 + lane] = x[j];
+          for (int j = 0; j < 16; ++j) to[j * rpad] = x[j];  // up to 15 that are not tokens: not read
         }
       }
       ptx::tc_fence_before();
