@@ -229,8 +229,8 @@ struct PoolSmem {
 };
 __device__ __forceinline__ PoolSmem pool_smem(uint8_t *raw, uint32_t bytes) {
   PoolSmem s;
-  // an offset, not a rounded pointer: the compiler has to see that this is shared memory (through generic addresses the
-  // partial sums' 16 stores a thread took 1.2 us, and 0.2 so)
+  // an offset, not a rounded pointer: the compiler has to see that this is shared memory (through generic addresses
+  // 2039 packed tokens took 32.6 us instead of 30.0)
   s.buf = raw + ((1024u - (ptx::smem_addr(raw) & 1023u)) & 1023u);
   s.bars = reinterpret_cast<uint64_t *>(s.buf + bytes);
   s.tmem_slot = reinterpret_cast<uint32_t *>(s.bars + kPoolBars);

@@ -220,6 +220,49 @@ def test_column_slices_of_wider_tensors(dt):
     assert (wide["dX"][:, :1] == 3).all() and (wide["dX"][:, 1 + k:] == 3).all()
 
 
+def test_rows_far_apart():
+    """Row strides of 2^30 elements: offsets past 32 bits in X, dY, Y and dX."""
+    m, n_out, k, r, n, ld = 3, 72, 136, 16, 2, 1 << 30
+    idx, A, B, scales, X, dY = _setup(m, n_out, k, r, n, 85, none=0.0)
+    pool, groups = _pool(A, B, scales, None), bd.adapter_groups(idx.cuda(), n)
+    Y, dX = torch.randn(m, n_out, device="cuda"), torch.randn(m, k, device="cuda")
+    far = lambda t: torch.empty_strided(t.shape, (ld, 1), dtype=t.dtype, device="cuda").copy_(t)  # noqa: E731
+    fX, fdY, fY, fdX = far(X), far(dY), far(Y), far(dX)
+    bd.adapters_fwd(pool, groups, X.cuda(), Y)
+    g0 = bd.adapters_bwd(pool, groups, X.cuda(), dY.cuda(), dX=dX)
+    bd.adapters_fwd(pool, groups, fX, fY)
+    g1 = bd.adapters_bwd(pool, groups, fX, fdY, dX=fdX)
+    assert torch.equal(fY, Y) and torch.equal(fdX, dX) and all(torch.equal(a, b) for a, b in zip(g0, g1))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace and outputs, give what they give alone."""
+    sets = []
+    for i, (m, n_out, k, r, n) in enumerate([(700, 520, 1096, 64, 5), (333, 1160, 328, 24, 9)]):
+        idx, A, B, scales, X, dY = _setup(m, n_out, k, r, n, 86 + i)
+        ws = bd.new_workspace(bd.workspace_bytes_adapters(m, n_out, k, r, True))
+        sets.append((_pool(A, B, scales, None), idx.cuda(), n, X.cuda(), dY.cuda(), ws))
+
+    def step(pool, idx, n, X, dY, ws):
+        groups = bd.adapter_groups(idx, n, ws=ws)
+        Y = torch.zeros(X.shape[0], dY.shape[1], device="cuda")
+        dX = torch.zeros(X.shape, device="cuda")
+        bd.adapters_fwd(pool, groups, X, Y, ws=ws)
+        return Y, dX, *bd.adapters_bwd(pool, groups, X, dY, dX=dX, ws=ws)
+
+    alone = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(step(*s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(alone, got) for a, b in zip(x, y))
+    assert all(bd.read_status(s[-1]) == 0 for s in sets)
+
+
 def test_parts_of_the_backward_alone():
     idx, A, B, scales, X, dY = _setup(90, 200, 136, 32, 4, 90)
     pool, groups = _pool(A, B, scales, None), bd.adapter_groups(idx.cuda(), 4)
