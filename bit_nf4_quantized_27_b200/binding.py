@@ -532,6 +532,7 @@ def linear_fwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, y_dtype=torch.bf
     Y = out if out is not None else torch.empty(M, q.rows, dtype=y_dtype, device=X.device)
     assert Y.is_contiguous() and tuple(Y.shape) == (M, q.rows)
     T = t_out if t_out is not None else (torch.empty(3, M, pool.r, dtype=torch.bfloat16, device=X.device) if save_t else None)
+    assert T is None or (T.dtype == torch.bfloat16 and T.is_contiguous() and T.numel() == 3 * M * pool.r)
     order, offsets = _group_ptrs(groups, pool, M)
     _here(X, Y, T, ws, pool.A, q.codes, *groups)
     if ws is None:
@@ -549,6 +550,7 @@ def linear_bwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, dY, T=None, dx_d
     M = X.shape[0]
     assert X.dtype == torch.bfloat16 and X.is_contiguous() and X.shape[1] == q.cols == pool.cols and pool.rows == q.rows
     assert dY.dtype == torch.bfloat16 and dY.is_contiguous() and tuple(dY.shape) == (M, q.rows)
+    assert T is None or (T.dtype == torch.bfloat16 and T.is_contiguous() and T.numel() == 3 * M * pool.r)
     dX = outs[0] if outs is not None else torch.empty(M, q.cols, dtype=dx_dtype, device=X.device)
     assert dX.is_contiguous() and tuple(dX.shape) == (M, q.cols)
     dA, dB = _pool_grads(pool, grad_dtype, None if outs is None else outs[1:], X.device)

@@ -361,3 +361,20 @@ def test_float8_grids_are_the_formats():
     e4 = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
     e5 = torch.arange(124, dtype=torch.uint8).view(torch.float8_e5m2).float().numpy()
     assert np.array_equal(MA.E4M3, e4) and np.array_equal(MA.E5M2, e5)
+
+
+def test_pool_layer_refuses_planes_of_another_size():
+    """The planes of T hold 3 M r elements; smaller ones are refused before any launch."""
+    import types
+
+    import torch
+
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    pool = bd.AdapterPool(z(2, 8, 64), z(2, 16, 8), z(2, dt=torch.float32))
+    q = types.SimpleNamespace(rows=16, cols=64, codes=z(16, 32, dt=torch.uint8))
+    groups = (z(5, dt=torch.int32), z(3, dt=torch.int32))
+    for planes in (z(2, 5, 8), z(3, 5, 8, dt=torch.float32), z(3, 8, 5).transpose(1, 2)):
+        with pytest.raises(AssertionError):
+            bd.linear_fwd_pool(q, pool, groups, z(5, 64), t_out=planes)
+        with pytest.raises(AssertionError):
+            bd.linear_bwd_pool(q, pool, groups, z(5, 64), z(5, 16), planes)
