@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const TensorTabl
 
 // ---------------------------------------------------------------------------
 // AdamW.  The arithmetic is adamw_one's, float32 operation by operation (with 8-bit
-// states but for the update's root and quotient).  8-bit states: a warp holds one block of 256 elements, eight consecutive ones per
-// lane; the block's new maxima come from warp shuffles, the codes from adding
+// states but for the update's root and quotient).  8-bit states: a warp holds one
+// block of 256 elements, eight consecutive ones per lane; the block's new maxima come from warp shuffles, the codes from adding
 // random bits below the last mantissa bit kept and cutting them off.  The result is
 // unbiased, which round-to-nearest is not where it matters: a step changes the
 // variance by 1 - beta2 of itself, far less than half an E5M2 step, and a rounded
