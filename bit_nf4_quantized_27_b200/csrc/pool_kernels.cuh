@@ -148,7 +148,7 @@ struct PoolArgs {
 // Rank of adapter a: a multiple of 8 in [0, r].
 __device__ __forceinline__ int pool_rank(const PoolArgs &p, int a) {
   if (!p.ranks) return p.r;
-  const int k = p.ranks[a], c = min(max(k, 0), p.r) & ~7;
+  const int k = __ldcg(p.ranks + a), c = min(max(k, 0), p.r) & ~7;
   if (c != k) raise_status(p.status, QLORA_ERR_INVALID_ARGUMENT);
   return c;
 }
@@ -156,8 +156,8 @@ __device__ __forceinline__ int pool_rank(const PoolArgs &p, int a) {
 // Places [lo, hi) of adapter a's tokens in order.
 __device__ __forceinline__ int2 pool_group(const PoolArgs &p, int a) {
   const int m = static_cast<int>(p.M);
-  const int lo = min(max(p.offsets[a], 0), m);
-  return make_int2(lo, min(max(p.offsets[a + 1], lo), m));
+  const int lo = min(max(__ldcg(p.offsets + a), 0), m);
+  return make_int2(lo, min(max(__ldcg(p.offsets + a + 1), lo), m));
 }
 
 // An entry of the order; -1 if it is out of range.
@@ -167,13 +167,13 @@ __device__ __forceinline__ int pool_checked(const PoolArgs &p, int t) {
   return -1;
 }
 // Token at place i (below M).
-__device__ __forceinline__ int pool_token(const PoolArgs &p, int i) { return pool_checked(p, __ldg(p.order + i)); }
+__device__ __forceinline__ int pool_token(const PoolArgs &p, int i) { return pool_checked(p, __ldcg(p.order + i)); }
 
 // Four entries for a load of rows, as they are, and checked: the load needs some row in range, row 0 then, whose result is
 // not written.  Apart, so that a step's entries can be on their way during the step before.
 __device__ __forceinline__ int4 pool_entries(const PoolArgs &p, int i, int last) {
-  return make_int4(__ldg(p.order + min(i, last)), __ldg(p.order + min(i + 1, last)), __ldg(p.order + min(i + 2, last)),
-                   __ldg(p.order + min(i + 3, last)));
+  return make_int4(__ldcg(p.order + min(i, last)), __ldcg(p.order + min(i + 1, last)), __ldcg(p.order + min(i + 2, last)),
+                   __ldcg(p.order + min(i + 3, last)));
 }
 __device__ __forceinline__ int4 pool_rows(const PoolArgs &p, const int4 &e) {
   return make_int4(max(pool_checked(p, e.x), 0), max(pool_checked(p, e.y), 0), max(pool_checked(p, e.z), 0),
@@ -240,9 +240,7 @@ __device__ __forceinline__ PoolSmem pool_smem(uint8_t *raw, uint32_t bytes) {
 __host__ __device__ constexpr uint32_t pool_smem_bytes(uint32_t bytes) { return 1024 + bytes + kPoolTailBytes; }
 
 // Set-up of the kernels: barriers (one arrival each; two, of two loading warps, below place `two`; four, one of each warp
-// of a set, from place `four` on), TMEM, then
-// the wait for the kernel ahead.  The next kernel may start only after that wait: one that reads early, or that waits for
-// this kernel alone, then finds everything before this kernel complete too.
+// of a set, from place `four` on) and TMEM.
 __device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_cols, uint32_t four, uint32_t two = 0) {
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < kPoolBars; ++i) ptx::mbar_init(&s.bars[i], i < two ? 2 : i < four ? 1 : 4);
@@ -256,9 +254,17 @@ __device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  return *s.tmem_slot;
+}
+
+// The wait for the kernel ahead.  The next kernel may start only after it: one that reads early, or that waits for this
+// kernel alone, then finds everything before this kernel complete too.  So up and grad, which follow a kernel with this
+// order in the same call, may read before their wait, through L2, all that the kernel ahead does not write (the groups,
+// the pool, Y), which hides their start behind that kernel's end; what it writes (the planes), and writes of their own,
+// come after.  Each CTA waits before it ends, whatever it had to do.
+__device__ __forceinline__ void pool_wait_ahead() {
   ptx::griddep_wait();
   ptx::griddep_launch();
-  return *s.tmem_slot;
 }
 
 __device__ __forceinline__ void pool_teardown(uint32_t tmem, uint32_t tmem_cols) {
@@ -311,7 +317,7 @@ __device__ __forceinline__ PoolWalk pool_walk(const PoolArgs &p, int tn, int *wa
   if (w.ad0 < p.n) {
     w.group0 = pool_group(p, w.ad0);
     w.rank0 = pool_rank(p, w.ad0);
-    w.scale0 = p.scales[w.ad0];
+    w.scale0 = __ldcg(p.scales + w.ad0);
     w.sum = (w.group0.y - w.group0.x + tn - 1) / tn;
     for (int i = 1; i < w.per && w.ad0 + i < p.n; ++i) {
       const int2 g = pool_group(p, w.ad0 + i);
@@ -353,7 +359,7 @@ __device__ __forceinline__ void pool_find(const PoolArgs &p, const PoolWalk &w, 
     out->lo = g.x + t * tn;
     out->cnt = min(tn, g.y - out->lo);
     out->rank = ad > w.ad0 ? pool_rank(p, ad) : w.rank0;
-    out->scale = ad > w.ad0 ? p.scales[ad] : w.scale0;
+    out->scale = ad > w.ad0 ? __ldcg(p.scales + ad) : w.scale0;
   }
 }
 
@@ -509,6 +515,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
   float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
   if (tid < 5) ptx::prefetch_tmap(tid == 0 ? &job.W : tid == 1 ? &job.V.row : tid == 2 ? &job.V.row16 : tid == 3 ? &job.V.row32 : &job.V.row64);
   const uint32_t tmem = pool_setup(sm, kPoolDownTmem, kPoolBars, kPoolMostStages);
+  pool_wait_ahead();
   const PoolWalk walk = pool_walk(p, tn, warp_sum);
   // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
   int g = cluster;
@@ -815,6 +822,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
         int b = 0, ch = 0;
         for (int i = 0; i < mine * nch; ++i) {
           if (i == min(static_cast<int>(stages), mine * nch) - 1) {
+            if (issued < stages) pool_wait_ahead();  // the first unit's
             ptx::mbar_arrive_expect_tx(p_full, nch * a.planes * rows.bytes());
             for (int c = 0; c < nch; ++c)
               pool_load_planes(rows, row4, sm.buf + l.planes_at + c * a.planes * l.plane, &tmP, p_full, c * 64, a.planes,
@@ -1038,6 +1046,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
     ring_drain(full, pos, stages, issued);
     ptx::mbar_wait(p_full, p_phase ^ 1, nullptr);
   }
+  pool_wait_ahead();
   pool_teardown(tmem, kPoolUpTmem);
 }
 
@@ -1105,6 +1114,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
     by_length[place] = i;
   }
   __syncthreads();
+  pool_wait_ahead();
   const int nrb = (p.r + 63) / 64;
   const int in_a = static_cast<int>((p.K + 127) / 128) * nrb, per_adapter = in_a + static_cast<int>((p.N + 127) / 128) * nrb;
   const int64_t units = static_cast<int64_t>(p.n) * per_adapter;
@@ -1314,6 +1324,7 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads)
   const uint32_t stage_bytes = 16384u + a.planes * 8192u, stages = min(kPoolGradSplitBytes / stage_bytes, kPoolMostStages);
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *acc_full = sm.bars + 2 * kPoolMostStages;
   const uint32_t tmem = pool_setup(sm, kPoolGradSplitTmem, kPoolBars);
+  pool_wait_ahead();
   const int nrb = (p.r + 63) / 64;
   const int in_a = static_cast<int>((p.K + 127) / 128) * nrb, per_adapter = in_a + static_cast<int>((p.N + 127) / 128) * nrb;
   const int64_t units = static_cast<int64_t>(p.n) * per_adapter;

@@ -263,6 +263,43 @@ def test_two_streams_at_once():
     assert all(bd.read_status(s[-1]) == 0 for s in sets)
 
 
+@pytest.mark.parametrize("m,n_out,k,r,n", [(6, 1160, 520, 64, 5), (330, 520, 1096, 24, 9), (2100, 264, 328, 64, 40)])
+def test_calls_back_to_back(m, n_out, k, r, n):
+    """Every buffer is written anew right ahead of the calls that read it, and read right
+    after, without a pause: the same bits as one batch at a time."""
+    q = bd.quantize(I.normal((n_out, 64 * (k // 64)), 0.02, 9).cuda())
+    kq = q.cols
+    batches = []
+    for i in range(6):
+        idx, A, B, scales, X, dY = _setup(m, n_out, kq, r, n, 140 + i, none=0.1 * i)
+        batches.append([t.cuda() for t in (idx, A, B, scales, X, dY)])
+    here = [torch.empty_like(t) for t in batches[0]]
+    idx, A, B, scales, X, dY = here
+    pool = bd.AdapterPool(A, B, scales)
+    groups = bd.adapter_groups(idx.fill_(-1), n)
+    ws = bd.new_workspace(bd.workspace_bytes_adapters(m, n_out, kq, r, True))
+
+    def step(batch):
+        for t, new in zip(here, batch):
+            t.copy_(new)
+        bd.adapter_groups(idx, n, out=groups, ws=ws)
+        Y, T = bd.linear_fwd_pool(q, pool, groups, X, ws=ws)
+        Z = Y.float()
+        bd.adapters_fwd(pool, groups, X, Z, ws=ws)
+        one = bd.linear_bwd_pool(q, pool, groups, X, dY, T, ws=ws)
+        dX = one[0].float()
+        return (Y, Z, *one, dX, *bd.adapters_bwd(pool, groups, X, dY, dX=dX, ws=ws))
+
+    alone = []
+    for b in batches:
+        alone.append(step(b))
+        torch.cuda.synchronize()
+    for _ in range(4):
+        got = [step(b) for b in batches]
+        assert all(torch.equal(x, y) for a, g in zip(alone, got) for x, y in zip(a, g))
+    assert bd.read_status(ws) == 0
+
+
 def test_parts_of_the_backward_alone():
     idx, A, B, scales, X, dY = _setup(90, 200, 136, 32, 4, 90)
     pool, groups = _pool(A, B, scales, None), bd.adapter_groups(idx.cuda(), 4)
