@@ -260,7 +260,7 @@ __device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_
 // The wait for the kernel ahead.  The next kernel may start only after it: one that reads early, or that waits for this
 // kernel alone, then finds everything before this kernel complete too.  So up and grad, which follow a kernel with this
 // order in the same call, may read before their wait, through L2, all that the kernel ahead does not write (the groups,
-// the pool, Y), which hides their start behind that kernel's end; what it writes (the planes), and writes of their own,
+// the pool, Y, X and dY), which hides their start behind that kernel's end; what it writes (the planes), and writes of their own,
 // come after.  Each CTA waits before it ends, whatever it had to do.
 __device__ __forceinline__ void pool_wait_ahead() {
   ptx::griddep_wait();
@@ -1114,7 +1114,6 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
     by_length[place] = i;
   }
   __syncthreads();
-  pool_wait_ahead();
   const int nrb = (p.r + 63) / 64;
   const int in_a = static_cast<int>((p.K + 127) / 128) * nrb, per_adapter = in_a + static_cast<int>((p.N + 127) / 128) * nrb;
   const int64_t units = static_cast<int64_t>(p.n) * per_adapter;
@@ -1164,6 +1163,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
             ptx::mbar_arrive_expect_tx(&full[pos.s], loads.bytes() * (2 + planes));
             pool_load_rows(loads, row4, d, tmV, &full[pos.s], u.fb * 128);
             pool_load_rows(loads, row4, d + 8192, tmV, &full[pos.s], u.fb * 128 + 64);
+            if (issued == 0) pool_wait_ahead();
             pool_load_planes(loads, row4, d + 16384, tmP, &full[pos.s], u.rb * 64, planes, m, 8192);
             ++issued;
           }
@@ -1229,6 +1229,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
   } else {
     // ------------------------------------------------------------ the gradients
     const int quad = warp & 3, half = (warp - 2) >> 2;
+    pool_wait_ahead();  // zeros are written without a load
     const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 32;
     for (int64_t round = 0; round < rounds && ok; ++round) {
       PoolGradUnit u;
@@ -1300,6 +1301,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
     if (!ok && lane == 0) pool_fail(sm, p.status);
   }
   if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the thread that loads
+  pool_wait_ahead();
   pool_teardown(tmem, kPoolGradTmem);
 }
 
