@@ -21,7 +21,8 @@ namespace qlora {
 // ---------------------------------------------------------------------------
 constexpr int kGroupThreads = 1024, kGroupWarps = kGroupThreads / 32;
 constexpr int kGroupCluster = 8;
-constexpr int64_t kGroupOneCta = 4096;  // tokens up to which one CTA is faster
+// Tokens up to which one CTA is faster (64 adapters: 1024 tokens 5.3 us against 6.4 with the cluster, 2048 7.3 against 6.6).
+constexpr int64_t kGroupOneCta = 1536;
 
 __device__ __forceinline__ int group_key(const int32_t *idx, int64_t t, int n, uint32_t *status) {
   const int a = idx[t];
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_groups_kernel(const int
 //   up    Out += s_a P W_a over the rank: Y with B^T, dX with A
 //   grad  s_a P^T V over the tokens of an adapter: dA, dB
 //
-// A tile holds tokens of one adapter, wherever their rows lie: runs of 32 rows come
+// A tile holds tokens of one adapter, wherever their rows lie: runs of 16, 32 or 64 rows come
 // with one tiled load, others four rows to a gather, and a short tile loads only the
 // rows it has.  Columns of the accumulator are independent, so a short tile's unused
 // columns need no zeros, and neither do rows past an adapter's rank.  How the tiles
@@ -463,20 +464,21 @@ struct PoolDownLayout {
   int rpad;      // floats a token of the partial sums
   uint32_t stage, stages, exch_at, bytes;
 };
-// roomy: the call is too small to give every SM a CTA, so that a deeper ring is worth more than a second one.
-__host__ __device__ constexpr PoolDownLayout pool_down_layout(int r, bool roomy) {
+// Two CTAs an SM up to rank 128; above it a stage is 36 KB and needs all of the shared memory.  (A ring twice as deep in
+// calls too small for two CTAs an SM was no faster: 8 tokens 13.0 against 13.1 us, 16 tokens 16.3 against 15.1.)
+__host__ __device__ constexpr PoolDownLayout pool_down_layout(int r) {
   PoolDownLayout l{};
   l.tn = r <= 128 ? 64 : 32;
   l.rpad = r <= 64 ? 64 : r <= 128 ? 128 : 256;
   l.stage = l.tn * 128u + l.rpad * 128u;  // token rows, then W's
   const uint32_t exch = l.tn * l.rpad * 4u;
-  const uint32_t fit = ((r <= 128 && !roomy ? kPoolHalfBytes : kPoolFullBytes) - exch) / l.stage;
+  const uint32_t fit = ((r <= 128 ? kPoolHalfBytes : kPoolFullBytes) - exch) / l.stage;
   l.stages = fit < kPoolMostStages ? fit : kPoolMostStages;
   l.exch_at = l.stages * l.stage;
   l.bytes = l.exch_at + exch;
   return l;
 }
-static_assert(pool_down_layout(64, false).stages >= 3 && pool_down_layout(128, false).stages >= 3 && pool_down_layout(256, false).stages >= 3,
+static_assert(pool_down_layout(64).stages >= 3 && pool_down_layout(128).stages >= 3 && pool_down_layout(256).stages >= 3,
               "a ring of three stages at least");
 
 struct PoolDownJob {
@@ -673,8 +675,8 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
 // four lanes (bf16; eight for float32) then share a token's 32 features in 16-byte pieces (element by element the
 // epilogue took 47 instructions an element and warp, and bound the kernel on issue).  The pieces are loaded an item
 // ahead, and the lines of the next block are prefetched to L2 (203 -> 172 us for 4096 tokens on 22016 float32 columns).
-// Tiles of up to four tokens go straight from the accumulator to Out, and other outputs, odd strides or columns of a
-// wider tensor, element by element.
+// Tiles of up to four tokens go straight from the accumulator to Out (32 decode tokens 16.8 -> 16.3 us), and other outputs,
+// odd strides or columns of a wider tensor, element by element.
 //   warp 0  loads; warp 1  products; warps 2..9  Out += s accumulator
 // W_MN false: W is [n][cols][r], K-major (Y: B); true: [n][r][cols], MN-major (dX: A).
 // ---------------------------------------------------------------------------
