@@ -261,8 +261,9 @@ __device__ __forceinline__ uint32_t pool_setup(const PoolSmem &s, uint32_t tmem_
 // The wait for the kernel ahead.  The next kernel may start only after it: one that reads early, or that waits for this
 // kernel alone, then finds everything before this kernel complete too.  So up and grad, which follow a kernel with this
 // order in the same call, may read before their wait, through L2, all that the kernel ahead does not write (the groups,
-// the pool, Y, X and dY), which hides their start behind that kernel's end; what it writes (the planes), and writes of their own,
-// come after.  Each CTA waits before it ends, whatever it had to do.
+// the pool, Y, X and dY), which hides their start behind that kernel's end; what it writes (the planes), and writes of
+// their own, come after.  Where grad is ahead of up, which share nothing but what both read, up does not wait for it
+// at all and fills the SMs as grad's CTAs end.  Each CTA waits before it ends, whatever it had to do.
 __device__ __forceinline__ void pool_wait_ahead() {
   ptx::griddep_wait();
   ptx::griddep_launch();
@@ -713,6 +714,7 @@ struct PoolUpArgs {
   int64_t cols, ldo;  // of Out
   void *out;
   int planes;
+  bool after_down;  // the kernel ahead writes P; else it is grad, which has waited for the one that did
   PoolUpLayout l;
 };
 
@@ -824,7 +826,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
         int b = 0, ch = 0;
         for (int i = 0; i < mine * nch; ++i) {
           if (i == min(static_cast<int>(stages), mine * nch) - 1) {
-            if (issued < stages) pool_wait_ahead();  // the first unit's
+            if (a.after_down && issued < stages) pool_wait_ahead();  // the first unit's
             ptx::mbar_arrive_expect_tx(p_full, nch * a.planes * rows.bytes());
             for (int c = 0; c < nch; ++c)
               pool_load_planes(rows, row4, sm.buf + l.planes_at + c * a.planes * l.plane, &tmP, p_full, c * 64, a.planes,

@@ -1152,10 +1152,11 @@ qlora_status launch_pool_down(const PoolArgs &p, const PoolDown *jobs, int dev, 
 
 // Out[t] += s_a P[t] W_a for every grouped token.  Y: W = B; dX: W = A (MN-major).
 template <bool W_MN, typename O>
-qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo, int dev,
-                              int sms, cudaStream_t st) {
+qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo,
+                              bool after_down, int dev, int sms, cudaStream_t st) {
   PoolUpArgs a;
   a.p = p;
+  a.after_down = after_down;
   a.cols = W_MN ? p.K : p.N;
   a.ldo = ldo;
   a.out = Out;
@@ -1178,9 +1179,9 @@ qlora_status launch_pool_up_t(const PoolArgs &p, const __nv_bfloat16 *P, const v
 }
 template <bool W_MN>
 qlora_status launch_pool_up(const PoolArgs &p, const __nv_bfloat16 *P, const void *W, void *Out, int64_t ldo, qlora_dtype dt,
-                            int dev, int sms, cudaStream_t st) {
-  return dt == QLORA_F32 ? launch_pool_up_t<W_MN, float>(p, P, W, Out, ldo, dev, sms, st)
-                         : launch_pool_up_t<W_MN, __nv_bfloat16>(p, P, W, Out, ldo, dev, sms, st);
+                            bool after_down, int dev, int sms, cudaStream_t st) {
+  return dt == QLORA_F32 ? launch_pool_up_t<W_MN, float>(p, P, W, Out, ldo, after_down, dev, sms, st)
+                         : launch_pool_up_t<W_MN, __nv_bfloat16>(p, P, W, Out, ldo, after_down, dev, sms, st);
 }
 
 template <typename O>
@@ -1306,7 +1307,7 @@ qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, cons
   __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
   const PoolDown down = {X, ldx, pool->A, T, false};
   const qlora_status s = launch_pool_down<kPoolT>(a, &down, dev, sms, st);
-  return s != QLORA_OK ? s : launch_pool_up<false>(a, T, pool->B, Y, ldy, y_dtype, dev, sms, st);
+  return s != QLORA_OK ? s : launch_pool_up<false>(a, T, pool->B, Y, ldy, y_dtype, true, dev, sms, st);
 }
 
 qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, const int32_t *offsets, const void *X,
@@ -1335,7 +1336,7 @@ qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, cons
                                 : launch_pool_grads<__nv_bfloat16>(a, U, X, ldx, T, dY, lddy, dA, dB, dev, sms, st);
     if (s != QLORA_OK) return s;
   }
-  return M > 0 && dX ? launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, dev, sms, st) : QLORA_OK;
+  return M > 0 && dX ? launch_pool_up<true>(a, U, pool->A, dX, lddx, dx_dtype, !dA, dev, sms, st) : QLORA_OK;
 }
 
 qlora_status check_out(const void *p, int64_t ld, int64_t cols, qlora_dtype dt) {
