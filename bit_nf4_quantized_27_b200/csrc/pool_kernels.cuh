@@ -539,7 +539,8 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
     const uint32_t idesc = ptx::idesc_bf16(128, (cnt + 15) / 16 * 16, mn ? 1 : 0, 0);
     if (warp == 0) {
       const PoolRowLoads rows = pool_tile_loads(p, tile_s, lane, row4);
-      if (ok && ptx::elect_one()) {
+      const bool one = ptx::elect_one();  // the whole warp, whatever a lane's own `ok`
+      if (ok && one) {
         const uint32_t bytes = rows.bytes();
         for (int ks = kb; ks < ke; ++ks) {
           // (a wait takes 140 cycles even where it is over: none for the first filling of the ring)
@@ -551,9 +552,10 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
         }
         if (!ok) pool_fail(sm, p.status);
       }
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);  // for all lanes, so that the warp stays together
     } else if (warp == 1) {
-      if (ok && ptx::elect_one()) {
+      const bool one = ptx::elect_one();
+      if (ok && one) {
         const uint32_t w_lbo = pool_desc_lbo(mn), w_16 = pool_desc_16(mn);
         const uint32_t v_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
         for (int ks = kb; ks < ke; ++ks) {
@@ -575,11 +577,12 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
         if (ok && ke > kb) ptx::mma_commit(sum_full);
         if (!ok) pool_fail(sm, p.status);
       }
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
     } else {
       const int quad = warp & 3, set = (warp - 2) >> 2;
       if (warp == 2) {
-        if (ok && ptx::elect_one()) {
+        const bool one = ptx::elect_one();
+        if (ok && one) {
           // W's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
           const int w_loads = mn ? (p.r + 63) / 64 : nrb;
           const uint32_t bytes = w_loads * (mn ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u);
@@ -822,7 +825,8 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
 
     if (warp == 0) {
       const PoolRowLoads rows = pool_tile_loads(p, tile_s, lane, row4);
-      if (ok && mine > 0 && ptx::elect_one()) {
+      const bool one = ptx::elect_one();
+      if (ok && mine > 0 && one) {
         // the first blocks of W, then P's rows, then the other blocks
         int b = 0, ch = 0;
         for (int i = 0; i < mine * nch; ++i) {
@@ -849,7 +853,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
         }
         if (!ok) pool_fail(sm, p.status);
       }
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
     } else if (warp == 1) {
       if (mine > 0 && ok) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(p_full, p_phase, sm.abort_flag));
@@ -887,12 +891,12 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
           }
           if (!ok) pool_fail(sm, p.status);
         }
+        ok = __all_sync(0xffffffffu, ok);
       } else {
         // The 8 ranks past the adapter's meet zeros in P and have to be finite: the warp clears them in each last chunk.
         const int leader = __ffs(__ballot_sync(0xffffffffu, one)) - 1;
         pos.s = __shfl_sync(0xffffffffu, pos.s, leader);
         pos.ph = __shfl_sync(0xffffffffu, pos.ph, leader);
-        ok = __all_sync(0xffffffffu, ok);
         for (int b = 0; b < mine && ok; ++b) {
           const uint32_t n = blocks + b, acc = n & 3;
           ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_empty[acc], ((n >> 2) & 1) ^ 1, sm.abort_flag));
