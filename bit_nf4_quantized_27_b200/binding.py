@@ -8,6 +8,8 @@ no fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import re
 
@@ -146,6 +148,23 @@ def _stream(stream=None):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _on_its_stream(fn):
+    """Gives fn a `stream` argument whose call runs with that stream as the current one.  What
+    a call allocates, its scratch and the outputs that the caller did not pass, then
+    belongs to the stream that its kernels run on: the scratch is zeroed in order with
+    them, and memory freed at the return is not handed to another stream under them."""
+    place = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        if "stream" not in kwargs and len(args) <= place:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(kwargs["stream"] if "stream" in kwargs else args[place]):  # no effect for None
+            return fn(*args, **kwargs)
+
+    return call
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -204,6 +223,7 @@ def new_workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return ws
 
 
+@_on_its_stream
 def quantize(w: torch.Tensor, out: NF4Weight | None = None, ws: torch.Tensor | None = None,
              stream=None, scale_format: str | None = None) -> NF4Weight:
     """NF4 codes with double-quantised block scales; scale_format (default the
@@ -221,6 +241,7 @@ def quantize(w: torch.Tensor, out: NF4Weight | None = None, ws: torch.Tensor | N
     return q
 
 
+@_on_its_stream
 def dequantize(q: NF4Weight, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None):
     y = out if out is not None else torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
     t = q.c_struct()
@@ -235,6 +256,7 @@ def _lora(A: torch.Tensor, B: torch.Tensor, alpha: float) -> LoraC:
     return LoraC(A.shape[0], float(alpha), A.data_ptr(), B.data_ptr())
 
 
+@_on_its_stream
 def linear_fwd(q: NF4Weight, A, B, alpha: float, X, y_dtype=torch.bfloat16, save_t: bool = True,
                ws: torch.Tensor | None = None, out: torch.Tensor | None = None, t_out=None, stream=None):
     """Y = X W'^T + (alpha/r) (X A^T) B^T.  Returns (Y, T or None); T is the
@@ -253,6 +275,7 @@ def linear_fwd(q: NF4Weight, A, B, alpha: float, X, y_dtype=torch.bfloat16, save
     return Y, T
 
 
+@_on_its_stream
 def linear_bwd(q: NF4Weight, A, B, alpha: float, X, dY, T=None, dx_dtype=torch.bfloat16,
                grad_dtype=torch.bfloat16, ws: torch.Tensor | None = None, outs=None, stream=None):
     """Returns (dX, dA, dB) for upstream gradient dY."""
@@ -313,6 +336,7 @@ class QLoRALinearFunction(torch.autograd.Function):
         return dX, dA, dB, None, None
 
 
+@_on_its_stream
 def merge(q: NF4Weight, A, B, alpha: float, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Merged export W_merged [N, K] bf16 = bf16(W' + (alpha/r) B A)."""
     if out is None:
@@ -336,6 +360,7 @@ def adamw_step(p: torch.Tensor, g: torch.Tensor, m: torch.Tensor, v: torch.Tenso
                                   step, _stream(stream)), "qlora_adamw_step")
 
 
+@_on_its_stream
 def linear_fwd_multi(q: NF4Weight, adapters, adapter_of_token, X, y_dtype=torch.bfloat16,
                      ws: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Decode forward of one base serving several adapters: adapters is a list of
@@ -362,6 +387,7 @@ def workspace_bytes_dropout(m: int, n: int, k: int, r: int, backward: bool) -> i
     return int(lib().qlora_workspace_bytes_dropout(m, n, k, r, 1 if backward else 0))
 
 
+@_on_its_stream
 def linear_fwd_dropout(q: NF4Weight, A, B, alpha: float, X, keep: torch.Tensor, p: float, y_dtype=torch.bfloat16,
                        save_t: bool = True, ws: torch.Tensor | None = None, stream=None):
     """Forward with LoRA dropout on the adapter input; keep is the packed
@@ -380,6 +406,7 @@ def linear_fwd_dropout(q: NF4Weight, A, B, alpha: float, X, keep: torch.Tensor, 
     return Y, T
 
 
+@_on_its_stream
 def linear_bwd_dropout(q: NF4Weight, A, B, alpha: float, X, dY, keep: torch.Tensor, p: float, T=None,
                        dx_dtype=torch.bfloat16, grad_dtype=torch.bfloat16, ws: torch.Tensor | None = None, stream=None):
     """Gradients (dX, dA, dB) of linear_fwd_dropout for upstream dY."""
@@ -440,6 +467,7 @@ def workspace_bytes_adapters(m: int, n: int, k: int, r: int, backward: bool) -> 
     return int(lib().qlora_workspace_bytes_adapters(m, n, k, r, 1 if backward else 0))
 
 
+@_on_its_stream
 def adapter_groups(adapter_of_token: torch.Tensor, n: int, out=None, ws: torch.Tensor | None = None, stream=None):
     """(order [M], offsets [n + 1]) int32: the tokens grouped by adapter (-1: none, last)."""
     idx = adapter_of_token
@@ -473,6 +501,7 @@ def _row_stride(t: torch.Tensor) -> int:
     return row if rows > 1 else max(row, cols)
 
 
+@_on_its_stream
 def adapters_fwd(pool: AdapterPool, groups, X: torch.Tensor, Y: torch.Tensor, save_t: bool = False, t_out=None,
                  ws: torch.Tensor | None = None, stream=None):
     """Adds every token's adapter term to Y in place: Y[t] += s_a (X[t] A_a^T) B_a^T.
@@ -502,6 +531,7 @@ def _pool_grads(pool: AdapterPool, grad_dtype, outs, device):
     return dA, dB
 
 
+@_on_its_stream
 def adapters_bwd(pool: AdapterPool, groups, X: torch.Tensor, dY: torch.Tensor, T=None, dX: torch.Tensor | None = None,
                  need_grads: bool = True, grad_dtype=torch.float32, outs=None, ws: torch.Tensor | None = None, stream=None):
     """Gradients of adapters_fwd.  Adds the adapters' part to dX in place (if given) and
@@ -524,6 +554,7 @@ def adapters_bwd(pool: AdapterPool, groups, X: torch.Tensor, dY: torch.Tensor, T
     return dA, dB
 
 
+@_on_its_stream
 def linear_fwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, y_dtype=torch.bfloat16, save_t: bool = True,
                     ws: torch.Tensor | None = None, out: torch.Tensor | None = None, t_out=None, stream=None):
     """Forward of the NF4 layer with every token's own adapter.  Returns (Y, T or None)."""
@@ -544,6 +575,7 @@ def linear_fwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, y_dtype=torch.bf
     return Y, T
 
 
+@_on_its_stream
 def linear_bwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, dY, T=None, dx_dtype=torch.bfloat16,
                     grad_dtype=torch.bfloat16, ws: torch.Tensor | None = None, outs=None, stream=None):
     """Returns (dX, dA [n, r, K], dB [n, N, r]) for upstream gradient dY."""
@@ -595,6 +627,7 @@ class TensorList:
     with a float32 scale per 256 elements.  The list keeps its tensors alive; they must
     not move (a gradient that is allocated anew needs a new list)."""
 
+    @_on_its_stream
     def __init__(self, grads, params=None, exp_avg=None, exp_avg_sq=None, p_bf16=None, exp_avg_scale=None,
                  exp_avg_sq_scale=None, lr_scale=None, stream=None):
         grads = list(grads)
@@ -646,6 +679,7 @@ def workspace_bytes_grad_norm() -> int:
     return int(lib().qlora_workspace_bytes_grad_norm())
 
 
+@_on_its_stream
 def grad_norm(tensors: TensorList, max_norm: float, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """float32 [2] on the device: the norm of all gradients and min(1, max_norm / (norm + 1e-6))."""

@@ -482,3 +482,40 @@ def test_captured_step_equals_the_eager_one():
             assert all(torch.equal(a, b) for a, b in zip(eager.state(), captured.state()))
             assert bd.read_status(eager.ws) == 0 and bd.read_status(captured.ws) == 0
     assert float(eager.clip[0]) > 0 and any(x.any() for x in eager.m)
+
+
+def test_a_given_stream_without_a_workspace():
+    """Calls that make their own scratch and outputs on a stream that is not the current one,
+    while the current stream fills memory of the same sizes as fast as it can: the bits
+    of calls on the current stream alone."""
+    m, n_out, k, r, n = 700, 520, 1088, 64, 5
+    idx, A, B, scales, X, dY = _setup(m, n_out, k, r, n, 150)
+    q = bd.quantize(I.normal((n_out, k), 0.02, 11).cuda())
+    pool, idx, X, dY = _pool(A, B, scales, None), idx.cuda(), X.cuda(), dY.cuda()
+    Y0, dX0 = torch.zeros(m, n_out, device="cuda"), torch.zeros(m, k, device="cuda")
+
+    def step(stream, Y, dX):
+        groups = bd.adapter_groups(idx, n, stream=stream)
+        T = bd.adapters_fwd(pool, groups, X, Y, save_t=True, stream=stream)
+        grads = bd.adapters_bwd(pool, groups, X, dY, dX=dX, stream=stream)
+        Z, T2 = bd.linear_fwd_pool(q, pool, groups, X, stream=stream)
+        more = bd.linear_bwd_pool(q, pool, groups, X, dY, T2, stream=stream)
+        tl = bd.TensorList([g.view(-1) for g in grads], stream=stream)
+        return (*groups, Y, dX, T, *grads, Z, T2, *more, bd.grad_norm(tl, 1.0, stream=stream)), tl
+
+    want, _ = step(None, Y0.clone(), dX0.clone())
+    side = torch.cuda.Stream()
+    sizes = [bd.STATUS_BYTES, bd.workspace_bytes_grad_norm(), 2 * (n + 1) * 4]
+    sizes += [bd.workspace_bytes_adapters(m, n_out, k, r, b) for b in (False, True)]
+    for _ in range(20):
+        Y, dX = Y0.clone(), dX0.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        got, tl = step(side, Y, dX)
+        for z in sizes * 4:
+            torch.empty(z, dtype=torch.uint8, device="cuda").fill_(0xff)
+        torch.cuda.synchronize()
+        # rows of T without an adapter are not written
+        rows = (idx >= 0)
+        for a, b in zip(want, got):
+            same = torch.equal(a[:, rows], b[:, rows]) if a.dim() == 3 and a.shape[:2] == (3, m) else torch.equal(a, b)
+            assert same
