@@ -1062,12 +1062,17 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 // grad: one unit is 128 features x 64 ranks of one adapter's dA or dB, summed over its tokens.  Both operands come as
 // token rows (MN-major), 64 tokens a step.  The first plane's products go round three accumulators and the other
-// planes' into a fourth, which keeps each one's chain of additions short.  While one unit is stored the next one's
-// tokens are loaded.  Units are taken longest adapter first, back and forth over the CTAs, so that long and short ones
+// planes' into a fourth; after kPoolGradFold steps the epilogue adds them to float32 sums in its registers and they start
+// anew.  Both keep an accumulator's chain of additions short: the tensor cores cut off where a float32 addition rounds,
+// which put a sum off by 2e-8 of itself for each addition in a chain.  While one unit is stored the next one's tokens are
+// loaded.  Units are taken longest adapter first, back and forth over the CTAs, so that long and short ones
 // meet: a CTA has one or two, and their lengths differ.  An adapter without tokens gets zeros.
 //   warp 0  loads; warp 1  products; warps 2..9  accumulators -> dA or dB
 // ---------------------------------------------------------------------------
 constexpr uint32_t kPoolGradTmem = 256;
+// Steps of 64 tokens until the accumulators start anew: chains of 64 additions.  One adapter, float32, error of dB: 8192
+// tokens 3.7e-6 -> 1.8e-6, 65536 2.6e-5 -> 1.9e-6; 16384 tokens of 11008 x 4096 take 418 us instead of 414.
+constexpr int kPoolGradFold = 48;
 
 struct PoolGradArgs {
   PoolArgs p;
@@ -1092,7 +1097,29 @@ struct PoolGradUnit {
   bool is_a;
 };
 
-template <typename O>
+// sum += 16 columns of the accumulators of `steps` steps (those that took part): three at 0, 64 and 128 with the first
+// plane's products, and the other planes' at 192.
+__device__ __forceinline__ void pool_add_accumulators(uint32_t from, int steps, float *sum) {
+  uint32_t v[16], w[16];
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+  if (steps > 1) {
+    ptx::tmem_ld16(from + 64, v);
+    if (steps > 2) ptx::tmem_ld16(from + 128, w);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]) + (steps > 2 ? __uint_as_float(w[i]) : 0.0f);
+  }
+  ptx::tmem_ld16(from, v);
+  ptx::tmem_ld16(from + 192, w);
+  ptx::tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum[i] += (__uint_as_float(v[i]) + x[i]) + __uint_as_float(w[i]);
+}
+
+// kFold: a unit may have more than kPoolGradFold steps.
+template <typename O, bool kFold>
 __global__ void __launch_bounds__(kPoolThreads, 2)
     pool_grad_kernel(const __grid_constant__ PoolMaps tmX, const __grid_constant__ PoolMaps tmU,
                      const __grid_constant__ PoolMaps tmDY, const __grid_constant__ PoolMaps tmT, const PoolGradArgs a) {
@@ -1191,46 +1218,50 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
     for (int64_t round = 0; round < rounds && ok; ++round) {
       PoolGradUnit u;
       if (!unit_of(round, u) || u.live <= 0 || u.cnt == 0) continue;
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_empty0, acc_phase ^ 1, sm.abort_flag) &&
-                                       ptx::mbar_wait(acc_empty1, acc_phase ^ 1, sm.abort_flag));
-      acc_phase ^= 1;
-      uint32_t turn = 0, used = 0;
-      for (int t0 = 0; t0 < u.cnt && ok; t0 += 64) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
-        if (!ok) break;
-        const int valid = min(64, u.cnt - t0);
-        if (valid & 15) {
-          // the last 16 tokens are not all there: zero rows of P meet repeated rows of V
-          uint8_t *d = sm.buf + pos.s * stage_bytes + 16384;
-          const int pad = 16 - (valid & 15);
-          for (int i = lane; i < pad * 8 * a.planes; i += 32) {
-            const int pl = i / (pad * 8), e = i - pl * pad * 8;
-            *reinterpret_cast<uint4 *>(d + pl * 8192 + (valid + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      for (int part = 0; part < u.cnt && ok; part += kPoolGradFold * 64) {
+        const int end = kFold ? min(u.cnt, part + kPoolGradFold * 64) : u.cnt;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_empty0, acc_phase ^ 1, sm.abort_flag) &&
+                                         ptx::mbar_wait(acc_empty1, acc_phase ^ 1, sm.abort_flag));
+        acc_phase ^= 1;
+        uint32_t turn = 0, used = 0;
+        for (int t0 = kFold ? part : 0; t0 < end && ok; t0 += 64) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
+          if (!ok) break;
+          const int valid = min(64, u.cnt - t0);
+          if (valid & 15) {
+            // the last 16 tokens are not all there: zero rows of P meet repeated rows of V
+            uint8_t *d = sm.buf + pos.s * stage_bytes + 16384;
+            const int pad = 16 - (valid & 15);
+            for (int i = lane; i < pad * 8 * a.planes; i += 32) {
+              const int pl = i / (pad * 8), e = i - pl * pad * 8;
+              *reinterpret_cast<uint4 *>(d + pl * 8192 + (valid + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
           }
-          ptx::fence_proxy_async_smem();
+          ptx::tc_fence_after();
+          if (one) {
+            const uint32_t v = base + pos.s * (stage_bytes >> 4), b = v + (16384 >> 4), d = tmem + turn * 64;
+            const uint32_t more = used & (1u << turn) ? 1u : 0u, rest = used ? 1u : 0u;
+#pragma unroll
+            for (int k16 = 0; k16 < 4; ++k16) {
+              if (k16 * 16 >= valid) break;
+              ptx::mma_bf16_lohi(d, v + k16 * k16s, kPoolDescHi, b + k16 * k16s, kPoolDescHi, idesc, k16 ? 1u : more);
+#pragma unroll
+              for (int pl = 1; pl < kPoolPlanes; ++pl)
+                if (pl < a.planes)
+                  ptx::mma_bf16_lohi(tmem + 192, v + k16 * k16s, kPoolDescHi, b + pl * (8192 >> 4) + k16 * k16s, kPoolDescHi, idesc,
+                                     (k16 || pl > 1) ? 1u : rest);
+            }
+            ptx::mma_commit(&empty[pos.s]);
+            if (t0 + 64 >= end) ptx::mma_commit(acc_full);
+          }
           __syncwarp();
+          used |= 1u << turn;
+          turn = turn == 2 ? 0 : turn + 1;
+          pos.next(stages);
         }
-        ptx::tc_fence_after();
-        if (one) {
-          const uint32_t v = base + pos.s * (stage_bytes >> 4), b = v + (16384 >> 4), d = tmem + turn * 64;
-          const uint32_t more = used & (1u << turn) ? 1u : 0u, rest = used ? 1u : 0u;
-#pragma unroll
-          for (int k16 = 0; k16 < 4; ++k16) {
-            if (k16 * 16 >= valid) break;
-            ptx::mma_bf16_lohi(d, v + k16 * k16s, kPoolDescHi, b + k16 * k16s, kPoolDescHi, idesc, k16 ? 1u : more);
-#pragma unroll
-            for (int pl = 1; pl < kPoolPlanes; ++pl)
-              if (pl < a.planes)
-                ptx::mma_bf16_lohi(tmem + 192, v + k16 * k16s, kPoolDescHi, b + pl * (8192 >> 4) + k16 * k16s, kPoolDescHi, idesc,
-                                   (k16 || pl > 1) ? 1u : rest);
-          }
-          ptx::mma_commit(&empty[pos.s]);
-          if (t0 + 64 >= u.cnt) ptx::mma_commit(acc_full);
-        }
-        __syncwarp();
-        used |= 1u << turn;
-        turn = turn == 2 ? 0 : turn + 1;
-        pos.next(stages);
+        if (!kFold) break;
       }
     }
     if (!ok && lane == 0) pool_fail(sm, p.status);
@@ -1247,38 +1278,43 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
       const int steps = (u.cnt + 63) / 64, j0 = u.rb * 64 + half * 32;  // ranks j0 .. j0 + 32
       const float s = p.scales[u.ad];
       const int64_t cols = u.is_a ? p.K : p.N, f = static_cast<int64_t>(u.fb) * 128 + quad * 32 + lane;
-      if (sums) {
+      auto wait = [&]() {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_full, acc_phase, sm.abort_flag));
         acc_phase ^= 1;
-        if (!ok) break;
-        ptx::tc_fence_after();
+        if (ok) ptx::tc_fence_after();
+        return ok;
+      };
+      auto done = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(half ? acc_empty1 : acc_empty0);
+      };
+      float sum[kFold ? 32 : 16];  // with one part, half of the ranks at a time, the first stored while the others are read
+      if (kFold) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i % (kFold ? 32 : 16)] = 0.0f;
+        for (int at = 0; sums && at < steps && wait(); at += kPoolGradFold) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 16) pool_add_accumulators(from + c, steps - at, sum + (kFold ? c : 0));
+          done();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i % (kFold ? 32 : 16)] = sums && half * 32 + i < u.live ? s * sum[i % (kFold ? 32 : 16)] : 0.0f;
+      } else if (sums) {
+        wait();
       }
+      if (!ok) break;
+#pragma unroll
       for (int c = 0; c < 32; c += 16) {
-        float x[16];
+        float *x = sum + (kFold ? c : 0);
+        if (!kFold) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-        if (sums) {
-          uint32_t v[16], w[16];
-          ptx::tmem_ld16(from + c, v);
-          ptx::tmem_ld16(from + 192 + c, w);
-          ptx::tmem_ld_wait();
+          for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+          if (sums) {
+            pool_add_accumulators(from + c, steps, x);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
-          float rest[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) rest[i] = __uint_as_float(w[i]);
-          if (steps > 1) {
-            ptx::tmem_ld16(from + 64 + c, v);
-            if (steps > 2) ptx::tmem_ld16(from + 128 + c, w);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(v[i]) + (steps > 2 ? __uint_as_float(w[i]) : 0.0f);
+            for (int i = 0; i < 16; ++i) x[i] = half * 32 + c + i < u.live ? s * x[i] : 0.0f;
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = s * (x[i] + rest[i]);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (half * 32 + c + i >= u.live) x[i] = 0.0f;
         }
         if (f >= cols) {
         } else if (u.is_a) {
@@ -1302,10 +1338,7 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
         }
         __syncwarp();
       }
-      if (sums) {
-        ptx::tc_fence_before();
-        if (lane == 0) ptx::mbar_arrive(half ? acc_empty1 : acc_empty0);
-      }
+      if (!kFold && sums) done();
     }
     if (!ok && lane == 0) pool_fail(sm, p.status);
   }
@@ -1316,15 +1349,24 @@ __global__ void __launch_bounds__(kPoolThreads, 2)
 
 // ---------------------------------------------------------------------------
 // grad, split: the same for calls with so few units that CTAs would be idle.  The CTAs of a cluster each take a part of
-// a unit's tokens and add up as in down.
-//   warp 0  loads; warp 1  products; warps 2..5  accumulator -> shared memory; all  the sum
+// a unit's tokens, sum it in the four accumulators as grad does (in one, 131072 tokens were 5e-5 off; now 1.1e-6), and add
+// up as in down.
+//   warp 0  loads; warp 1  products; warps 2..5  accumulators -> shared memory; all  the sum
 // ---------------------------------------------------------------------------
 constexpr int kPoolGradSplitThreads = 192;
-constexpr uint32_t kPoolGradSplitTmem = 64;
+// Units of 128 features x 64 ranks of all adapters' dA and dB.
+__host__ __device__ constexpr int64_t pool_grad_units(int n, int r, int64_t K, int64_t N) {
+  return static_cast<int64_t>(n) * ((r + 63) / 64) * ((K + 127) / 128 + (N + 127) / 128);
+}
+// An adapter's tokens are split over CTAs where units are few, so that CTAs are idle, and tokens many (16 units: 8192
+// tokens 32 us against 90, 2048 17.6 against 30.6, but 256 13.3 against 12.1; 64 units of 512 tokens 22.5 against 16.9).
+__host__ __device__ constexpr bool pool_grad_splits(int64_t units, int64_t M, int n, int sms) {
+  return 2 * units < sms && M >= 1024 * static_cast<int64_t>(n);
+}
 constexpr uint32_t kPoolGradSplitBytes = 98 * 1024;  // two CTAs share an SM
 
 template <typename O>
-__global__ void __launch_bounds__(kPoolGradSplitThreads)
+__global__ void __launch_bounds__(kPoolGradSplitThreads, 2)
     pool_grad_split_kernel(const __grid_constant__ PoolMaps tmX, const __grid_constant__ PoolMaps tmU,
                            const __grid_constant__ PoolMaps tmDY, const __grid_constant__ PoolMaps tmT, const PoolGradArgs a) {
   extern __shared__ uint8_t pool_raw[];
@@ -1334,7 +1376,8 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t stage_bytes = 16384u + a.planes * 8192u, stages = min(kPoolGradSplitBytes / stage_bytes, kPoolMostStages);
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *acc_full = sm.bars + 2 * kPoolMostStages;
-  const uint32_t tmem = pool_setup(sm, kPoolGradSplitTmem, kPoolBars);
+  uint64_t *acc_empty = acc_full + 1;  // from the four warps
+  const uint32_t tmem = pool_setup(sm, kPoolGradTmem, 2 * kPoolMostStages + 1);
   pool_wait_ahead();
   const int nrb = (p.r + 63) / 64;
   const int in_a = static_cast<int>((p.K + 127) / 128) * nrb, per_adapter = in_a + static_cast<int>((p.N + 127) / 128) * nrb;
@@ -1382,7 +1425,17 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads)
       if (!ok && lane == 0) pool_fail(sm, p.status);
     } else if (warp == 1) {
       const uint32_t idesc = ptx::idesc_bf16(128, 64, 1, 1);
+      constexpr uint32_t kLbo = pool_desc_lbo(true), k16s = pool_desc_16(true);
+      const uint32_t base = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024)) + kLbo;
+      uint32_t turn = 0, used = 0;
       for (int st = sb; st < se && ok; ++st) {
+        const int in_part = (st - sb) % kPoolGradFold;
+        if (in_part == 0) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_empty, acc_phase ^ 1, sm.abort_flag));
+          if (!ok) break;
+          acc_phase ^= 1;
+          turn = used = 0;
+        }
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag));
         if (!ok) break;
         uint8_t *d = sm.buf + pos.s * stage_bytes;
@@ -1399,42 +1452,52 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads)
         }
         ptx::tc_fence_after();
         if (lane == 0) {
-          const uint32_t v = ptx::smem_addr(d), b = v + 16384;
-          for (int k16 = 0; k16 * 16 < valid; ++k16)
-            for (int pl = 0; pl < a.planes; ++pl)
-              ptx::mma_bf16(tmem, ptx::smem_desc_sw128(v + k16 * 2048, 8192, 1024),
-                            ptx::smem_desc_sw128(b + pl * 8192 + k16 * 2048, 8192, 1024), idesc, (st != sb || k16 || pl) ? 1u : 0u);
+          const uint32_t v = base + pos.s * (stage_bytes >> 4), b = v + (16384 >> 4), acc = tmem + turn * 64;
+          const uint32_t more = used & (1u << turn) ? 1u : 0u, rest = used ? 1u : 0u;
+#pragma unroll
+          for (int k16 = 0; k16 < 4; ++k16) {
+            if (k16 * 16 >= valid) break;
+            ptx::mma_bf16_lohi(acc, v + k16 * k16s, kPoolDescHi, b + k16 * k16s, kPoolDescHi, idesc, k16 ? 1u : more);
+#pragma unroll
+            for (int pl = 1; pl < kPoolPlanes; ++pl)
+              if (pl < a.planes)
+                ptx::mma_bf16_lohi(tmem + 192, v + k16 * k16s, kPoolDescHi, b + pl * (8192 >> 4) + k16 * k16s, kPoolDescHi, idesc,
+                                   (k16 || pl > 1) ? 1u : rest);
+          }
           ptx::mma_commit(&empty[pos.s]);
+          if (in_part == kPoolGradFold - 1 || st + 1 == se) ptx::mma_commit(acc_full);
         }
         __syncwarp();
+        used |= 1u << turn;
+        turn = turn == 2 ? 0 : turn + 1;
         pos.next(stages);
       }
-      if (ok && se > sb && lane == 0) ptx::mma_commit(acc_full);
       if (!ok && lane == 0) pool_fail(sm, p.status);
       __syncwarp();
     } else if (steps > 0) {
       const int quad = warp & 3, f = quad * 32 + lane;
-      if (se > sb && ok) {
+      float sum[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) sum[j] = 0.0f;
+      for (int done = sb; done < se && ok; done += kPoolGradFold) {
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(acc_full, acc_phase, sm.abort_flag));
         acc_phase ^= 1;
-        if (!ok && lane == 0) pool_fail(sm, p.status);
+        if (!ok) {
+          if (lane == 0) pool_fail(sm, p.status);
+          break;
+        }
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 64; c += 16)
+          pool_add_accumulators(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, se - done, sum + c);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(acc_empty);
       }
-      ptx::tc_fence_after();
       // dA: [rank][feature], dB: [feature][rank] with a pitch that keeps pairs aligned and lanes on 16 banks
       const int pitch = is_a ? 128 : 1, lane_pitch = is_a ? 1 : 66;
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t v[32];
-        if (se > sb && ok) {
-          ptx::tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0, v);
-          ptx::tmem_ld_wait();
-        } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) exch[(c0 + j) * pitch + f * lane_pitch] = __uint_as_float(v[j]);
-      }
-      ptx::tc_fence_before();
+      for (int j = 0; j < 64; ++j) exch[j * pitch + f * lane_pitch] = sum[j];
     }
     if (steps > 0) pool_cluster_sync();
     // this CTA's share, in pairs of consecutive elements of the output
@@ -1470,7 +1533,7 @@ __global__ void __launch_bounds__(kPoolGradSplitThreads)
     }
   }
   if (issued && *sm.abort_flag) ring_drain(full, pos, stages, issued);  // the thread that loads
-  pool_teardown(tmem, kPoolGradSplitTmem);
+  pool_teardown(tmem, kPoolGradTmem);
 }
 
 }  // namespace qlora

@@ -1197,15 +1197,15 @@ qlora_status launch_pool_grads(const PoolArgs &p, const __nv_bfloat16 *U, const 
   if (p.M > 0 && (!tmap_tokens(&tmX, X, p.K, p.M, ldx) || !tmap_planes(&tmU, U, p.r, p.M, a.planes) ||
                   !tmap_tokens(&tmDY, dY, p.N, p.M, lddy) || !tmap_planes(&tmT, T, p.r, p.M, a.planes)))
     return QLORA_ERR_CUDA;
-  const int64_t units = static_cast<int64_t>(p.n) * ((p.r + 63) / 64) * ((p.K + 127) / 128 + (p.N + 127) / 128);
-  // An adapter's tokens are split over CTAs where units are few, so that CTAs are idle, and tokens many (16 units: 8192
-  // tokens 32 us against 90, 2048 17.6 against 30.6, but 256 13.3 against 12.1; 64 units of 512 tokens 22.5 against 16.9).
-  if (2 * units >= sms || p.M < 1024 * static_cast<int64_t>(p.n)) {
+  const int64_t units = pool_grad_units(p.n, p.r, p.K, p.N);
+  if (!pool_grad_splits(units, p.M, p.n, sms)) {
     a.stages = pool_grad_stages(a.planes, p.n);
     a.bytes = pool_grad_bytes(a.planes, p.n);
-    static PoolKernelState states[64];
-    auto kernel = pool_grad_kernel<O>;
-    const qlora_status s = pool_attributes(kernel, kPoolHalfBytes, states[dev]);
+    static PoolKernelState states[2][64];
+    // sums in parts where an adapter may have that many tokens
+    const bool fold = p.M > kPoolGradFold * 64;
+    auto kernel = fold ? pool_grad_kernel<O, true> : pool_grad_kernel<O, false>;
+    const qlora_status s = pool_attributes(kernel, kPoolHalfBytes, states[fold][dev]);
     if (s != QLORA_OK) return s;
     return launch_pool(kernel, std::min<int64_t>(units, 2 * sms), 1, kPoolThreads, a.bytes, st, tmX, tmU, tmDY, tmT, a);
   }
