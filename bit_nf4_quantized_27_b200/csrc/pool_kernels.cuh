@@ -447,7 +447,7 @@ __host__ __device__ constexpr uint32_t pool_desc_16(bool mn) { return mn ? 128u 
 // down: g CTAs of a cluster take a tile of 64 tokens (32 above rank 128) and sum a part of the long dimension each,
 // with the accumulator's rows as ranks and its columns as tokens.  The steps of 64 go round four accumulators, which
 // keeps each one's chain of float32 additions short (the tensor cores' additions cut off: one chain over 1400 elements
-// was 3e-6 off, all to one side).  Each CTA leaves its float32 partial sums in shared memory; each then adds up a share
+// was 3e-6 off, all to one side); after kPoolDownFold steps they are added to the partial sums and start anew.  Each CTA leaves its float32 partial sums in shared memory; each then adds up a share
 // of the tokens over the g CTAs, in CTA order, through distributed shared memory, and writes the planes: no partial
 // planes in HBM, no further launch, and the same bits every time.  g, a divisor of the cluster, follows on the device
 // from the number of tiles.
@@ -458,6 +458,10 @@ __host__ __device__ constexpr uint32_t pool_desc_16(bool mn) { return mn ? 128u 
 // mn false: W is [n][r][len], K-major (T: A); true: [n][len][r], MN-major (U: B).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kPoolDownTmem = 256;
+// Steps of 64 until the accumulators start anew: chains of 64 additions.  U summed by one CTA over 11008 elements put dA
+// 1.7e-6 further off before, and T over 20008 was 5.4e-6 off; such calls take as long as before within 1% (8192 tokens of
+// 11008 x 4096, one adapter, backward 216 us, forward of 22016 -> 8192 186).
+constexpr int kPoolDownFold = 64;
 // Shared memory: two CTAs an SM, or all of it for one.
 constexpr uint32_t kPoolHalfBytes = 107 * 1024, kPoolFullBytes = 218 * 1024;
 
@@ -499,7 +503,8 @@ struct PoolDownArgs {
 
 // kSums: T, U, or both (found at run time, they cost a call with one token 0.9 us of 12.8).
 enum PoolSums { kPoolT, kPoolU, kPoolBoth };
-template <PoolSums kSums>
+// kFold: a CTA may have more than kPoolDownFold steps.
+template <PoolSums kSums, bool kFold>
 __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid_constant__ PoolDownArgs a) {
   extern __shared__ uint8_t pool_raw[];
   __shared__ int4 row4[16];
@@ -518,7 +523,8 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
   uint64_t *full = sm.bars, *empty = sm.bars + kPoolMostStages, *sum_full = sm.bars + 2 * kPoolMostStages;
   float *exch = reinterpret_cast<float *>(sm.buf + l.exch_at);
   if (tid < 5) ptx::prefetch_tmap(tid == 0 ? &job.W : tid == 1 ? &job.V.row : tid == 2 ? &job.V.row16 : tid == 3 ? &job.V.row32 : &job.V.row64);
-  const uint32_t tmem = pool_setup(sm, kPoolDownTmem, kPoolBars, kPoolMostStages);
+  uint64_t *sum_empty0 = sum_full + 1, *sum_empty1 = sum_full + 2;  // from the two sets of four warps
+  const uint32_t tmem = pool_setup(sm, kPoolDownTmem, 2 * kPoolMostStages + 1, kPoolMostStages);
   pool_wait_ahead();
   const PoolWalk walk = pool_walk(p, tn, warp_sum);
   // a tile is shared by g CTAs of the cluster: the largest divisor with which all tiles are at work at once
@@ -559,10 +565,19 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
         const uint32_t w_lbo = pool_desc_lbo(mn), w_16 = pool_desc_16(mn);
         const uint32_t v_lo = static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(sm.buf), 16, 1024));
         for (int ks = kb; ks < ke; ++ks) {
+          const int in_part = kFold ? (ks - kb) % kPoolDownFold : ks - kb;
+          if (kFold && in_part == 0 && ks > kb) {
+            ptx::mma_commit(sum_full);
+            if (!ptx::mbar_wait(sum_empty0, sum_phase, sm.abort_flag) || !ptx::mbar_wait(sum_empty1, sum_phase, sm.abort_flag)) {
+              ok = false;
+              break;
+            }
+            sum_phase ^= 1;
+          }
           if (!ptx::mbar_wait(&full[pos.s], pos.ph, sm.abort_flag)) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint32_t v = v_lo + pos.s * (l.stage >> 4), w = v + (v_bytes >> 4) + w_lbo, d = tmem + ((ks - kb) & 3) * acc_cols;
-          const uint32_t more = ks - kb >= 4 ? 1u : 0u;
+          const uint32_t v = v_lo + pos.s * (l.stage >> 4), w = v + (v_bytes >> 4) + w_lbo, d = tmem + (in_part & 3) * acc_cols;
+          const uint32_t more = in_part >= 4 ? 1u : 0u;
 #pragma unroll
           for (int k16 = 0; k16 < 4; ++k16)
             ptx::mma_bf16_lohi(d, w + k16 * w_16, kPoolDescHi, v + k16 * 2, kPoolDescHi, idesc, k16 ? 1u : more);
@@ -580,58 +595,69 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
       ok = __all_sync(0xffffffffu, ok);
     } else {
       const int quad = warp & 3, set = (warp - 2) >> 2;
-      if (warp == 2) {
-        const bool one = ptx::elect_one();
-        if (ok && one) {
-          // W's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
-          const int w_loads = mn ? (p.r + 63) / 64 : nrb;
-          const uint32_t bytes = w_loads * (mn ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u);
-          for (int ks = kb; ks < ke; ++ks) {
-            if (issued >= stages && !ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
-            uint8_t *st = sm.buf + pos.s * l.stage + v_bytes;
-            uint64_t *bar = &full[pos.s];
-            ptx::mbar_arrive_expect_tx(bar, bytes);
-            for (int i = 0; i < w_loads; ++i)
-              ptx::tma_load_3d(st + i * (mn ? 8192 : 16384), &job.W, bar, mn ? i * 64 : ks * 64, mn ? ks * 64 : i * 128, ad);
-            ++issued;
-            pos.next(stages);
+      // a part at a time: W's loads for it, then its accumulators
+      for (int part = kb;; part += kPoolDownFold) {
+        const int end = kFold ? min(ke, part + kPoolDownFold) : ke;
+        if (warp == 2) {
+          const bool one = ptx::elect_one();
+          if (ok && one) {
+            // W's ranks [0, min(r, 256)): K-major in boxes of up to 128 rows, MN-major in boxes of 64 ranks
+            const int w_loads = mn ? (p.r + 63) / 64 : nrb;
+            const uint32_t bytes = w_loads * (mn ? 8192u : static_cast<uint32_t>(min(p.r, 128)) * 128u);
+            for (int ks = kFold ? part : kb; ks < end; ++ks) {
+              if (issued >= stages && !ptx::mbar_wait(&empty[pos.s], pos.ph ^ 1, sm.abort_flag)) { ok = false; break; }
+              uint8_t *st = sm.buf + pos.s * l.stage + v_bytes;
+              uint64_t *bar = &full[pos.s];
+              ptx::mbar_arrive_expect_tx(bar, bytes);
+              for (int i = 0; i < w_loads; ++i)
+                ptx::tma_load_3d(st + i * (mn ? 8192 : 16384), &job.W, bar, mn ? i * 64 : ks * 64, mn ? ks * 64 : i * 128, ad);
+              ++issued;
+              pos.next(stages);
+            }
+            if (!ok) pool_fail(sm, p.status);
           }
-          if (!ok) pool_fail(sm, p.status);
+          ok = __all_sync(0xffffffffu, ok);
         }
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      if (ke > kb && ok) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(sum_full, sum_phase, sm.abort_flag));
-        sum_phase ^= 1;
-        if (!ok && lane == 0) pool_fail(sm, p.status);
-      }
-      ptx::tc_fence_after();
-      int rpad = l.rpad;
-      asm volatile("" : "+r"(rpad));  // in a register: read again as a parameter, each store took 60 ns
-      const int nacc = ok ? min(4, ke - kb) : 0, c_end = min(cnt, (set + 1) * (tn / 2));
-      for (int rb = 0; rb < nrb; ++rb) {
-        if (rb * 128 + quad * 32 >= p.r) break;
-        for (int c0 = set * (tn / 2); c0 < c_end; c0 += 16) {
-          const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + rb * tn + c0;
-          float *to = exch + c0 * rpad + rb * 128 + quad * 32 + lane;
-          float x[16];
+        if (ke > kb && ok) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(sum_full, sum_phase, sm.abort_flag));
+          sum_phase ^= 1;
+          if (!ok && lane == 0) pool_fail(sm, p.status);
+        }
+        ptx::tc_fence_after();
+        int rpad = l.rpad;
+        asm volatile("" : "+r"(rpad));  // in a register: read again as a parameter, each store took 60 ns
+        const int nacc = ok ? min(4, end - (kFold ? part : kb)) : 0, c_end = min(cnt, (set + 1) * (tn / 2));
+        for (int rb = 0; rb < nrb; ++rb) {
+          if (rb * 128 + quad * 32 >= p.r) break;
+          for (int c0 = set * (tn / 2); c0 < c_end; c0 += 16) {
+            const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + rb * tn + c0;
+            float *to = exch + c0 * rpad + rb * 128 + quad * 32 + lane;
+            float x[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+            for (int j = 0; j < 16; ++j) x[j] = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            if (i >= nacc) break;
-            uint32_t v[16], w[16];
-            ptx::tmem_ld16(from + i * acc_cols, v);
-            if (i + 1 < nacc) ptx::tmem_ld16(from + (i + 1) * acc_cols, w);
-            ptx::tmem_ld_wait();
+            for (int i = 0; i < 4; i += 2) {
+              if (i >= nacc) break;
+              uint32_t v[16], w[16];
+              ptx::tmem_ld16(from + i * acc_cols, v);
+              if (i + 1 < nacc) ptx::tmem_ld16(from + (i + 1) * acc_cols, w);
+              ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]) + (i + 1 < nacc ? __uint_as_float(w[j]) : 0.0f);
+              for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]) + (i + 1 < nacc ? __uint_as_float(w[j]) : 0.0f);
+            }
+            if (kFold && part > kb) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] += to[j * rpad];
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) to[j * rpad] = x[j];  // up to 15 that are not tokens: not read
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) to[j * rpad] = x[j];  // up to 15 that are not tokens: not read
         }
+        ptx::tc_fence_before();
+        if (!kFold || end >= ke || !ok) break;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(set ? sum_empty1 : sum_empty0);
       }
-      ptx::tc_fence_before();
     }
 
     pool_cluster_sync();

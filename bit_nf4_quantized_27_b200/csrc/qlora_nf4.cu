@@ -1093,10 +1093,10 @@ int64_t pool_down_steps(int64_t tiles, int64_t steps, int64_t clusters, int cs) 
 }
 
 // T, U, or U and T in one launch.
-template <PoolSums kSums>
-qlora_status launch_pool_down(const PoolArgs &p, const PoolDown *jobs, int dev, int sms, cudaStream_t st) {
+template <PoolSums kSums, bool kFold>
+qlora_status launch_pool_down_t(const PoolArgs &p, const PoolDown *jobs, int dev, cudaStream_t st) {
   constexpr int n_jobs = kSums == kPoolBoth ? 2 : 1;
-  auto kernel = pool_down_kernel<kSums>;
+  auto kernel = pool_down_kernel<kSums, kFold>;
   const int64_t adapters = std::min<int64_t>(p.n, p.M);
   PoolDownArgs a = {};
   a.p = p;
@@ -1148,6 +1148,14 @@ qlora_status launch_pool_down(const PoolArgs &p, const PoolDown *jobs, int dev, 
   a.job[0].clusters = a.job[1].first = c0;
   a.job[1].clusters = c1;
   return launch_pool(kernel, c0 + c1, best_cs, kPoolThreads, a.l.bytes, st, a);
+}
+
+template <PoolSums kSums>
+qlora_status launch_pool_down(const PoolArgs &p, const PoolDown *jobs, int dev, cudaStream_t st) {
+  int64_t longest = 0;
+  for (int i = 0; i < (kSums == kPoolBoth ? 2 : 1); ++i) longest = std::max(longest, jobs[i].mn ? p.N : p.K);
+  return longest > kPoolDownFold * 64 ? launch_pool_down_t<kSums, true>(p, jobs, dev, st)
+                                      : launch_pool_down_t<kSums, false>(p, jobs, dev, st);
 }
 
 // Out[t] += s_a P[t] W_a for every grouped token.  Y: W = B; dX: W = A (MN-major).
@@ -1306,7 +1314,7 @@ qlora_status pool_fwd(const qlora_adapter_pool *pool, const int32_t *order, cons
   }
   __nv_bfloat16 *T = static_cast<__nv_bfloat16 *>(T_save ? T_save : static_cast<uint8_t *>(ws) + QLORA_STATUS_BYTES);
   const PoolDown down = {X, ldx, pool->A, T, false};
-  const qlora_status s = launch_pool_down<kPoolT>(a, &down, dev, sms, st);
+  const qlora_status s = launch_pool_down<kPoolT>(a, &down, dev, st);
   return s != QLORA_OK ? s : launch_pool_up<false>(a, T, pool->B, Y, ldy, y_dtype, true, dev, sms, st);
 }
 
@@ -1324,9 +1332,9 @@ qlora_status pool_bwd(const qlora_adapter_pool *pool, const int32_t *order, cons
       __nv_bfloat16 *Tw = U + align256(static_cast<size_t>(kPoolPlanes) * M * a.r * 2) / 2;
       down[1] = {X, ldx, pool->A, Tw, false};
       T = Tw;
-      s = launch_pool_down<kPoolBoth>(a, down, dev, sms, st);
+      s = launch_pool_down<kPoolBoth>(a, down, dev, st);
     } else {
-      s = launch_pool_down<kPoolU>(a, down, dev, sms, st);
+      s = launch_pool_down<kPoolU>(a, down, dev, st);
     }
     if (s != QLORA_OK) return s;
   }

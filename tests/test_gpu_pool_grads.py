@@ -101,3 +101,36 @@ def test_sums_over_many_tokens(case):
     for name, got, want in (("dA", dA[0], 0.75 * (U.t() @ x)), ("dB", dB[0], 0.75 * (dy.t() @ T))):
         off = float((got.double() - want).norm() / want.norm())
         assert off <= 2.0 ** -18, f"{name}: {off * 2 ** 18:.2f} of 2^-18"
+
+
+@pytest.mark.parametrize("n,r,length", [(300, 8, 40008), (300, 64, 22016), (160, 136, 20008), (40, 24, 40008), (3, 200, 20008)])
+def test_sums_over_a_long_dimension(n, r, length):
+    """T over a long K and U over a long N: with many adapters one CTA has the whole sum, with few it is
+    split.  The error's root mean square stays within 2^-18 of the result's."""
+    m, short = 2 * n, 64
+    g = torch.Generator(device="cuda").manual_seed(n + r)
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    V, W = normal(m, length), normal(n, r, length)
+    idx = torch.arange(m, dtype=torch.int32, device="cuda") % n
+    groups = bd.adapter_groups(idx, n)
+    ones = torch.ones(n, device="cuda")
+    want = torch.stack([W[a].double() @ V[t].double() for t, a in enumerate(idx.tolist())])  # [m, r]
+
+    def hold(name, got, ref):
+        off = float((got.double() - ref).norm() / ref.norm())
+        assert off <= 2.0 ** -18, f"{name}: {off * 2 ** 18:.2f} of 2^-18"
+
+    ws = bd.new_workspace(bd.workspace_bytes_adapters(m, short, length, r, True))
+    B = torch.zeros(n, short, r, dtype=torch.bfloat16, device="cuda")
+    T = bd.adapters_fwd(bd.AdapterPool(W, B, ones), groups, V, torch.zeros(m, short, device="cuda"), save_t=True, ws=ws)
+    hold("T", T.double().sum(0), want)
+    # U = dY B with B = W^T; A has a one in each row, so dX holds U
+    A = torch.zeros(n, r, 256, dtype=torch.bfloat16, device="cuda")
+    A[:, torch.arange(r), torch.arange(r)] = 1.0
+    pool = bd.AdapterPool(A, W.transpose(1, 2).contiguous(), ones)
+    X = torch.zeros(m, 256, dtype=torch.bfloat16, device="cuda")
+    for grads in (False, True):  # U alone, and beside T
+        dX = torch.zeros(m, 256, device="cuda")
+        bd.adapters_bwd(pool, groups, X, V, dX=dX, need_grads=grads, grad_dtype=torch.bfloat16, ws=ws)
+        hold("U", dX[:, :r], want)
+    assert bd.read_status(ws) == 0
