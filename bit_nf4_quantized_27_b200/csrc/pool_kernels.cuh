@@ -501,6 +501,11 @@ struct PoolDownArgs {
   PoolDownLayout l;
 };
 
+// What plane h leaves of x.  An infinity is all in the first plane: inf - inf would make the others, and so every result, NaN.
+__device__ __forceinline__ float pool_rest(float x, float h, bool first) {
+  return first && fabsf(h) == __int_as_float(0x7f800000) ? 0.0f : x - h;
+}
+
 // kSums: T, U, or both (found at run time, they cost a call with one token 0.9 us of 12.8).
 enum PoolSums { kPoolT, kPoolU, kPoolBoth };
 // kFold: a CTA may have more than kPoolDownFold steps.
@@ -684,10 +689,10 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_down_kernel(const __grid
 #pragma unroll
         for (int pl = 0; pl < kPoolPlanes; ++pl) {
           const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-          x.x -= bf16lo_to_f32(h.x);
-          x.y -= bf16hi_to_f32(h.x);
-          x.z -= bf16lo_to_f32(h.y);
-          x.w -= bf16hi_to_f32(h.y);
+          x.x = pool_rest(x.x, bf16lo_to_f32(h.x), pl == 0);
+          x.y = pool_rest(x.y, bf16hi_to_f32(h.x), pl == 0);
+          x.z = pool_rest(x.z, bf16lo_to_f32(h.y), pl == 0);
+          x.w = pool_rest(x.w, bf16hi_to_f32(h.y), pl == 0);
           *reinterpret_cast<uint2 *>(out + pl * p.M * p.r) = h;
         }
       }

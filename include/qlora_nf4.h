@@ -348,8 +348,13 @@ QLORA_API size_t qlora_workspace_bytes_adapters(int64_t M, int64_t N, int64_t K,
  *   T_save  nullable bf16 [3, M, r], 16-byte aligned: receives T[t] = X[t] A_a^T for
  *       the backward pass as three planes, each the bf16 rounding of what the ones
  *       before leave, so that their sum carries 24 bits (columns past the adapter's
- *       rank as zeros; rows of tokens without an adapter are not written)
- * K and N multiples of 8, 0 <= M < 2^29.  An entry of order outside [0, M) is
+ *       rank as zeros; rows of tokens without an adapter are not written); an
+ *       infinity stands in the first plane alone, as does what bf16 rounds to one
+ * K and N multiples of 8, 0 <= M < 2^29.  NaN and infinities stay with their token
+ * (and, in dA and dB, with its adapter).  An infinite T or U gives the definition's
+ * infinities; an infinity in B, or in the gradients one in A, X or dY, that meets a
+ * finite T or U may give NaN in its place, as that is multiplied in parts of either sign.
+ * An entry of order outside [0, M) is
  * skipped (the backward's dA and dB are then unspecified), and, like a rank that is
  * not a multiple of 8 in [0, r] (rounded down and clamped), sets
  * QLORA_ERR_INVALID_ARGUMENT in the status word. */

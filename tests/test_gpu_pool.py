@@ -519,3 +519,44 @@ def test_a_given_stream_without_a_workspace():
         for a, b in zip(want, got):
             same = torch.equal(a[:, rows], b[:, rows]) if a.dim() == 3 and a.shape[:2] == (3, m) else torch.equal(a, b)
             assert same
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("r", [24, 64, 136])
+def test_an_infinite_intermediate_is_the_definitions(r, dt):
+    """T or U of a token is infinite: its rows of Y and dX, and all that its adapter's gradients make
+    of it, are infinite or NaN where the definition's are, with the same signs."""
+    m, n_out, k, n = 70, 136, 200, 2
+    idx, A, B, scales, X, dY = _setup(m, n_out, k, r, n, 160, none=0.0)
+    t, u = (idx == 0).nonzero().view(-1)[:2].tolist()
+    at_k, at_n = 5, 9
+    sign = torch.where(torch.rand(r, generator=torch.Generator().manual_seed(r)) < 0.5, -1.0, 1.0).to(torch.bfloat16)
+    third = n_out // 3  # sums of infinities of one sign, of the other, and of both
+    B[0, :third], B[0, third : 2 * third] = B[0, :third].abs() * sign, -B[0, third : 2 * third].abs() * sign
+    A[0, :, : k // 2] = A[0, :, : k // 2].abs() * sign[:, None]
+    X[t, at_k], dY[u, at_n] = float("inf"), float("-inf")
+    pool, groups = _pool(A, B, scales, None), bd.adapter_groups(idx.cuda(), n)
+    Y, dX = torch.zeros(m, n_out, dtype=DT[dt], device="cuda"), torch.zeros(m, k, dtype=DT[dt], device="cuda")
+    T = bd.adapters_fwd(pool, groups, X.cuda(), Y, save_t=True)
+    dA, dB = bd.adapters_bwd(pool, groups, X.cuda(), dY.cuda(), T, dX=dX, grad_dtype=DT[dt])
+    x, dy, a, b = X.double(), dY.double(), A.double(), B.double()
+    s, own = scales.double(), idx == 0
+    wT = torch.stack([x[i] @ a[idx[i]].t() for i in range(m)])
+    wU = torch.stack([dy[i] @ b[idx[i]] for i in range(m)])
+    wY = torch.stack([s[idx[i]] * (b[idx[i]] @ wT[i]) for i in range(m)])
+    wX = torch.stack([s[idx[i]] * (wU[i] @ a[idx[i]]) for i in range(m)])
+    wA, wB = s[0] * (wU[own].t() @ x[own]), s[0] * (dy[own].t() @ wT[own])
+
+    def same(got, want):
+        got = got.double().cpu()
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+        assert torch.equal(got[want.isinf()], want[want.isinf()])
+
+    assert wT[t].isinf().all() and wU[u].isinf().all() and wY[t].isinf().sum() >= n_out // 4 and wX[u].isinf().any()
+    same(T[0], wT), same(Y, wY), same(dX, wX)
+    assert not T[1:, t].any()
+    # where the infinity itself meets the other, finite intermediate, NaN may stand for it
+    keep_k, keep_n = torch.arange(k) != at_k, torch.arange(n_out) != at_n
+    same(dA[0][:, keep_k.cuda()], wA[:, keep_k]), same(dB[0][keep_n.cuda()], wB[keep_n])
+    assert not dA[0][:, at_k].isfinite().any() and not dB[0][at_n].isfinite().any()
+    assert wA[:, keep_k].isinf().any() and wB[keep_n].isinf().any()
