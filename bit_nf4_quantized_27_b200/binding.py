@@ -695,12 +695,16 @@ def grad_norm(tensors: TensorList, max_norm: float, out: torch.Tensor | None = N
 
 
 def adamw_multi(tensors: TensorList, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-                weight_decay: float = 0.0, clip: torch.Tensor | None = None, seed: int = 0, stream=None) -> None:
+                weight_decay: float = 0.0, clip: torch.Tensor | None = None, seed: int | None = None, stream=None) -> None:
     """One AdamW step in place on every tensor of the list.  clip: what grad_norm returned
-    (gradients are multiplied by clip[1]; NaN there leaves everything as it is).  seed:
-    random bits of the 8-bit states' rounding, another one for each step."""
+    (gradients are multiplied by clip[1]; NaN there leaves everything as it is).  seed: the
+    random bits of the 8-bit states' rounding, by default of the step; with the same ones at
+    every step each element would always be rounded by the same threshold, and a
+    slowly changing variance would not move.  A call captured into a graph keeps its step and
+    seed."""
     assert clip is None or (clip.dtype == torch.float32 and clip.is_contiguous() and clip.numel() == 2)
     _here(tensors.table, clip)
     hp = AdamWC(lr, beta1, beta2, eps, weight_decay)
-    _check(lib().qlora_adamw_multi(tensors._ref, ctypes.byref(hp), step, _ptr(clip), seed & 0xffffffff,
+    _check(lib().qlora_adamw_multi(tensors._ref, ctypes.byref(hp), step, _ptr(clip),
+                                   (step if seed is None else seed) & 0xffffffff,
                                    _stream(stream)), "qlora_adamw_multi")

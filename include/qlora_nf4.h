@@ -453,7 +453,9 @@ QLORA_API qlora_status qlora_grad_norm(const qlora_tensor_list *list, float max_
  *       by norm_and_clip[1]; where that is NaN the step changes nothing
  *   seed  8-bit states are rounded stochastically: the random bits are a hash of
  *       (seed, place in the list, element), so a step is reproducible; give each
- *       step another seed
+ *       step another seed, or an element meets the same threshold at every step and a
+ *       slowly changing variance stays where it is (a captured call keeps its seed, as
+ *       it keeps its step)
  * The parameters see the new states before they are rounded to 8 bits, and with
  * those take the update's root and quotient to a few 2^-23 of the update (an eps
  * below 2^-126 counts as 2^-126).  A variance that is not zero is never rounded to
