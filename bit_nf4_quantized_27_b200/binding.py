@@ -577,34 +577,40 @@ def linear_fwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, y_dtype=torch.bf
 
 @_on_its_stream
 def linear_bwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, dY, T=None, dx_dtype=torch.bfloat16,
-                    grad_dtype=torch.bfloat16, ws: torch.Tensor | None = None, outs=None, stream=None):
-    """Returns (dX, dA [n, r, K], dB [n, N, r]) for upstream gradient dY."""
+                    grad_dtype=torch.bfloat16, ws: torch.Tensor | None = None, outs=None, stream=None,
+                    need_grads: bool = True):
+    """Returns (dX, dA [n, r, K], dB [n, N, r]) for upstream gradient dY, or (dX, None, None)
+    without need_grads.  (dA and dB without dX, and so without the base product, are
+    adapters_bwd's.)"""
     M = X.shape[0]
     assert X.dtype == torch.bfloat16 and X.is_contiguous() and X.shape[1] == q.cols == pool.cols and pool.rows == q.rows
     assert dY.dtype == torch.bfloat16 and dY.is_contiguous() and tuple(dY.shape) == (M, q.rows)
     assert T is None or (T.dtype == torch.bfloat16 and T.is_contiguous() and T.numel() == 3 * M * pool.r)
     dX = outs[0] if outs is not None else torch.empty(M, q.cols, dtype=dx_dtype, device=X.device)
     assert dX.is_contiguous() and tuple(dX.shape) == (M, q.cols)
-    dA, dB = _pool_grads(pool, grad_dtype, None if outs is None else outs[1:], X.device)
+    dA, dB = _pool_grads(pool, grad_dtype, None if outs is None else outs[1:], X.device) if need_grads else (None, None)
     order, offsets = _group_ptrs(groups, pool, M)
     _here(X, dY, T, dX, dA, dB, ws, pool.A, q.codes, *groups)
     if ws is None:
         ws = new_workspace(workspace_bytes_adapters(M, q.rows, q.cols, pool.r, True), X.device)
     t = q.c_struct()
     _check(lib().qlora_linear_bwd_pool(ctypes.byref(t), pool._ref, order, offsets, _ptr(X), _ptr(dY), M,
-                                       _ptr(T), _ptr(dX), _dtype_code(dX.dtype), _ptr(dA), _ptr(dB), _dtype_code(dA.dtype),
-                                       _ptr(ws), ws.numel(), _stream(stream)), "qlora_linear_bwd_pool")
+                                       _ptr(T), _ptr(dX), _dtype_code(dX.dtype), _ptr(dA), _ptr(dB),
+                                       QLORA_F32 if dA is None else _dtype_code(dA.dtype), _ptr(ws), ws.numel(),
+                                       _stream(stream)), "qlora_linear_bwd_pool")
     return dX, dA, dB
 
 
 class QLoRAPoolLinearFunction(torch.autograd.Function):
     """Autograd wrapper of the NF4 layer with a pool: X, A [n, r, K] and B [n, N, r] get
-    gradients; groups, scales and ranks are the batch's and the pool's constants."""
+    gradients, those of them that require one; groups, scales and ranks are the batch's and
+    the pool's constants."""
 
     @staticmethod
     def forward(ctx, X, A, B, q: NF4Weight, groups, scales, ranks=None):
         X = X.contiguous()
-        Y, T = linear_fwd_pool(q, AdapterPool(A, B, scales, ranks), groups, X)
+        grads = any(ctx.needs_input_grad[1:3])  # T is for them alone
+        Y, T = linear_fwd_pool(q, AdapterPool(A, B, scales, ranks), groups, X, save_t=grads)
         ctx.save_for_backward(X, A, B, T, scales, *groups, *([] if ranks is None else [ranks]))
         ctx.q = q
         return Y
@@ -613,8 +619,14 @@ class QLoRAPoolLinearFunction(torch.autograd.Function):
     def backward(ctx, dY):
         X, A, B, T, scales, order, offsets, *ranks = ctx.saved_tensors
         pool = AdapterPool(A, B, scales, ranks[0] if ranks else None)
-        dX, dA, dB = linear_bwd_pool(ctx.q, pool, (order, offsets), X, dY.contiguous().to(torch.bfloat16), T)
-        return dX, dA, dB, None, None, None, None
+        groups, dY = (order, offsets), dY.contiguous().to(torch.bfloat16)
+        need_x, need_a, need_b = ctx.needs_input_grad[:3]
+        dX = None
+        if need_x:
+            dX, dA, dB = linear_bwd_pool(ctx.q, pool, groups, X, dY, T, need_grads=need_a or need_b)
+        else:
+            dA, dB = adapters_bwd(pool, groups, X, dY, T, grad_dtype=torch.bfloat16)
+        return dX, dA if need_a else None, dB if need_b else None, None, None, None, None
 
 
 # ---------------------------------------------------------------------------

@@ -1452,7 +1452,7 @@ qlora_status qlora_linear_bwd_pool(const qlora_nf4_tensor *W, const qlora_adapte
   qlora_status s = check_nf4(W);
   if (s != QLORA_OK) return s;
   const int64_t N = W->rows, K = W->cols;
-  if (M < 1 || !dY || !dX || !dA || !dB || !valid_dtype(dx_dtype) || !valid_dtype(grad_dtype))
+  if (M < 1 || !dY || !dX || (!dA) != (!dB) || !valid_dtype(dx_dtype) || !valid_dtype(grad_dtype))
     return QLORA_ERR_INVALID_ARGUMENT;
   if ((s = check_pool_call(pool, order, offsets, X, K, M, N, K, ws)) != QLORA_OK) return s;
   if (!aligned(dY, 16) || !aligned(dX, 16) || !aligned(T_saved, 16) || !aligned(dA, 16) || !aligned(dB, 16))

@@ -382,7 +382,7 @@ QLORA_API qlora_status qlora_adapters_bwd(const qlora_adapter_pool *pool, const 
  * into Y (a bf16 Y is thus rounded twice: after the base product and after the
  * adapters' term); and dX = dY W', then qlora_adapters_bwd into dX.  Arguments as
  * qlora_linear_fwd / qlora_linear_bwd with the pool and the groups for the adapter
- * (dX, dA and dB all required); M >= 1, W->rows a multiple of 8, contiguous rows.
+ * (dX required; dA and dB nullable, both or neither); M >= 1, W->rows a multiple of 8, contiguous rows.
  * ws as for qlora_adapters_fwd / qlora_adapters_bwd. */
 QLORA_API qlora_status qlora_linear_fwd_pool(const qlora_nf4_tensor *W, const qlora_adapter_pool *pool,
                                              const int32_t *order, const int32_t *offsets, const void *X, int64_t M,

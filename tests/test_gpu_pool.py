@@ -560,3 +560,21 @@ def test_an_infinite_intermediate_is_the_definitions(r, dt):
     same(dA[0][:, keep_k.cuda()], wA[:, keep_k]), same(dB[0][keep_n.cuda()], wB[keep_n])
     assert not dA[0][:, at_k].isfinite().any() and not dB[0][at_n].isfinite().any()
     assert wA[:, keep_k].isinf().any() and wB[keep_n].isinf().any()
+
+
+@pytest.mark.parametrize("need", [(True, False, False), (False, True, False), (False, False, True), (True, True, False), (True, True, True)])
+def test_autograd_of_some_of_the_inputs(need):
+    """The gradients asked for have the bits of all of them together."""
+    m, n_out, k, r, n = 150, 136, 320, 24, 3
+    idx, A, B, scales, X, dY = _setup(m, n_out, k, r, n, 170)
+    q = bd.quantize(I.normal((n_out, k), 0.02, 12).cuda())
+    groups = bd.adapter_groups(idx.cuda(), n)
+    pool = _pool(A, B, scales, None)
+    Y, T = bd.linear_fwd_pool(q, pool, groups, X.cuda())
+    want = bd.linear_bwd_pool(q, pool, groups, X.cuda(), dY.cuda(), T)
+    leaves = [t.cuda().requires_grad_(x) for t, x in zip((X, A, B), need)]
+    got = bd.QLoRAPoolLinearFunction.apply(*leaves, q, groups, scales.cuda(), None)
+    assert torch.equal(got, Y)
+    got.backward(dY.cuda())
+    for leaf, w, x in zip(leaves, want, need):
+        assert torch.equal(leaf.grad, w) if x else leaf.grad is None
