@@ -604,15 +604,17 @@ def linear_bwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, dY, T=None, dx_d
 class QLoRAPoolLinearFunction(torch.autograd.Function):
     """Autograd wrapper of the NF4 layer with a pool: X, A [n, r, K] and B [n, N, r] get
     gradients, those of them that require one; groups, scales and ranks are the batch's and
-    the pool's constants."""
+    the pool's constants.  ws: a workspace of the backward's size, which both
+    directions then use; its status word (read_status) tells of a bad group, a bad rank or a wait
+    that ran out, and without one nothing does."""
 
     @staticmethod
-    def forward(ctx, X, A, B, q: NF4Weight, groups, scales, ranks=None):
+    def forward(ctx, X, A, B, q: NF4Weight, groups, scales, ranks=None, ws: torch.Tensor | None = None):
         X = X.contiguous()
         grads = any(ctx.needs_input_grad[1:3])  # T is for them alone
-        Y, T = linear_fwd_pool(q, AdapterPool(A, B, scales, ranks), groups, X, save_t=grads)
+        Y, T = linear_fwd_pool(q, AdapterPool(A, B, scales, ranks), groups, X, save_t=grads, ws=ws)
         ctx.save_for_backward(X, A, B, T, scales, *groups, *([] if ranks is None else [ranks]))
-        ctx.q = q
+        ctx.q, ctx.ws = q, ws
         return Y
 
     @staticmethod
@@ -623,10 +625,10 @@ class QLoRAPoolLinearFunction(torch.autograd.Function):
         need_x, need_a, need_b = ctx.needs_input_grad[:3]
         dX = None
         if need_x:
-            dX, dA, dB = linear_bwd_pool(ctx.q, pool, groups, X, dY, T, need_grads=need_a or need_b)
+            dX, dA, dB = linear_bwd_pool(ctx.q, pool, groups, X, dY, T, need_grads=need_a or need_b, ws=ctx.ws)
         else:
-            dA, dB = adapters_bwd(pool, groups, X, dY, T, grad_dtype=torch.bfloat16)
-        return dX, dA if need_a else None, dB if need_b else None, None, None, None, None
+            dA, dB = adapters_bwd(pool, groups, X, dY, T, grad_dtype=torch.bfloat16, ws=ctx.ws)
+        return dX, dA if need_a else None, dB if need_b else None, None, None, None, None, None
 
 
 # ---------------------------------------------------------------------------

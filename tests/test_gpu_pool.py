@@ -578,3 +578,21 @@ def test_autograd_of_some_of_the_inputs(need):
     got.backward(dY.cuda())
     for leaf, w, x in zip(leaves, want, need):
         assert torch.equal(leaf.grad, w) if x else leaf.grad is None
+
+
+def test_autograd_reports_through_the_callers_workspace():
+    m, n_out, k, r, n = 40, 64, 128, 16, 2
+    idx, A, B, scales, X, dY = _setup(m, n_out, k, r, n, 180, none=0.0)
+    q = bd.quantize(I.normal((n_out, k), 0.02, 13).cuda())
+    ws = bd.new_workspace(bd.workspace_bytes_adapters(m, n_out, k, r, True))
+    order, offsets = bd.adapter_groups(idx.cuda(), n, ws=ws)
+    for bad in (False, True):
+        if bad:
+            order = order.clone()
+            order[3] = m + 7
+        leaves = [t.cuda().requires_grad_() for t in (X, A, B)]
+        Y = bd.QLoRAPoolLinearFunction.apply(*leaves, q, (order, offsets), scales.cuda(), None, ws)
+        assert bd.read_status(ws) == (1 if bad else 0)
+        bd.clear_status(ws)
+        Y.backward(dY.cuda())
+        assert bd.read_status(ws) == (1 if bad else 0)

@@ -60,3 +60,10 @@ def test_only_the_gradients_that_are_required_are_computed(calls, need):
     assert calls == want
     for g, n, value in zip(got, need, (1, 2, 3)):
         assert (g is not None and bool((g == value).all())) if n else g is None
+
+
+@pytest.mark.parametrize("need_x", [False, True])
+def test_both_directions_use_the_callers_workspace(calls, need_x):
+    ws = _z(256, dt=torch.uint8)
+    _run((need_x, True, True), None, ws)
+    assert len(calls) == 2 and all(c[-1] is ws for c in calls)
