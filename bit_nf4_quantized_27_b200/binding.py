@@ -14,6 +14,7 @@ import os
 import re
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqlora_nf4.so")
@@ -330,6 +331,7 @@ class QLoRALinearFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, A, B, T = ctx.saved_tensors
         dX, dA, dB = linear_bwd(ctx.q, A, B, ctx.alpha, X, dY.contiguous().to(torch.bfloat16), T)
@@ -618,6 +620,7 @@ class QLoRAPoolLinearFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, A, B, T, scales, order, offsets, *ranks = ctx.saved_tensors
         pool = AdapterPool(A, B, scales, ranks[0] if ranks else None)

@@ -67,3 +67,20 @@ def test_both_directions_use_the_callers_workspace(calls, need_x):
     ws = _z(256, dt=torch.uint8)
     _run((need_x, True, True), None, ws)
     assert len(calls) == 2 and all(c[-1] is ws for c in calls)
+
+
+@pytest.mark.parametrize("layer", ["one adapter", "pool"])
+def test_a_second_derivative_is_refused(calls, monkeypatch, layer):
+    """The gradients come from kernels that autograd does not see: differentiating them would
+    leave out everything behind them."""
+    X = _z(M, K).requires_grad_()
+    if layer == "pool":
+        groups = _z(M, dt=torch.int32), _z(S + 1, dt=torch.int32)
+        Y = bd.QLoRAPoolLinearFunction.apply(X, _z(S, R, K), _z(S, N, R), Q, groups, _z(S, dt=torch.float32))
+    else:
+        monkeypatch.setattr(bd, "linear_fwd", lambda *a: (_z(M, N), _z(2, M, R)))
+        monkeypatch.setattr(bd, "linear_bwd", lambda *a: (_z(M, K) + 1, _z(R, K), _z(N, R)))
+        Y = bd.QLoRALinearFunction.apply(X, _z(R, K), _z(N, R), Q, 1.0)
+    dX, = torch.autograd.grad((Y * Y).sum(), X, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (dX * X).sum().backward()
