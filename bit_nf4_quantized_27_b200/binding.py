@@ -432,12 +432,19 @@ def linear_bwd_dropout(q: NF4Weight, A, B, alpha: float, X, dY, keep: torch.Tens
 # ---------------------------------------------------------------------------
 def _here(*tensors):
     """The operands of a call lie on the current device, where its kernels run."""
-    if not torch.cuda.is_initialized():
-        torch.cuda.init()
     dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:  # -1 for a tensor on the CPU
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+_increment_version = torch._C._increment_version  # torch.autograd.graph.increment_version without its own checks
+
+
+def _wrote(*tensors):
+    """The call has written these tensors of the caller's.  Autograd learns of it, so that a backward
+    whose forward read what stood there before raises, as after any operation in place."""
+    _increment_version([t for t in tensors if t is not None])
 
 
 class AdapterPool:
@@ -484,8 +491,10 @@ def adapter_groups(adapter_of_token: torch.Tensor, n: int, out=None, ws: torch.T
     _here(idx, order, offsets, ws)
     if ws is None:
         ws = new_workspace(STATUS_BYTES, idx.device)
-    _check(lib().qlora_adapter_groups(_ptr(idx), M, n, _ptr(order), _ptr(offsets), _ptr(ws), _stream(stream)),
+    _check(lib().qlora_adapter_groups(idx.data_ptr(), M, n, order.data_ptr(), offsets.data_ptr(), ws.data_ptr(), _stream(stream)),
            "qlora_adapter_groups")
+    if out is not None:
+        _wrote(order, offsets)
     return order, offsets
 
 
@@ -493,7 +502,7 @@ def _group_ptrs(groups, pool: AdapterPool, m: int):
     order, offsets = groups
     assert order.dtype == offsets.dtype == torch.int32 and order.is_contiguous() and offsets.is_contiguous()
     assert order.numel() == m and offsets.numel() == pool.n + 1
-    return _ptr(order), _ptr(offsets)
+    return order.data_ptr(), offsets.data_ptr()
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -509,17 +518,18 @@ def adapters_fwd(pool: AdapterPool, groups, X: torch.Tensor, Y: torch.Tensor, sa
     """Adds every token's adapter term to Y in place: Y[t] += s_a (X[t] A_a^T) B_a^T.
     groups: (order, offsets) of adapter_groups.  X and Y may be column slices of wider
     tensors.  Returns T, the bf16 [3, M, r] planes whose sum is X A^T, or None."""
-    M = X.shape[0]
-    assert X.dtype == torch.bfloat16 and X.shape[1] == pool.cols and tuple(Y.shape) == (M, pool.rows)
+    M, cols = X.shape
+    assert X.dtype == torch.bfloat16 and cols == pool.cols and Y.shape == (M, pool.rows)
     order, offsets = _group_ptrs(groups, pool, M)
     T = t_out if t_out is not None else (torch.empty(3, M, pool.r, dtype=torch.bfloat16, device=X.device) if save_t else None)
     assert T is None or (T.dtype == torch.bfloat16 and T.is_contiguous() and T.numel() == 3 * M * pool.r)
     _here(X, Y, T, ws, pool.A, *groups)
     if ws is None:
         ws = new_workspace(workspace_bytes_adapters(M, pool.rows, pool.cols, pool.r, False), X.device)
-    _check(lib().qlora_adapters_fwd(pool._ref, order, offsets, _ptr(X), _row_stride(X), M, pool.rows,
-                                    pool.cols, _ptr(Y), _row_stride(Y), _dtype_code(Y.dtype), _ptr(T), _ptr(ws),
+    _check(lib().qlora_adapters_fwd(pool._ref, order, offsets, X.data_ptr(), _row_stride(X), M, pool.rows,
+                                    pool.cols, Y.data_ptr(), _row_stride(Y), _dtype_code(Y.dtype), _ptr(T), ws.data_ptr(),
                                     ws.numel(), _stream(stream)), "qlora_adapters_fwd")
+    _wrote(Y, t_out)
     return T
 
 
@@ -540,19 +550,20 @@ def adapters_bwd(pool: AdapterPool, groups, X: torch.Tensor, dY: torch.Tensor, T
     returns (dA [n, r, K], dB [n, N, r]), or (None, None) without need_grads."""
     M = X.shape[0]
     assert X.dtype == torch.bfloat16 and X.shape[1] == pool.cols
-    assert dY.dtype == torch.bfloat16 and tuple(dY.shape) == (M, pool.rows)
-    assert dX is None or tuple(dX.shape) == (M, pool.cols)
+    assert dY.dtype == torch.bfloat16 and dY.shape == (M, pool.rows)
+    assert dX is None or dX.shape == (M, pool.cols)
     assert T is None or (T.dtype == torch.bfloat16 and T.is_contiguous() and T.numel() == 3 * M * pool.r)
     order, offsets = _group_ptrs(groups, pool, M)
     dA, dB = _pool_grads(pool, grad_dtype, outs, X.device) if need_grads else (None, None)
     _here(X, dY, T, dX, dA, dB, ws, pool.A, *groups)
     if ws is None:
         ws = new_workspace(workspace_bytes_adapters(M, pool.rows, pool.cols, pool.r, True), X.device)
-    _check(lib().qlora_adapters_bwd(pool._ref, order, offsets, _ptr(X), _row_stride(X), _ptr(dY),
+    _check(lib().qlora_adapters_bwd(pool._ref, order, offsets, X.data_ptr(), _row_stride(X), dY.data_ptr(),
                                     _row_stride(dY), M, pool.rows, pool.cols, _ptr(T), _ptr(dX),
                                     0 if dX is None else _row_stride(dX), QLORA_F32 if dX is None else _dtype_code(dX.dtype),
                                     _ptr(dA), _ptr(dB), QLORA_F32 if dA is None else _dtype_code(dA.dtype), _ptr(ws),
                                     ws.numel(), _stream(stream)), "qlora_adapters_bwd")
+    _wrote(dX, *(outs or ()))
     return dA, dB
 
 
@@ -574,6 +585,8 @@ def linear_fwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, y_dtype=torch.bf
     _check(lib().qlora_linear_fwd_pool(ctypes.byref(t), pool._ref, order, offsets, _ptr(X), M, _ptr(Y),
                                        _dtype_code(Y.dtype), _ptr(T), _ptr(ws), ws.numel(), _stream(stream)),
            "qlora_linear_fwd_pool")
+    if out is not None or t_out is not None:
+        _wrote(out, t_out)
     return Y, T
 
 
@@ -600,6 +613,8 @@ def linear_bwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, dY, T=None, dx_d
                                        _ptr(T), _ptr(dX), _dtype_code(dX.dtype), _ptr(dA), _ptr(dB),
                                        QLORA_F32 if dA is None else _dtype_code(dA.dtype), _ptr(ws), ws.numel(),
                                        _stream(stream)), "qlora_linear_bwd_pool")
+    if outs is not None:
+        _wrote(*outs)
     return dX, dA, dB
 
 
@@ -685,6 +700,9 @@ class TensorList:
         _check(lib().qlora_tensor_list_init(arr, count, _dtype_code(gdt), bits, _ptr(self.table), nbytes,
                                             ctypes.byref(self._c), _stream(stream)), "qlora_tensor_list_init")
         self._keep = columns
+        # what adamw_multi writes and a graph may have saved; views of one tensor share its version
+        written = [t if t._base is None else t._base for c in (params, p_bf16) if bits and c is not None for t in c]
+        self._written = list({id(t): t for t in written}.values())
         self.state_bits = bits
         self._ref = ctypes.byref(self._c)
 
@@ -700,15 +718,16 @@ def workspace_bytes_grad_norm() -> int:
 def grad_norm(tensors: TensorList, max_norm: float, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """float32 [2] on the device: the norm of all gradients and min(1, max_norm / (norm + 1e-6))."""
-    if out is None:
-        out = torch.empty(2, dtype=torch.float32, device=tensors.table.device)
-    assert out.dtype == torch.float32 and out.is_contiguous() and out.numel() == 2
-    _here(tensors.table, out, ws)
+    result = torch.empty(2, dtype=torch.float32, device=tensors.table.device) if out is None else out
+    assert result.dtype == torch.float32 and result.is_contiguous() and result.numel() == 2
+    _here(tensors.table, result, ws)
     if ws is None:
         ws = new_workspace(workspace_bytes_grad_norm(), tensors.table.device)
-    _check(lib().qlora_grad_norm(tensors._ref, float(max_norm), _ptr(out), _ptr(ws), ws.numel(),
+    _check(lib().qlora_grad_norm(tensors._ref, float(max_norm), result.data_ptr(), ws.data_ptr(), ws.numel(),
                                  _stream(stream)), "qlora_grad_norm")
-    return out
+    if out is not None:
+        _wrote(out)
+    return result
 
 
 def adamw_multi(tensors: TensorList, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -725,3 +744,4 @@ def adamw_multi(tensors: TensorList, step: int, lr: float, beta1: float = 0.9, b
     _check(lib().qlora_adamw_multi(tensors._ref, ctypes.byref(hp), step, _ptr(clip),
                                    (step if seed is None else seed) & 0xffffffff,
                                    _stream(stream)), "qlora_adamw_multi")
+    _wrote(*tensors._written)

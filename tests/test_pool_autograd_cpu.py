@@ -84,3 +84,53 @@ def test_a_second_derivative_is_refused(calls, monkeypatch, layer):
     dX, = torch.autograd.grad((Y * Y).sum(), X, create_graph=True)
     with pytest.raises(RuntimeError):
         (dX * X).sum().backward()
+
+
+class _Library:
+    def __getattr__(self, name):
+        return lambda *args: 512 if "bytes" in name else 0
+
+
+@pytest.fixture
+def library(monkeypatch):
+    monkeypatch.setattr(bd, "lib", _Library)
+    monkeypatch.setattr(bd, "_here", lambda *tensors: None)
+    monkeypatch.setattr(bd, "_stream", lambda stream=None: 0)
+
+
+def test_calls_tell_autograd_what_they_wrote(library):
+    """Each tensor of the caller's that a call writes gets a new version, and no other does."""
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    pool = bd.AdapterPool(_z(S, R, K), _z(S, N, R), _z(S, dt=f32))
+    q = types.SimpleNamespace(rows=N, cols=K, codes=_z(N, 32, dt=u8), c_struct=lambda: bd.NF4TensorC())
+    idx, groups, ws = _z(M, dt=i32), (_z(M, dt=i32), _z(S + 1, dt=i32)), _z(1 << 16, dt=u8)
+    X, Y, dY, dX, T = _z(M, K), _z(M, N), _z(M, N), _z(M, K), _z(3, M, R)
+    outs = _z(S, R, K), _z(S, N, R)
+    p, flat, g, m, v = (_z(40, dt=f32) for _ in range(5))
+    p16, clip = _z(40), _z(2, dt=f32)
+    tl = bd.TensorList([g, g[:8]], [p, flat[8:16]], [m, m[:8]], [v, v[:8]], p_bf16=[p16, p16[:8]])
+    read = [idx, X, dY, pool.A, pool.B, pool.scales, g]
+    for call, wrote in [
+            (lambda: bd.adapter_groups(idx, S, out=groups, ws=ws), groups),
+            (lambda: bd.adapters_fwd(pool, groups, X, Y, t_out=T, ws=ws), (Y, T)),
+            (lambda: bd.adapters_bwd(pool, groups, X, dY, T, dX=dX, outs=outs, ws=ws), (dX, *outs)),
+            (lambda: bd.linear_fwd_pool(q, pool, groups, X, out=Y, t_out=T, ws=ws), (Y, T)),
+            (lambda: bd.linear_bwd_pool(q, pool, groups, X, dY, T, outs=(dX, *outs), ws=ws), (dX, *outs)),
+            (lambda: bd.linear_bwd_pool(q, pool, groups, X, dY, T, outs=(dX, None, None), need_grads=False, ws=ws), (dX,)),
+            (lambda: bd.grad_norm(tl, 1.0, out=clip, ws=ws), (clip,)),
+            (lambda: bd.adamw_multi(tl, 1, 1e-3, clip=clip), (p, flat, p16))]:
+        every = [*read, *groups, Y, dX, T, *outs, p, flat, p16, clip]
+        before = [t._version for t in every]
+        call()
+        for t, b in zip(every, before):
+            assert (t._version > b) == any(t is w for w in wrote)
+
+
+def test_groups_written_again_before_the_backward_are_noticed(calls, library):
+    """The backward would take the gradients by the new batch's groups."""
+    idx, groups = _z(M, dt=torch.int32), (_z(M, dt=torch.int32), _z(S + 1, dt=torch.int32))
+    X = _z(M, K).requires_grad_()
+    Y = bd.QLoRAPoolLinearFunction.apply(X, _z(S, R, K), _z(S, N, R), Q, groups, _z(S, dt=torch.float32))
+    bd.adapter_groups(idx, S, out=groups, ws=_z(256, dt=torch.uint8))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        Y.sum().backward()
