@@ -506,10 +506,11 @@ def _group_ptrs(groups, pool: AdapterPool, m: int):
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a [rows, cols] tensor whose rows are contiguous."""
+    """Row stride of a [rows, cols] tensor whose rows are contiguous; that of a single row, which nothing
+    goes by, is its length."""
     (rows, cols), (row, col) = t.shape, t.stride()
     assert cols == 1 or col == 1
-    return row if rows > 1 else max(row, cols)
+    return row if rows > 1 else cols
 
 
 @_on_its_stream

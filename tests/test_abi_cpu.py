@@ -378,3 +378,12 @@ def test_pool_layer_refuses_planes_of_another_size():
             bd.linear_fwd_pool(q, pool, groups, z(5, 64), t_out=planes)
         with pytest.raises(AssertionError):
             bd.linear_bwd_pool(q, pool, groups, z(5, 64), z(5, 16), planes)
+
+
+def test_the_stride_of_a_single_row_is_its_length():
+    """One token may be a row of a tensor of any width: there is no next row."""
+    import torch
+
+    wide = torch.zeros(5, 100)
+    assert bd._row_stride(wide[:, :64]) == 100 and bd._row_stride(wide[3:4, :64]) == 64
+    assert bd._row_stride(wide[3:3, :64]) == 64 and bd._row_stride(wide.t()[:1, :1]) == 1

@@ -596,3 +596,18 @@ def test_autograd_reports_through_the_callers_workspace():
         bd.clear_status(ws)
         Y.backward(dY.cuda())
         assert bd.read_status(ws) == (1 if bad else 0)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_one_token_in_a_tensor_of_any_width(dt):
+    n_out, k, r, n = 136, 200, 24, 2
+    _, A, B, scales, X, dY = _setup(1, n_out, k, r, n, 190, none=0.0)
+    pool, groups = _pool(A, B, scales, None), bd.adapter_groups(torch.tensor([1], dtype=torch.int32, device="cuda"), n)
+    Y, dX = torch.ones(1, n_out, dtype=DT[dt], device="cuda"), torch.ones(1, k, dtype=DT[dt], device="cuda")
+    row = lambda t, pad: torch.zeros(2, t.shape[1] + pad, dtype=t.dtype, device="cuda")[:1, : t.shape[1]].copy_(t)  # noqa: E731
+    vX, vdY, vY, vdX = row(X, 4), row(dY, 1), row(Y, 3), row(dX, 5)
+    bd.adapters_fwd(pool, groups, X.cuda(), Y)
+    want = bd.adapters_bwd(pool, groups, X.cuda(), dY.cuda(), dX=dX)
+    bd.adapters_fwd(pool, groups, vX, vY)
+    got = bd.adapters_bwd(pool, groups, vX, vdY, dX=vdX)
+    assert torch.equal(vY, Y) and torch.equal(vdX, dX) and all(torch.equal(a, b) for a, b in zip(got, want))
