@@ -282,6 +282,7 @@ def linear_bwd(q: NF4Weight, A, B, alpha: float, X, dY, T=None, dx_dtype=torch.b
     """Returns (dX, dA, dB) for upstream gradient dY."""
     M = X.shape[0]
     r = A.shape[0]
+    assert X.dtype == torch.bfloat16 and X.is_contiguous() and X.shape[1] == q.cols
     assert dY.dtype == torch.bfloat16 and dY.is_contiguous() and dY.shape == (M, q.rows)
     if outs is not None:
         dX, dA, dB = outs
@@ -325,7 +326,8 @@ class QLoRALinearFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, A, B, q: NF4Weight, alpha: float):
-        Y, T = linear_fwd(q, A, B, alpha, X.contiguous())
+        X = X.contiguous()  # the backward reads its rows one behind the other, too
+        Y, T = linear_fwd(q, A, B, alpha, X)
         ctx.save_for_backward(X, A, B, T)
         ctx.q, ctx.alpha = q, alpha
         return Y

@@ -134,3 +134,33 @@ def test_groups_written_again_before_the_backward_are_noticed(calls, library):
     bd.adapter_groups(idx, S, out=groups, ws=_z(256, dt=torch.uint8))
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         Y.sum().backward()
+
+
+@pytest.mark.parametrize("layer", ["one adapter", "pool"])
+def test_the_backward_gets_contiguous_rows(monkeypatch, layer):
+    """The kernels read X's rows one behind the other: a transposed or expanded input is copied for
+    both directions, or the backward would read other rows, or past the last."""
+    seen = []
+    note = lambda X, out: (seen.append((X.is_contiguous(), X.clone())), out)[1]  # noqa: E731
+    x = torch.arange(M * K, dtype=torch.float32).view(K, M).to(torch.bfloat16)
+    X = x.clone().requires_grad_()
+    if layer == "pool":
+        monkeypatch.setattr(bd, "linear_fwd_pool", lambda q, p, g, X, **kw: note(X, (_z(M, N), _z(3, M, R))))
+        monkeypatch.setattr(bd, "linear_bwd_pool", lambda q, p, g, X, *a, **kw: note(X, (_z(M, K), _z(S, R, K), _z(S, N, R))))
+        groups = _z(M, dt=torch.int32), _z(S + 1, dt=torch.int32)
+        Y = bd.QLoRAPoolLinearFunction.apply(X.t(), _z(S, R, K), _z(S, N, R), Q, groups, _z(S, dt=torch.float32))
+    else:
+        monkeypatch.setattr(bd, "linear_fwd", lambda q, A, B, alpha, X: note(X, (_z(M, N), _z(2, M, R))))
+        monkeypatch.setattr(bd, "linear_bwd", lambda q, A, B, alpha, X, *a: note(X, (_z(M, K), _z(R, K), _z(N, R))))
+        Y = bd.QLoRALinearFunction.apply(X.t(), _z(R, K), _z(N, R), Q, 1.0)
+    Y.sum().backward()
+    assert len(seen) == 2 and all(c and torch.equal(v, x.t()) for c, v in seen)
+
+
+def test_the_layers_backward_refuses_strided_rows(library):
+    q = types.SimpleNamespace(rows=N, cols=K, c_struct=lambda: bd.NF4TensorC())
+    ws = _z(1 << 16, dt=torch.uint8)
+    bd.linear_bwd(q, _z(R, K), _z(N, R), 1.0, _z(M, K), _z(M, N), ws=ws)
+    for X in (_z(K, M).t(), _z(1, K).expand(M, K), _z(M, K, dt=torch.float32), _z(M, 2 * K)[:, :K]):
+        with pytest.raises(AssertionError):
+            bd.linear_bwd(q, _z(R, K), _z(N, R), 1.0, X, _z(M, N), ws=ws)
