@@ -371,6 +371,7 @@ def linear_fwd_multi(q: NF4Weight, adapters, adapter_of_token, X, y_dtype=torch.
     (A, B, alpha) of one rank; token t uses adapters[adapter_of_token[t]]."""
     M = X.shape[0]
     r = adapters[0][0].shape[0]
+    assert X.dtype == torch.bfloat16 and X.is_contiguous() and X.shape[1] == q.cols
     Y = out if out is not None else torch.empty(M, q.rows, dtype=y_dtype, device=X.device)
     arr = (LoraC * len(adapters))(*[_lora(a, b, alpha) for a, b, alpha in adapters])
     idx = (ctypes.c_int32 * M)(*[int(i) for i in adapter_of_token])
@@ -398,6 +399,7 @@ def linear_fwd_dropout(q: NF4Weight, A, B, alpha: float, X, keep: torch.Tensor, 
     uint8 [M, K/8] mask.  Returns (Y, T pair or None) as linear_fwd."""
     M, K = X.shape
     r = A.shape[0]
+    assert X.dtype == torch.bfloat16 and X.is_contiguous() and K == q.cols
     assert keep.dtype == torch.uint8 and keep.is_contiguous() and tuple(keep.shape) == (M, K // 8)
     Y = torch.empty(M, q.rows, dtype=y_dtype, device=X.device)
     T = torch.empty(2, M, r, dtype=torch.bfloat16, device=X.device) if save_t else None
@@ -416,6 +418,9 @@ def linear_bwd_dropout(q: NF4Weight, A, B, alpha: float, X, dY, keep: torch.Tens
     """Gradients (dX, dA, dB) of linear_fwd_dropout for upstream dY."""
     M, K = X.shape
     r = A.shape[0]
+    assert X.dtype == torch.bfloat16 and X.is_contiguous() and K == q.cols
+    assert dY.dtype == torch.bfloat16 and dY.is_contiguous() and dY.shape == (M, q.rows)
+    assert keep.dtype == torch.uint8 and keep.is_contiguous() and tuple(keep.shape) == (M, K // 8)
     dX = torch.empty(M, K, dtype=dx_dtype, device=X.device)
     dA = torch.empty(r, K, dtype=grad_dtype, device=X.device)
     dB = torch.empty(q.rows, r, dtype=grad_dtype, device=X.device)

@@ -157,10 +157,18 @@ def test_the_backward_gets_contiguous_rows(monkeypatch, layer):
     assert len(seen) == 2 and all(c and torch.equal(v, x.t()) for c, v in seen)
 
 
-def test_the_layers_backward_refuses_strided_rows(library):
+def test_the_layers_calls_refuse_strided_rows(library):
     q = types.SimpleNamespace(rows=N, cols=K, c_struct=lambda: bd.NF4TensorC())
     ws = _z(1 << 16, dt=torch.uint8)
-    bd.linear_bwd(q, _z(R, K), _z(N, R), 1.0, _z(M, K), _z(M, N), ws=ws)
-    for X in (_z(K, M).t(), _z(1, K).expand(M, K), _z(M, K, dt=torch.float32), _z(M, 2 * K)[:, :K]):
-        with pytest.raises(AssertionError):
-            bd.linear_bwd(q, _z(R, K), _z(N, R), 1.0, X, _z(M, N), ws=ws)
+    A, B, dY, keep = _z(R, K), _z(N, R), _z(M, N), _z(M, K // 8, dt=torch.uint8)
+    calls = [lambda X: bd.linear_bwd(q, A, B, 1.0, X, dY, ws=ws),
+             lambda X: bd.linear_fwd_multi(q, [(A, B, 1.0)], [0] * M, X, ws=ws),
+             lambda X: bd.linear_fwd_dropout(q, A, B, 1.0, X, keep, 0.1, ws=ws),
+             lambda X: bd.linear_bwd_dropout(q, A, B, 1.0, X, dY, keep, 0.1, ws=ws)]
+    for call in calls:
+        call(_z(M, K))
+        for X in (_z(K, M).t(), _z(1, K).expand(M, K), _z(M, K, dt=torch.float32), _z(M, 2 * K)[:, :K]):
+            with pytest.raises(AssertionError):
+                call(X)
+    with pytest.raises(AssertionError):
+        bd.linear_bwd_dropout(q, A, B, 1.0, _z(M, K), _z(N, M).t(), keep, 0.1, ws=ws)
