@@ -523,7 +523,8 @@ def _row_stride(t: torch.Tensor) -> int:
 @_on_its_stream
 def adapters_fwd(pool: AdapterPool, groups, X: torch.Tensor, Y: torch.Tensor, save_t: bool = False, t_out=None,
                  ws: torch.Tensor | None = None, stream=None):
-    """Adds every token's adapter term to Y in place: Y[t] += s_a (X[t] A_a^T) B_a^T.
+    """Adds every token's adapter term to Y in place: Y[t] += s_a (X[t] A_a^T) B_a^T, outside autograd
+    (QLoRAPoolLinearFunction is the layer with gradients).
     groups: (order, offsets) of adapter_groups.  X and Y may be column slices of wider
     tensors.  Returns T, the bf16 [3, M, r] planes whose sum is X A^T, or None."""
     M, cols = X.shape
@@ -578,7 +579,9 @@ def adapters_bwd(pool: AdapterPool, groups, X: torch.Tensor, dY: torch.Tensor, T
 @_on_its_stream
 def linear_fwd_pool(q: NF4Weight, pool: AdapterPool, groups, X, y_dtype=torch.bfloat16, save_t: bool = True,
                     ws: torch.Tensor | None = None, out: torch.Tensor | None = None, t_out=None, stream=None):
-    """Forward of the NF4 layer with every token's own adapter.  Returns (Y, T or None)."""
+    """Forward of the NF4 layer with every token's own adapter, outside autograd.  Returns (Y, T or
+    None).  For a decode step of up to 16 tokens whose adapters the host knows, of one rank,
+    linear_fwd_multi is faster."""
     M = X.shape[0]
     assert X.dtype == torch.bfloat16 and X.is_contiguous() and X.shape[1] == q.cols == pool.cols and pool.rows == q.rows
     Y = out if out is not None else torch.empty(M, q.rows, dtype=y_dtype, device=X.device)

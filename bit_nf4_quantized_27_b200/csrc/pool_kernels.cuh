@@ -135,7 +135,9 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_groups_kernel(const int
 // ---------------------------------------------------------------------------
 // The intermediates T = X A^T and U = dY B are [M, r] in float32 and kept as three bf16 planes [3, M, r], each the rounding
 // of what the ones before leave: 24 bits together, in the type the tensor cores take beside bf16 operands.  A bf16 result
-// is computed from the first two (16 bits), a float32 one from all.
+// is computed from the first two (16 bits), a float32 one from all.  With all three a bf16 result is as far from 64 bits,
+// 1.7e-3 of it by its own rounding, differs from float32 products' in fewer places (1e-5 of the result against 1e-4), and
+// takes longer (48 decode tokens 34.1 us against 30.0, 2039 packed 29.4 against 28.5, 1003 backward 23.1 against 21.8).
 constexpr int kPoolPlanes = 3;
 
 struct PoolArgs {
@@ -1389,8 +1391,9 @@ constexpr int kPoolGradSplitThreads = 192;
 __host__ __device__ constexpr int64_t pool_grad_units(int n, int r, int64_t K, int64_t N) {
   return static_cast<int64_t>(n) * ((r + 63) / 64) * ((K + 127) / 128 + (N + 127) / 128);
 }
-// An adapter's tokens are split over CTAs where units are few, so that CTAs are idle, and tokens many (16 units: 8192
-// tokens 32 us against 90, 2048 17.6 against 30.6, but 256 13.3 against 12.1; 64 units of 512 tokens 22.5 against 16.9).
+// An adapter's tokens are split over CTAs where units are few, so that CTAs are idle, and tokens many (gradients, 16 units:
+// 8192 tokens 32.2 us against 89.1 by pool_grad_kernel, 2048 19.9 against 30.1, 1024 16.8 against 20.4, but 512 15.4 against
+// 15.4 and 256 14.6 against 13.1; 64 units of 512 tokens 24.9 against 17.1, of 1024 27.6 against 26.9).
 __host__ __device__ constexpr bool pool_grad_splits(int64_t units, int64_t M, int n, int sms) {
   return 2 * units < sms && M >= 1024 * static_cast<int64_t>(n);
 }

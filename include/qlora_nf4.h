@@ -341,7 +341,9 @@ QLORA_API qlora_status qlora_adapter_groups(const int32_t *adapter_of_token, int
 QLORA_API size_t qlora_workspace_bytes_adapters(int64_t M, int64_t N, int64_t K, int32_t r, int for_backward);
 
 /* Y[t] += s_a (X[t] A_a^T) B_a^T for every token of order[0 .. offsets[n]); the
- * other rows of Y are not touched.  The sum is formed in float32 and rounded once.
+ * other rows of Y are not touched.  The sum is formed in float32 and rounded once; T,
+ * summed in float32 too, enters it with 24 bits for a float32 Y and with 16 for a bf16 one,
+ * as T and U enter the gradients.
  *   order, offsets  as qlora_adapter_groups writes them: a token at most once
  *   X   bf16 [M, K], row stride ldx (elements, a multiple of 8, >= K), 16-byte aligned
  *   Y   [M, N] of y_dtype, row stride ldy >= N, element aligned; read and written
@@ -458,8 +460,9 @@ QLORA_API qlora_status qlora_grad_norm(const qlora_tensor_list *list, float max_
  *       it keeps its step)
  * The parameters see the new states before they are rounded to 8 bits, and with
  * those take the update's root and quotient to a few 2^-23 of the update (an eps
- * below 2^-126 counts as 2^-126).  A variance that is not zero is never rounded to
- * zero, unless all of its block are below 2^-100: such a block is stored as zeros. */
+ * below 2^-126 counts as 2^-126, a variance below it as zero there).  A variance that is
+ * not zero is never rounded to zero, but a block of either state whose largest
+ * magnitude is below 2^-100 is stored as zeros. */
 QLORA_API qlora_status qlora_adamw_multi(const qlora_tensor_list *list, const qlora_adamw_hparams *hp, int64_t step,
                                          const float *norm_and_clip, uint32_t seed, qlora_stream_t stream);
 
