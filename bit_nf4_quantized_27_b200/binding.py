@@ -450,7 +450,8 @@ _increment_version = torch._C._increment_version  # torch.autograd.graph.increme
 
 def _wrote(*tensors):
     """The call has written these tensors of the caller's.  Autograd learns of it, so that a backward
-    whose forward read what stood there before raises, as after any operation in place."""
+    whose forward read what stood there before raises, as after any operation in place (a graph's
+    replays write without a call, and do not tell)."""
     _increment_version([t for t in tensors if t is not None])
 
 

@@ -449,10 +449,10 @@ __host__ __device__ constexpr uint32_t pool_desc_16(bool mn) { return mn ? 128u 
 // down: g CTAs of a cluster take a tile of 64 tokens (32 above rank 128) and sum a part of the long dimension each,
 // with the accumulator's rows as ranks and its columns as tokens.  The steps of 64 go round four accumulators, which
 // keeps each one's chain of float32 additions short (the tensor cores' additions cut off: one chain over 1400 elements
-// was 3e-6 off, all to one side); after kPoolDownFold steps they are added to the partial sums and start anew.  Each CTA leaves its float32 partial sums in shared memory; each then adds up a share
-// of the tokens over the g CTAs, in CTA order, through distributed shared memory, and writes the planes: no partial
-// planes in HBM, no further launch, and the same bits every time.  g, a divisor of the cluster, follows on the device
-// from the number of tiles.
+// was 3e-6 off, all to one side); after kPoolDownFold steps they are added to the partial sums and start anew.  Each CTA
+// leaves its float32 partial sums in shared memory; each then adds up a share of the tokens over the g CTAs, in CTA
+// order, through distributed shared memory, and writes the planes: no partial planes in HBM, no further launch, and the
+// same bits every time.  g, a divisor of the cluster, follows on the device from the number of tiles.
 //   warp 0  loads V; warp 2 W (one thread that loaded both bounded the kernel: 480 cycles a step); warp 1  products;
 //   warps 2..9  accumulators -> shared memory; all  the sums
 // A launch has one or two sums to do (a backward whose T was not kept does U and T, which saves a launch that would wait
@@ -1103,9 +1103,9 @@ __global__ void __launch_bounds__(kPoolThreads, 2) pool_up_kernel(const __grid_c
 //   warp 0  loads; warp 1  products; warps 2..9  accumulators -> dA or dB
 // ---------------------------------------------------------------------------
 constexpr uint32_t kPoolGradTmem = 256;
-// Steps of 64 tokens until the accumulators start anew: chains of 64 additions.  One adapter, float32, error of dB: 8192
-// tokens 3.7e-6 -> 1.8e-6, 65536 2.6e-5 -> 1.9e-6; 16384 tokens of 11008 x 4096 take 418 us instead of 414.
-constexpr int kPoolGradFold = 48;
+// Steps of 64 tokens until the accumulators start anew: chains of 60 additions.  One adapter, float32, error of dB: 8192
+// tokens 3.7e-6 -> 1.8e-6, 65536 2.6e-5 -> 1.8e-6; 16384 tokens of 11008 x 4096 take 420 us instead of 414.
+constexpr int kPoolGradFold = 45;
 
 struct PoolGradArgs {
   PoolArgs p;
