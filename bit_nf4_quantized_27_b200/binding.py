@@ -486,7 +486,9 @@ def workspace_bytes_adapters(m: int, n: int, k: int, r: int, backward: bool) -> 
 
 @_on_its_stream
 def adapter_groups(adapter_of_token: torch.Tensor, n: int, out=None, ws: torch.Tensor | None = None, stream=None):
-    """(order [M], offsets [n + 1]) int32: the tokens grouped by adapter (-1: none, last)."""
+    """(order [M], offsets [n + 1]) int32: the tokens grouped by adapter (-1: none, last).  Here and in the
+    calls that take the groups, what the kernels find wrong (an index, a place or a rank out of range) stands in
+    ws's status word, for read_status; a call without ws does not tell of it."""
     idx = adapter_of_token
     assert idx.dtype == torch.int32 and idx.is_contiguous() and idx.dim() == 1
     M = idx.numel()
